@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libnq.so")
 NQ_OK, NQ_ERR_ARG, NQ_ERR_UNSUPPORTED, NQ_ERR_SIZE, NQ_ERR_CUDA = range(5)
 NQ_HIST_BINS = 274
 FORMAT_VERSION = 1
+NQ_F16, NQ_BF16 = range(2)
 
 
 class Shape(ctypes.Structure):
@@ -40,6 +41,20 @@ class Layout(ctypes.Structure):
 # name -> (restype, argtypes); the exported C ABI, in header order
 class LayerBits(ctypes.Structure):
     _fields_ = [("key_bits", ctypes.c_int32), ("value_bits", ctypes.c_int32)]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("requests", ctypes.c_int32),
+                ("table_cols", ctypes.c_int32), ("max_q", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("table_stride", ctypes.c_int64),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
 
 
 _LB = ctypes.POINTER(LayerBits)
@@ -76,6 +91,18 @@ SIGNATURES = {
                                          ctypes.POINTER(Params), ctypes.c_void_p, ctypes.c_void_p]),
     "nq_e8_nearest": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_void_p]),
+    "nq_page_map": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                   ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                   ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "nq_paged_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.POINTER(Pool), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "nq_paged_attention_workspace": (ctypes.c_int, [ctypes.POINTER(Attention), ctypes.POINTER(Pool), _U64P]),
+    "nq_paged_attention": (ctypes.c_int, [ctypes.POINTER(Attention), ctypes.c_void_p, ctypes.POINTER(Pool),
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p]),
     "nq_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

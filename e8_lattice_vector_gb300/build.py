@@ -11,12 +11,19 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+CSRC_PAGED = os.path.join(HERE, "csrc_paged")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libnq.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["nq_api.cu", "nq_compress.cu", "nq_compress_delta.cu", "nq_decompress.cu", "nq_decompress_delta.cu", "nq_roundtrip.cu", "nq_stats.cu", "nq_layers.cu", "nq_noalloc.cu"]
-HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
+# the paged-cache operators, in a folder of their own: the codec's traffic record names a hash of csrc
+PAGED_SOURCES = ["nq_page_map.cu", "nq_paged_append.cu", "nq_paged_attention.cu"]
+
+
+def _headers(folder):
+    return [os.path.join(folder, f) for f in sorted(os.listdir(folder)) if f.endswith((".cuh", ".h"))]
+
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -40,11 +47,11 @@ def _stale(target, deps):
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     nvcc = _nvcc()
-    common_deps = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "nq.h"), __file__]
+    common_deps = _headers(CSRC) + _headers(CSRC_PAGED) + [os.path.join(INCLUDE, "nq.h"), __file__]
+    sources = [os.path.join(CSRC, f) for f in SOURCES] + [os.path.join(CSRC_PAGED, f) for f in PAGED_SOURCES]
     objs, jobs = [], []
-    for src in SOURCES:
-        s = os.path.join(CSRC, src)
-        o = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
+    for s in sources:
+        o = os.path.join(OUT_DIR, os.path.basename(s).replace(".cu", ".o"))
         objs.append(o)
         if force or _stale(o, [s] + common_deps):
             cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + ["-c", s, "-o", o]

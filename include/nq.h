@@ -274,6 +274,112 @@ int nq_code_histogram(const void* in, size_t in_bytes, const nq_shape* shape, co
  * box-constrained codebook of a b-bit code.  Test and inspection entry. */
 int nq_e8_nearest(const float* u, float* out, int64_t n_blocks, int strict, int bits, void* stream);
 
+/* ---------------------------------------------------------------- paged cache
+ *
+ * Serving from the restored cache: K and V kept in pages of page_size tokens,
+ * the step's new tokens written into them, and their attention over
+ * everything cached.  One step is nq_page_map once, then per layer
+ * nq_paged_append and nq_paged_attention.  Lengths, tables and slots are
+ * device data that the host never reads, so a step can be captured once as a
+ * CUDA graph and replayed while they change.
+ *
+ * Values found in device data are clamped before they are used as addresses
+ * (each call says how): no table, length or slot makes a call read or write
+ * outside the buffers that its host arguments describe. */
+
+enum { NQ_F16 = 0, NQ_BF16 = 1 };
+
+/* A page pool, the same for K and for V (two buffers of one layout): element
+ * (page, head, slot, d) sits at page * page_stride + head * head_stride +
+ * slot * slot_stride + d elements.  [pages][kv_heads][page_size][head_dim]
+ * (the layout of the cache above with a page for a batch entry) and
+ * [pages][page_size][kv_heads][head_dim] are both such layouts, and so are
+ * slices of a larger pool.
+ *  dtype: NQ_F16 or NQ_BF16.  head_dim: 64, 96 or 128.  page_size: 16, 32, 64,
+ *  128 or 256.  pages >= 1, kv_heads >= 1.  Strides: multiples of 8 elements,
+ *  >= head_dim and < 2^39 (the stride of an extent of one is not looked at).
+ *  Buffers are 16-byte aligned. */
+typedef struct {
+    int32_t dtype, pages, kv_heads, page_size, head_dim, reserved;
+    int64_t page_stride, head_stride, slot_stride;
+} nq_pool;
+
+/* Block table and slot map of one step, from the requests' lengths.
+ * Request r has c = ctx_lens[r] tokens cached and brings n = new_lens[r] (both
+ * device int32[requests]; negative counts as 0).  Its token i gets position
+ * c + i.  Its table row holds pages already for the first ceil(c / page_size)
+ * columns; the columns that the new tokens begin take the next pages of
+ * free_pages (device int32[n_free]), requests in order, columns in order.
+ *   block_table  device int32 [requests][table_cols], rows table_stride apart:
+ *                new columns are written (-1 when the free list has run out),
+ *                others stay
+ *   q_start      device int32[requests + 1]: exclusive sums of n (the row of
+ *                each request's first new token), the total last
+ *   kv_lens      device int32[requests]: c + n
+ *   slots        device int64[tokens]: page * page_size + offset of each new
+ *                token; -1 for a token without a page (free list or table
+ *                columns exhausted) and for the rows past the last token
+ *   positions    device int32[tokens]: c + i; -1 for the rows past the last token
+ *   counts       device int32[4]: total of n; pages asked for; pages that
+ *                the free list lacked; requests longer than their table row
+ * `tokens` is the step's room: tokens past it get no row and no page
+ * (counts[0] > tokens tells).  Sums past 2^31 - 1 are stored as 2^31 - 1.
+ * The free list is not changed: the caller drops its first counts[1] entries.
+ * Entries of the table and of the free list are copied, not checked. */
+int nq_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int32_t requests, const int32_t* free_pages,
+                int32_t n_free, int32_t* block_table, int64_t table_stride, int32_t table_cols, int32_t page_size,
+                int32_t tokens, int32_t* q_start, int32_t* kv_lens, int64_t* slots, int32_t* positions,
+                int32_t* counts, void* stream);
+
+/* Write the step's K and V rows into the pools.  Row (t, h) of k sits at
+ * t * k_token_stride + h * k_head_stride elements (v likewise; strides
+ * multiples of 8, so the codec's head-major output goes in as it is) and goes to slot
+ * slots[t] (device int64[tokens]) of its head; a slot outside [0, pages *
+ * page_size) writes nothing.  Two rows with the same slot leave one of the two
+ * values in each element.  The source must not overlap the pools. */
+int nq_paged_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                    int64_t v_token_stride, int64_t v_head_stride, int32_t tokens, const int64_t* slots,
+                    const nq_pool* pool, void* k_pages, void* v_pages, void* stream);
+
+/* Attention of the step's new tokens over the paged cache.
+ *  tokens: rows of q and out; q_heads: a multiple of kv_heads (query head j
+ *  reads KV head j / (q_heads / kv_heads)); requests, table_cols, table_stride: the
+ *  table.  max_q: a bound on a request's new tokens, for choosing the kernel
+ *  (results do not depend on it).  causal: 0 or 1.  window: 0 = none, else the
+ *  number of most recent keys a token sees, its own included.  scale > 0, finite.
+ *  q / out element (t, head, d): t * token_stride + head * head_stride + d, strides
+ *  multiples of 8 elements. */
+typedef struct {
+    int32_t tokens, q_heads, requests, table_cols, max_q, causal, window;
+    float scale;
+    int64_t table_stride, q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+} nq_attention;
+
+/* With c = kv_lens[r] and the request's rows q_start[r] .. q_start[r + 1], row i
+ * of n has position p = c - n + i and sees key j < c when its table entry
+ * is a page of the pool, j <= p (causal) and j > p - window (window > 0):
+ *   s_j = scale * q . k_j,  m = max s_j,  l = sum exp(s_j - m),
+ *   out = sum exp(s_j - m) v_j / l,  lse = m + ln(l)
+ * Scores, maxima, sums and accumulators are 32-bit; exp(s - m) is rounded to
+ * the pool's type for its product with v, and out once at the end.  A row that
+ * sees no key gets out = 0 and lse = -infinity.
+ *   q, out   device, the pool's type; must not overlap
+ *   lse      device float [tokens][q_heads], or NULL
+ *   workspace  device scratch of nq_paged_attention_workspace() bytes, 16-byte
+ *              aligned; nothing in it has to start at zero and nothing is kept in it
+ * Rows of no request are left as they are.  q_start is clamped to [0,
+ * tokens], kv_lens to [0, table_cols * page_size]; a table entry outside [0,
+ * pages) hides its keys.  q_start must not decrease (a request whose end is
+ * before its start has no rows; rows of two requests hold one of the results).
+ * Keys and values that some row of the request sees must be finite; what no
+ * row of it may see (slots past its length, pages outside its table) may hold anything.
+ * The result does not depend on the run: no atomics, partial sums are added in a fixed order. */
+int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uint64_t* bytes);
+int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool, const void* k_pages,
+                       const void* v_pages, const int32_t* block_table, const int32_t* q_start,
+                       const int32_t* kv_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 /* Static description of a status code. */
 const char* nq_strerror(int status);
 
