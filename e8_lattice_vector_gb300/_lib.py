@@ -103,6 +103,7 @@ SIGNATURES = {
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                           ctypes.c_size_t, ctypes.c_void_p]),
+    "nq_paged_status": (ctypes.c_int, [ctypes.c_void_p]),
     "nq_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }
 

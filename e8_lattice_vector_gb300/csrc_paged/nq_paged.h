@@ -1,6 +1,7 @@
 // nq_paged.h -- declarations shared by the paged-cache translation units.
 #pragma once
 
+#include <cuda.h>  // CUtensorMap (type only; the encoder is fetched at run time)
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -59,5 +60,52 @@ struct AttnArgs {
     float scale;
     cudaStream_t stream;
 };
+
+// Both kernels run one block per multiprocessor of a GB300, each with an equal share of the step's (row tile, key
+// tile) pairs, in the order request, row tile, KV head, key tile.  A row tile whose keys end up in several
+// blocks leaves partial results in the workspace: per block two slots (0: its first piece, which an earlier
+// block began; 1: its last, which a later block ends), joined by a second launch.
+constexpr int kAttnGrid = 152;
+
+struct AttnSplit {  // per block: the row tile that it began and did not end, or last_block = -1
+    int request, row_tile, head, last_block;
+};
+
+struct AttnWorkspace {
+    AttnSplit* split;  // [kAttnGrid]
+    float2* ml;        // [kAttnGrid * 2][rows]: running maximum (unscaled score), sum
+    float* o;          // [kAttnGrid * 2][rows][head_dim]
+    uint64_t total;
+};
+
+inline AttnWorkspace attn_workspace(void* base, int rows, int head_dim) {
+    char* p = static_cast<char*>(base);
+    AttnWorkspace w;
+    uint64_t off = 0;
+    w.split = reinterpret_cast<AttnSplit*>(p);
+    off += (kAttnGrid * sizeof(AttnSplit) + 255) / 256 * 256;
+    w.ml = reinterpret_cast<float2*>(p + off);
+    off += (uint64_t(kAttnGrid) * 2 * rows * sizeof(float2) + 255) / 256 * 256;
+    w.o = reinterpret_cast<float*>(p + off);
+    off += uint64_t(kAttnGrid) * 2 * rows * head_dim * sizeof(float);
+    w.total = off;
+    return w;
+}
+
+// Rows of q (times the heads that share a KV head) per tile of the small kernel.
+constexpr int kSmallRows = 16;
+
+// TMA maps of the two pools: boxes of 64 columns x min(page_size, 128) slots, 128-byte swizzle.  false on failure.
+bool make_pool_maps(const AttnArgs& a, CUtensorMap* k, CUtensorMap* v);
+
+int launch_attention_small(const AttnArgs& a);
+// Joins the pieces of split row tiles of `rows` rows (launched after either kernel, as its dependent).
+int launch_attention_join(const AttnArgs& a, int rows);
+
+// Whether a kernel gave up a wait since the last call.
+int small_gave_up(int* seen);
+
+// Allow `kernel` `smem` bytes of dynamic shared memory on the current device (once per device); false on a CUDA error.
+bool ensure_smem(const void* kernel, int smem);
 
 }  // namespace nq

@@ -1,94 +1,84 @@
-// nq_paged_attention.cu -- attention of a step's new tokens over the paged cache.
-//
-// One warp for each (row, query head): it walks the visible keys one by one with a
-// running maximum and sum, each lane holding head_dim / 32 elements.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+// nq_paged_attention.cu -- attention of a step's new tokens over the paged cache: argument checks, the choice of
+// the kernel, and the second launch that joins row tiles whose keys were read by several blocks.
+#include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
 
-#include "nq_paged.h"
+#include "nq_paged_device.cuh"
 
 namespace nq {
 namespace {
 
-constexpr int kRowThreads = 128;
+constexpr int kJoinWarps = 8;
 
+// Block (b, y): the row tile that block b of the attention kernel began and did not end, its rows y, y + gridDim.y, ...
+// Every warp finds the pieces' common maximum, takes every eighth piece, and the eight sums meet in shared
+// memory, in an order that depends on the lengths alone.
 template <bool BF16>
-__device__ __forceinline__ float2 to_float2(uint32_t w) {
-    if constexpr (BF16)
-        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-    else
-        return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t from_float2(float x, float y) {
-    if constexpr (BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-        const __half2 h = __floats2half2_rn(x, y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-}
-
-template <bool BF16>
-__global__ void __launch_bounds__(kRowThreads) attention_rows_kernel(const AttnArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
-    if (item >= int64_t(a.tokens) * a.q_heads) return;
-    const int t = int(item / a.q_heads), head = int(item - int64_t(t) * a.q_heads), kvh = head / a.group;
-    int r = 0;
-    for (; r < a.requests; ++r)
-        if (a.q_start[r] <= t && t < a.q_start[r + 1]) break;
-    if (r == a.requests) return;  // a row of no request
-    const int begin = max(a.q_start[r], 0), end = min(a.q_start[r + 1], a.tokens);
-    const int64_t room = int64_t(a.table_cols) << a.page_shift;
-    const int kv = int(min(int64_t(max(a.kv_lens[r], 0)), room));
-    const int p = kv - (end - begin) + (t - begin);
-    const int hi = a.causal ? min(kv, p + 1) : kv;
-    const int lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
-    const int pairs = a.head_dim / 2;  // pair lane, lane + 32 of each row
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + t * a.q_token_stride +
-                                                          head * a.q_head_stride);
-    float2 qv[2], o[2];
-    for (int e = 0; e < 2; ++e) {
-        o[e] = make_float2(0.0f, 0.0f);
-        qv[e] = lane + 32 * e < pairs ? to_float2<BF16>(q[lane + 32 * e]) : make_float2(0.0f, 0.0f);
-    }
-    float m = -INFINITY, l = 0.0f;
-    for (int j = lo; j < hi; ++j) {
-        const int page = a.table[r * a.table_stride + (j >> a.page_shift)];
-        if (page < 0 || page >= a.pages) continue;
-        const int64_t at = page * a.page_stride + kvh * a.head_stride + (j & ((1 << a.page_shift) - 1)) * a.slot_stride;
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.k_pages) + at);
-        const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.v_pages) + at);
-        float s = 0.0f;
-        for (int e = 0; e < 2; ++e)
-            if (lane + 32 * e < pairs) {
-                const float2 kk = to_float2<BF16>(k[lane + 32 * e]);
-                s = fmaf(qv[e].x, kk.x, fmaf(qv[e].y, kk.y, s));
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    attention_join_kernel(const AttnArgs a, const AttnWorkspace ws, int rows) {
+    __shared__ float4 part[kJoinWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+    pdl_wait();
+    const AttnSplit s = ws.split[b];
+    if (s.last_block < 0) return;
+    const Request q = load_request(a, s.request);
+    const int64_t row0 = int64_t(s.row_tile) * rows;
+    const int n_rows = int(min(int64_t(q.n) * a.group - row0, int64_t(rows)));
+    const int pieces = s.last_block - b + 1;
+    const float sc = a.scale * kLog2e;
+    const int D = a.head_dim;
+    for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
+        auto at = [&](int i) { return int64_t(i == 0 ? 2 * b + 1 : 2 * (b + i)) * rows + row; };
+        float top = -INFINITY, sum = 0.0f;
+        for (int i = lane; i < pieces; i += 32) top = fmaxf(top, ws.ml[at(i)].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        for (int i = lane; i < pieces; i += 32) {
+            const float2 ml = ws.ml[at(i)];
+            if (ml.x != -INFINITY) sum += ml.y * exp2_fast((ml.x - top) * sc);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (4 * lane < D) {
+#pragma unroll 4
+            for (int i = warp; i < pieces; i += kJoinWarps) {
+                const float m = ws.ml[at(i)].x;
+                const float4 o = *reinterpret_cast<const float4*>(ws.o + at(i) * D + 4 * lane);
+                const float f = m == -INFINITY ? 0.0f : exp2_fast((m - top) * sc);
+                acc.x = fmaf(o.x, f, acc.x);
+                acc.y = fmaf(o.y, f, acc.y);
+                acc.z = fmaf(o.z, f, acc.z);
+                acc.w = fmaf(o.w, f, acc.w);
             }
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale;
-        const float mn = fmaxf(m, s), keep = expf(m - mn), w = expf(s - mn);
-        l = fmaf(l, keep, w);
-        m = mn;
-        for (int e = 0; e < 2; ++e)
-            if (lane + 32 * e < pairs) {
-                const float2 vv = to_float2<BF16>(v[lane + 32 * e]);
-                o[e].x = fmaf(o[e].x, keep, w * vv.x);
-                o[e].y = fmaf(o[e].y, keep, w * vv.y);
+        }
+        part[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0 && 4 * lane < D) {
+            for (int v = 1; v < kJoinWarps; ++v) {
+                const float4 o = part[v][lane];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
             }
+            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+            const int64_t gi = row0 + row;
+            const int t = q.begin + int(gi / a.group), h = s.head * a.group + int(gi % a.group);
+            uint2 packed;
+            packed.x = pack2<BF16>(acc.x * inv, acc.y * inv);
+            packed.y = pack2<BF16>(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_token_stride + h * a.out_head_stride +
+                                      4 * lane) = packed;
+            if (lane == 0 && a.lse != nullptr)
+                a.lse[int64_t(t) * a.q_heads + h] = sum > 0.0f ? top * a.scale + logf(sum) : -INFINITY;
+        }
+        __syncthreads();  // part is read
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + t * a.out_token_stride +
-                                                head * a.out_head_stride);
-    for (int e = 0; e < 2; ++e)
-        if (lane + 32 * e < pairs) out[lane + 32 * e] = from_float2<BF16>(o[e].x * inv, o[e].y * inv);
-    if (lane == 0 && a.lse != nullptr) a.lse[int64_t(t) * a.q_heads + head] = l > 0.0f ? m + logf(l) : -INFINITY;
 }
 
 int check_attention(const nq_attention* a, const nq_pool* pool) {
@@ -99,7 +89,8 @@ int check_attention(const nq_attention* a, const nq_pool* pool) {
     if (a->causal != 0 && a->causal != 1) return NQ_ERR_ARG;
     if (a->q_heads < 1 || a->q_heads % pool->kv_heads != 0) return NQ_ERR_ARG;
     if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return NQ_ERR_ARG;
-    if (int64_t(a->table_cols) * pool->page_size > INT_MAX) return NQ_ERR_ARG;
+    // positions and tile ends stay within 32 bits
+    if (int64_t(a->table_cols) * pool->page_size > INT_MAX - 65536) return NQ_ERR_ARG;
     if (a->requests > 1 && a->table_stride < a->table_cols) return NQ_ERR_ARG;
     if (!paged_stride_ok(a->q_token_stride, a->tokens, 0) || !paged_stride_ok(a->q_head_stride, a->q_heads, 0) ||
         !paged_stride_ok(a->out_token_stride, a->tokens, 0) || !paged_stride_ok(a->out_head_stride, a->q_heads, 0))
@@ -107,7 +98,55 @@ int check_attention(const nq_attention* a, const nq_pool* pool) {
     return NQ_OK;
 }
 
+bool make_pool_map(const AttnArgs& a, const void* base, CUtensorMap* map) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (!encode) return false;
+    const int page_size = 1 << a.page_shift;
+    const cuuint64_t dims[4] = {cuuint64_t(a.head_dim), cuuint64_t(page_size), cuuint64_t(a.kv_heads), cuuint64_t(a.pages)};
+    // the stride of a single head or page is never used, but has to be a valid one
+    const cuuint64_t strides[3] = {cuuint64_t(a.slot_stride) * 2,
+                                   cuuint64_t(a.kv_heads > 1 ? a.head_stride : a.slot_stride) * 2,
+                                   cuuint64_t(a.pages > 1 ? a.page_stride : a.slot_stride) * 2};
+    const cuuint32_t box[4] = {64, cuuint32_t(std::min(page_size, kKeyTile)), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return encode(map, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
+
+bool make_pool_maps(const AttnArgs& a, CUtensorMap* k, CUtensorMap* v) {
+    return make_pool_map(a, a.k_pages, k) && make_pool_map(a, a.v_pages, v);
+}
+
+int launch_attention_join(const AttnArgs& a, int rows) {
+    const AttnWorkspace ws = attn_workspace(a.workspace, rows, a.head_dim);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    // a block per row, up to 16
+    cfg.gridDim = dim3(kAttnGrid, unsigned(std::min<int64_t>(std::max<int64_t>(int64_t(a.tokens) * a.group, 1), 16)));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = a.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true>, a, ws, rows)
+                                 : cudaLaunchKernelEx(&cfg, attention_join_kernel<false>, a, ws, rows);
+    return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+}
+
 }  // namespace nq
 
 extern "C" {
@@ -116,7 +155,14 @@ int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uin
     const int st = nq::check_attention(a, pool);
     if (st != NQ_OK) return st;
     if (!bytes) return NQ_ERR_ARG;
-    *bytes = 0;
+    *bytes = nq::attn_workspace(nullptr, nq::kSmallRows, pool->head_dim).total;
+    return NQ_OK;
+}
+
+int nq_paged_status(void* stream) {
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return NQ_ERR_CUDA;
+    int seen = 0;
+    if (nq::small_gave_up(&seen) != NQ_OK || seen) return NQ_ERR_CUDA;
     return NQ_OK;
 }
 
@@ -169,14 +215,7 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
     x.bf16 = pool->dtype == NQ_BF16;
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
-    const int64_t items = int64_t(x.tokens) * x.q_heads;
-    const int64_t blocks = (items * 32 + nq::kRowThreads - 1) / nq::kRowThreads;
-    if (blocks > INT_MAX) return NQ_ERR_ARG;
-    if (x.bf16)
-        nq::attention_rows_kernel<true><<<int(blocks), nq::kRowThreads, 0, x.stream>>>(x);
-    else
-        nq::attention_rows_kernel<false><<<int(blocks), nq::kRowThreads, 0, x.stream>>>(x);
-    return cudaGetLastError() == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+    return nq::launch_attention_small(x);
 }
 
 }  // extern "C"

@@ -19,7 +19,7 @@ import torch
 from . import _lib
 from .codec import _call, _stream_handle, ctypes_ref, ctypes_void, workspace
 
-__all__ = ["PageMap", "page_map", "paged_append", "paged_attention", "paged_attention_workspace"]
+__all__ = ["PageMap", "page_map", "paged_append", "paged_attention", "paged_attention_workspace", "paged_status"]
 
 _DTYPES = {torch.float16: _lib.NQ_F16, torch.bfloat16: _lib.NQ_BF16}
 
@@ -202,3 +202,10 @@ def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=No
           None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
           0 if ws is None else ws.numel(), _stream_handle(dev))
     return out if lse is None else (out, lse)
+
+
+def paged_status(device=None):
+    """Waits for the device's current stream; raises NQError when it failed or when an attention kernel gave up
+    waiting for its loads (outputs since the last paged_status are then void)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    _call(dev, "nq_paged_status", _stream_handle(dev))

@@ -380,6 +380,11 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
                        const int32_t* kv_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/* Waits for `stream`, then returns NQ_ERR_CUDA if it failed or if an attention
+ * kernel on the current device gave up waiting for its loads since the last call of this
+ * function (its outputs are then void; waits are limited to about two seconds), else NQ_OK. */
+int nq_paged_status(void* stream);
+
 /* Static description of a status code. */
 const char* nq_strerror(int status);
 
