@@ -94,16 +94,21 @@ inline AttnWorkspace attn_workspace(void* base, int rows, int head_dim) {
 
 // Rows of q (times the heads that share a KV head) per tile of the small kernel.
 constexpr int kSmallRows = 16;
+// ... and of the large one.
+constexpr int kChunkRows = 256;
 
 // TMA maps of the two pools: boxes of 64 columns x min(page_size, 128) slots, 128-byte swizzle.  false on failure.
 bool make_pool_maps(const AttnArgs& a, CUtensorMap* k, CUtensorMap* v);
 
 int launch_attention_small(const AttnArgs& a);
+int launch_attention_chunk(const AttnArgs& a);
+uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim);
 // Joins the pieces of split row tiles of `rows` rows (launched after either kernel, as its dependent).
 int launch_attention_join(const AttnArgs& a, int rows);
 
 // Whether a kernel gave up a wait since the last call.
 int small_gave_up(int* seen);
+int chunk_gave_up(int* seen);
 
 // Allow `kernel` `smem` bytes of dynamic shared memory on the current device (once per device); false on a CUDA error.
 bool ensure_smem(const void* kernel, int smem);

@@ -98,6 +98,11 @@ int check_attention(const nq_attention* a, const nq_pool* pool) {
     return NQ_OK;
 }
 
+// Whether a request's rows for one KV head fit a tile of the small kernel.
+bool few_rows(const nq_attention* a, int group) {
+    return int64_t(std::min(a->max_q, a->tokens)) * group <= kSmallRows;
+}
+
 bool make_pool_map(const AttnArgs& a, const void* base, CUtensorMap* map) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
@@ -155,15 +160,17 @@ int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uin
     const int st = nq::check_attention(a, pool);
     if (st != NQ_OK) return st;
     if (!bytes) return NQ_ERR_ARG;
-    *bytes = nq::attn_workspace(nullptr, nq::kSmallRows, pool->head_dim).total;
+    const int group = a->q_heads / pool->kv_heads;
+    *bytes = nq::few_rows(a, group) ? nq::attn_workspace(nullptr, nq::kSmallRows, pool->head_dim).total
+                                    : nq::chunk_workspace(a->tokens, group, a->requests, pool->head_dim);
     return NQ_OK;
 }
 
 int nq_paged_status(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return NQ_ERR_CUDA;
-    int seen = 0;
-    if (nq::small_gave_up(&seen) != NQ_OK || seen) return NQ_ERR_CUDA;
-    return NQ_OK;
+    int small = 0, chunk = 0;
+    if (nq::small_gave_up(&small) != NQ_OK || nq::chunk_gave_up(&chunk) != NQ_OK) return NQ_ERR_CUDA;
+    return small || chunk ? NQ_ERR_CUDA : NQ_OK;
 }
 
 int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool, const void* k_pages,
@@ -215,7 +222,7 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
     x.bf16 = pool->dtype == NQ_BF16;
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
-    return nq::launch_attention_small(x);
+    return nq::few_rows(a, x.group) ? nq::launch_attention_small(x) : nq::launch_attention_chunk(x);
 }
 
 }  // extern "C"

@@ -1,0 +1,701 @@
+// nq_paged_chunk.cu -- attention of many rows per request over the paged cache (prompt chunks, whole prompts).
+//
+// A row tile is 256 rows (tokens times the query heads that share a KV head), two halves of 128.  For each tile of 128
+// keys and each half, on the tensor cores (tcgen05, accumulators in tensor memory):
+//   S = Q K^T                    128 x 128, fp32
+//   P = exp2((S - m) c)          by a warpgroup, a thread per row: no exchange between threads
+//   O = O f + P V                P from tensor memory, where it takes the place of S
+// m is a reference that follows the running maximum only when that has grown by more than 2^8 in P (kSlack): O is
+// rescaled on those few tiles, and on the others the tensor cores add to it undisturbed.  P stays below 2^8, and
+// its sum below 2^31 for any length.
+//
+// The two halves alternate on the tensor cores: while one half's exponentials are taken, the other half's
+// products run.  One warp loads (TMA, one box per page and 64 columns), one issues the products.
+//
+// Shares: the row tiles' key tiles, in order, in equal parts over 152 blocks; a launch of one block finds where each part
+// begins.  Row tiles that end up in several blocks are joined by a second launch.
+#include "nq_paged_device.cuh"
+
+namespace nq {
+namespace {
+
+__device__ int g_gave_up;  // set when a wait was given up
+
+constexpr int kThreadsChunk = 384;  // two warpgroups for the halves; load, product and two spare warps
+constexpr int kPlanThreads = 1024;
+constexpr float kSlack = 8.0f;  // in powers of two
+
+template <int D>
+struct Chunk {
+    static constexpr int HALVES = D > 64 ? 2 : 1;  // 64-column halves of a tile
+    static constexpr int TILE = HALVES * kHalfBytes;
+    static constexpr int Q = 2 * TILE;
+    static constexpr int STAGES = (224 * 1024 - Q) / TILE > 8 ? 8 : (224 * 1024 - Q) / TILE;
+    static constexpr int SMEM = 1024 + Q + STAGES * TILE;
+};
+constexpr int kLiveRing = 8;  // tiles whose page masks are kept; the loads are at most five tiles ahead of a half
+
+// Where a block's share begins.
+struct ChunkStart {
+    int request, row_tile, head, tile;
+    long long begin, end, total;
+};
+
+struct ChunkPlan {
+    ChunkStart* start;     // [kAttnGrid]
+    long long* tile_sum;   // [pairs + 1]: tiles of the (request, row tile) pairs before, all heads
+    int* pair_request;     // [pairs]
+    int* pair_row_tile;    // [pairs]
+};
+
+inline int64_t chunk_pairs(int64_t tokens, int group, int requests) { return tokens * group / kChunkRows + requests; }
+
+inline ChunkPlan chunk_plan(char* p, int64_t pairs, uint64_t* total) {
+    ChunkPlan c;
+    uint64_t off = 0;
+    auto take = [&](uint64_t bytes) {
+        char* at = p + off;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    c.start = reinterpret_cast<ChunkStart*>(take(kAttnGrid * sizeof(ChunkStart)));
+    c.tile_sum = reinterpret_cast<long long*>(take(uint64_t(pairs + 1) * sizeof(long long)));
+    c.pair_request = reinterpret_cast<int*>(take(uint64_t(pairs) * sizeof(int)));
+    c.pair_row_tile = reinterpret_cast<int*>(take(uint64_t(pairs) * sizeof(int)));
+    *total = off;
+    return c;
+}
+
+__device__ __forceinline__ int row_tiles_of(const AttnArgs& a, const Request& q) {
+    return int((int64_t(q.n) * a.group + kChunkRows - 1) / kChunkRows);
+}
+
+// The rows and keys of one row tile.
+struct RowTile {
+    int64_t row0;
+    int n_rows, lo, hi;  // keys [lo, hi) are seen by some row
+    int first, count;    // key tiles, at least one so that rows without keys are written too
+};
+__device__ __forceinline__ RowTile row_tile_of(const AttnArgs& a, const Request& q, int row_tile) {
+    RowTile t;
+    t.row0 = int64_t(row_tile) * kChunkRows;
+    t.n_rows = int(min(int64_t(q.n) * a.group - t.row0, int64_t(kChunkRows)));
+    const int base = q.kv - q.n;
+    t.lo = keys_from(a, base + int(t.row0 / a.group));
+    t.hi = keys_to(a, q.kv, base + int((t.row0 + t.n_rows - 1) / a.group));
+    t.first = min(t.lo, t.hi) / kKeyTile;
+    t.count = max((t.hi + kKeyTile - 1) / kKeyTile - t.first, 1);
+    return t;
+}
+
+// Block-wide inclusive sum; *total the sum over all threads.
+__device__ __forceinline__ long long plan_scan(long long x, long long* total) {
+    __shared__ long long warps[kPlanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += v;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = x;
+    __syncthreads();
+    long long t = warps[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, t, d);
+        if (lane >= d) t += v;
+    }
+    *total = __shfl_sync(0xffffffffu, t, 31);
+    const long long before = __shfl_sync(0xffffffffu, t, max(warp - 1, 0));
+    return x + (warp > 0 ? before : 0);
+}
+
+// One block: the running sum of key tiles over the (request, row tile) pairs, then the beginning of every share.  `room`:
+// pairs that the arrays hold, all there are unless row starts decrease.
+__global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const AttnArgs a, const ChunkPlan plan, long long room) {
+    __shared__ int s_pair[kPlanThreads];
+    pdl_trigger();
+    long long pairs = 0, tiles = 0;
+    for (int r0 = 0; r0 < a.requests; r0 += kPlanThreads) {
+        const int r = r0 + threadIdx.x;
+        const int n = r < a.requests ? row_tiles_of(a, load_request(a, r)) : 0;
+        long long chunk_pairs, chunk_tiles;
+        const int upto = int(plan_scan(n, &chunk_pairs));
+        __syncthreads();  // s_pair of the previous chunk is read
+        s_pair[threadIdx.x] = upto - n;
+        __syncthreads();
+        chunk_pairs = min(chunk_pairs, room - pairs);
+        for (int p0 = 0; p0 < int(chunk_pairs); p0 += kPlanThreads) {
+            const int p = p0 + threadIdx.x;
+            long long mine = 0;
+            if (p < int(chunk_pairs)) {
+                int lo = 0, hi = kPlanThreads;  // the last request whose first pair is at or before p
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_pair[mid] <= p)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                const int row_tile = p - s_pair[lo];
+                mine = (long long)row_tile_of(a, load_request(a, r0 + lo), row_tile).count * a.kv_heads;
+                plan.pair_request[pairs + p] = r0 + lo;
+                plan.pair_row_tile[pairs + p] = row_tile;
+            }
+            const long long sum = plan_scan(mine, &chunk_tiles);
+            if (p < int(chunk_pairs)) plan.tile_sum[pairs + p] = tiles + sum - mine;
+            tiles += chunk_tiles;
+        }
+        pairs += chunk_pairs;
+    }
+    if (threadIdx.x == 0) plan.tile_sum[pairs] = tiles;
+    __syncthreads();
+    for (int b = threadIdx.x; b < kAttnGrid; b += kPlanThreads)
+        if (share_begin(tiles, b) >= tiles) plan.start[b] = ChunkStart{0, 0, 0, 0, tiles, tiles, tiles};
+    for (long long p = threadIdx.x; p < pairs; p += kPlanThreads) {
+        const long long from = plan.tile_sum[p], to = plan.tile_sum[p + 1];
+        const int count = int((to - from) / a.kv_heads);
+        int b = share_holding(tiles, from);
+        if (share_begin(tiles, b) < from) ++b;
+        for (; b < kAttnGrid; ++b) {
+            const long long begin = share_begin(tiles, b);
+            if (begin >= to) break;
+            const long long at = begin - from;
+            plan.start[b] = ChunkStart{plan.pair_request[p], plan.pair_row_tile[p], int(at / count), int(at % count),
+                                       begin, share_begin(tiles, b + 1), tiles};
+        }
+    }
+}
+
+// ------------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand: 128-byte swizzle, `lead` and `stride` in 16-byte units.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t(lead) << 16 | uint64_t(stride) << 32 | uint64_t(1) << 46 |
+           uint64_t(2) << 61;
+}
+// Instruction descriptor: fp32 accumulator, both operands bf16 or fp16, 128 x N; B with N innermost when `b_n_major`.
+template <bool BF16>
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_n_major) {
+    return 1u << 4 | (BF16 ? 1u : 0u) << 7 | (BF16 ? 1u : 0u) << 10 | (b_n_major ? 1u : 0u) << 16 | uint32_t(n >> 3) << 17 |
+           uint32_t(128 >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        : "memory");
+}
+
+// 32 columns of this thread's row.
+__device__ __forceinline__ void tm_load(float* r, uint32_t addr) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+}
+// Ends the loads into r[0, N): nothing that uses them comes before the wait.
+template <int N>
+__device__ __forceinline__ void tm_wait(float* r) {
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
+}
+__device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t* u) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+        ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+          "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
+          "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
+          "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
+        : "memory");
+}
+
+// Pairs of fp32 in one operation.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// -------------------------------------------------------------------- kernel
+
+struct ChunkControl {
+    uint64_t full[8], empty[8];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint32_t live[kLiveRing];  // per key tile: which of its pages are loaded
+    uint32_t tmem;
+    int gave_up;
+};
+
+// Walks the pieces of a block's share.
+struct ChunkWalk {
+    int r, row_tile, head, tile;
+    long long left;
+    Request q;
+    int row_tiles;
+    RowTile t;
+
+    __device__ __forceinline__ void begin(const AttnArgs& a, const ChunkStart& s) {
+        r = s.request;
+        row_tile = s.row_tile;
+        head = s.head;
+        tile = s.tile;
+        left = s.end - s.begin;
+        if (left > 0) {
+            q = load_request(a, r);
+            row_tiles = row_tiles_of(a, q);
+            t = row_tile_of(a, q, row_tile);
+        }
+    }
+    __device__ __forceinline__ int take() const { return int(min((long long)(t.count - tile), left)); }
+    __device__ __forceinline__ void next(const AttnArgs& a) {
+        const int n = take();
+        left -= n;
+        tile += n;
+        if (tile < t.count) return;  // left == 0
+        tile = 0;
+        if (++head < a.kv_heads) return;
+        head = 0;
+        if (left <= 0) return;
+        if (++row_tile >= row_tiles) {
+            row_tile = 0;
+            do {
+                if (++r >= a.requests) {  // not reached while the lengths stay as they were summed
+                    left = 0;
+                    return;
+                }
+                q = load_request(a, r);
+                row_tiles = row_tiles_of(a, q);
+            } while (row_tiles == 0);
+        }
+        t = row_tile_of(a, q, row_tile);
+    }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreadsChunk, 1)
+    attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
+                           const __grid_constant__ CUtensorMap v_map, const AttnWorkspace ws, const ChunkPlan plan) {
+    using C = Chunk<D>;
+    constexpr int HALVES = C::HALVES, STAGES = C::STAGES;
+    extern __shared__ char smem_raw[];
+    __shared__ ChunkControl c;
+    char* q_smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    char* ring = q_smem + C::Q;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(smem_ptr(&c.full[i]), 1);
+            mbar_init(smem_ptr(&c.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_ptr(&c.q_full[i]), 4);
+            mbar_init(smem_ptr(&c.s_full[i]), 1);
+            mbar_init(smem_ptr(&c.p_full[i]), 4);
+            mbar_init(smem_ptr(&c.o_full[i]), 1);
+        }
+        mbar_init(smem_ptr(&c.drained), 1);
+        mbar_init_fence();
+        c.gave_up = 0;
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
+    }
+    if (warp == 9) {  // all 512 columns: one block per multiprocessor
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_ptr(&c.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&c.tmem);
+    pdl_wait();  // the plan is written
+    const ChunkStart start = plan.start[blockIdx.x];
+    ChunkWalk w;
+    w.begin(a, start);
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8) {
+            // -------------------------------------------------------- loads
+            const int ppt = max(kKeyTile >> a.page_shift, 1), rows = min(1 << a.page_shift, kKeyTile);
+            const int pg = lane % ppt, half = lane / ppt;  // a lane for each page and 64 columns
+            int n = 0, tiles = 0;
+            bool go = true;
+            while (go && w.left > 0) {
+                const int take = w.take();
+                for (int i = 0; go && i < take; ++i, ++tiles) {
+                    const int k0 = (w.t.first + w.tile + i) * kKeyTile + (pg << a.page_shift);
+                    int page = -1;
+                    if (half < HALVES && k0 < w.t.hi && k0 + rows > w.t.lo)
+                        page = a.table[w.r * a.table_stride + (k0 >> a.page_shift)];
+                    const bool load = page >= 0 && page < a.pages;
+                    const uint32_t mask = __ballot_sync(0xffffffffu, load && half == 0);
+                    for (int is_v = 0; is_v < 2; ++is_v, ++n) {
+                        const int st = n % STAGES;
+                        if (n >= STAGES)
+                            go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.empty[st]), (n / STAGES - 1) & 1, &c.gave_up));
+                        if (!go) break;
+                        const uint32_t full = smem_ptr(&c.full[st]);
+                        if (lane == 0) {
+                            if (!is_v) *(volatile uint32_t*)&c.live[tiles % kLiveRing] = mask;
+                            mbar_arrive_tx(full, uint32_t(__popc(mask)) * uint32_t(rows) * 128u * HALVES);
+                        }
+                        __syncwarp();
+                        if (load)
+                            tma_load_box(smem_ptr(ring + st * C::TILE + half * kHalfBytes + pg * rows * 128),
+                                         is_v ? &v_map : &k_map, full, half * 64, k0 & ((1 << a.page_shift) - 1), w.head, page);
+                    }
+                }
+                w.next(a);
+            }
+            // no copy is left in flight when the block ends, after a wait that was given up too
+            if (lane == 0) {
+                int late = 0;
+                for (int i = max(n - STAGES, 0); i < n; ++i)
+                    mbar_wait(smem_ptr(&c.full[i % STAGES]), (i / STAGES) & 1, &late);
+                if (late) *(volatile int*)&c.gave_up = 1;
+            }
+        } else if (warp == 9) {
+            // ----------------------------------------------------- products
+            constexpr uint32_t s_idesc = tc_idesc<BF16>(kKeyTile, false), o_idesc = tc_idesc<BF16>(D, true);
+            const uint32_t ring0 = smem_ptr(ring), q0 = smem_ptr(q_smem);
+            int n = 0, tiles = 0;
+            uint32_t q_phase = 0, p_phase = 0;  // bit h: half h
+            bool go = true;
+            auto await = [&](uint64_t& bar, uint32_t parity) {
+                go = __all_sync(0xffffffffu, go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up));
+                tc_fence_after();
+            };
+            auto scores = [&](int h, int st) {  // S_h = Q_h K^T
+                if (lane == 0) {
+                    const uint64_t qd = tc_desc(q0 + h * C::TILE, 1, 64), kd = tc_desc(ring0 + st * C::TILE, 1, 64);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t step = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
+                        tc_mma(tmem + h * 128, qd + step, kd + step, s_idesc, k > 0);
+                    }
+                    tc_commit(smem_ptr(&c.s_full[h]));
+                }
+                __syncwarp();
+            };
+            while (go && w.left > 0) {
+                const int take = w.take(), halves = w.t.n_rows > 128 ? 2 : 1;
+                await(c.full[n % STAGES], (n / STAGES) & 1);
+                for (int h = 0; h < halves; ++h) {
+                    await(c.q_full[h], q_phase >> h & 1);
+                    q_phase ^= 1u << h;
+                    if (go) scores(h, n % STAGES);
+                }
+                if (go && lane == 0) tc_commit(smem_ptr(&c.empty[n % STAGES]));
+                ++n;
+                for (int i = 0; go && i < take; ++i, ++tiles) {
+                    const int vst = n % STAGES, kst = (n + 1) % STAGES;
+                    await(c.full[vst], (n / STAGES) & 1);
+                    ++n;
+                    const bool more = i + 1 < take;
+                    if (more) await(c.full[kst], (n / STAGES) & 1);
+                    const int key0 = (w.t.first + w.tile + i) * kKeyTile;
+                    const int ppt = max(kKeyTile >> a.page_shift, 1);
+                    const uint32_t live = *(volatile uint32_t*)&c.live[tiles % kLiveRing], all = uint32_t((1ull << ppt) - 1);
+                    if (key0 < w.t.lo || key0 + kKeyTile > w.t.hi || live != all) {
+                        // values that no row sees may be anything, and 0 * NaN is NaN: their rows are cleared
+                        for (int r0 = 0; r0 < kKeyTile; r0 += 2) {
+                            const int r = r0 + (lane >> 4), half = (lane >> 3) & 1;
+                            const bool seen = key0 + r >= w.t.lo && key0 + r < w.t.hi && (live >> (r >> a.page_shift) & 1u);
+                            if (!seen && half < HALVES)
+                                *reinterpret_cast<uint4*>(ring + vst * C::TILE + half * kHalfBytes + r * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        proxy_fence();
+                        __syncwarp();
+                    }
+                    for (int h = 0; h < halves; ++h) {
+                        await(c.p_full[h], p_phase >> h & 1);
+                        p_phase ^= 1u << h;
+                        if (!go) break;
+                        if (lane == 0) {  // O_h += P_h V
+                            const uint64_t vd = tc_desc(ring0 + vst * C::TILE, kHalfBytes >> 4, 64);
+                            const uint32_t o = tmem + 256 + h * 128, p = tmem + h * 128;
+#pragma unroll
+                            for (int k = 0; k < kKeyTile / 16; ++k) {
+                                tc_mma_ta(o, p + 8 * k, vd + 128 * k, o_idesc, i > 0 || k > 0);
+                                if constexpr (BF16) tc_mma_ta(o, p + 64 + 8 * k, vd + 128 * k, o_idesc, true);
+                            }
+                            tc_commit(smem_ptr(&c.o_full[h]));
+                        }
+                        __syncwarp();
+                        if (more) scores(h, kst);
+                    }
+                    if (go && lane == 0) {
+                        tc_commit(smem_ptr(&c.empty[vst]));
+                        if (more) tc_commit(smem_ptr(&c.empty[kst]));
+                    }
+                    if (more) ++n;
+                }
+                w.next(a);
+            }
+            // no product is in flight when tensor memory is freed
+            if (lane == 0) {
+                int late = 0;
+                tc_commit(smem_ptr(&c.drained));
+                mbar_wait(smem_ptr(&c.drained), 0, &late);
+                if (late) *(volatile int*)&c.gave_up = 1;
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------- softmax of one half
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int h = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+        const uint32_t s_at = tmem + h * 128 + lanes, o_at = tmem + 256 + h * 128 + lanes;
+        const float sc = a.scale * kLog2e;
+        auto wait = [&](uint64_t& bar, uint32_t parity) {
+            mbar_wait(smem_ptr(&bar), parity, &c.gave_up);
+            __syncwarp();
+            tc_fence_after();
+        };
+        int n_s = 0;      // tiles of this half so far
+        int tiles = 0;    // tiles of the block so far
+        bool first = true;
+        if (threadIdx.x == 0) ws.split[blockIdx.x].last_block = -1;
+        for (; w.left > 0; first = false, w.next(a)) {
+            const int take = w.take();
+            const bool whole = w.tile == 0 && take == w.t.count;
+            if (threadIdx.x == 0 && w.tile == 0 && !whole)
+                ws.split[blockIdx.x] = AttnSplit{w.r, w.row_tile, w.head,
+                                                 share_holding(start.total, start.end - 1 + (w.t.count - take))};
+            const int n_rows = min(w.t.n_rows - h * 128, 128);
+            if (n_rows <= 0) {  // the product warp skips this half too
+                tiles += take;
+                continue;
+            }
+            const int64_t row0 = w.t.row0 + h * 128;
+            // ------------------------------------------------ Q of this half
+            for (int i = row; i < 128 * (D / 8); i += 128) {
+                const int rr = i / (D / 8), ch = i - rr * (D / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (rr < n_rows) {
+                    const int64_t gi = row0 + rr;
+                    const int t = int(gi / a.group), hd = w.head * a.group + int(gi - int64_t(t) * a.group);
+                    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                             (w.q.begin + t) * a.q_token_stride + hd * a.q_head_stride + ch * 8));
+                }
+                *reinterpret_cast<uint4*>(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_ptr(&c.q_full[h]));
+
+            const int64_t gi = row0 + min(row, n_rows - 1);
+            const int token = int(gi / a.group), head = w.head * a.group + int(gi - int64_t(token) * a.group);
+            const int base = w.q.kv - w.q.n;
+            const int lo = keys_from(a, base + token), hi = keys_to(a, w.q.kv, base + token);
+            // keys [all_lo, all_hi) are seen by every row of the half
+            const int all_lo = keys_from(a, base + int((row0 + n_rows - 1) / a.group));
+            const int all_hi = keys_to(a, w.q.kv, base + int(row0 / a.group));
+            const int ppt = max(kKeyTile >> a.page_shift, 1);
+            const uint32_t all = uint32_t((1ull << ppt) - 1);
+            float m = -INFINITY, l = 0.0f;
+            for (int i = 0; i < take; ++i, ++n_s, ++tiles) {
+                const int key0 = (w.t.first + w.tile + i) * kKeyTile;
+                wait(c.s_full[h], n_s & 1);
+                const uint32_t live = *(volatile uint32_t*)&c.live[tiles % kLiveRing];
+                float s[kKeyTile];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tm_load(s + 32 * x, s_at + 32 * x);
+                tm_wait<kKeyTile>(s);
+                if (key0 < all_lo || key0 + kKeyTile > all_hi || live != all) {
+                    const int from = lo - key0, to = hi - key0;
+#pragma unroll
+                    for (int x = 0; x < kKeyTile; ++x)
+                        if (x < from || x >= to || !(live >> (x >> a.page_shift) & 1u)) s[x] = -INFINITY;
+                }
+                float top = s[0];
+#pragma unroll
+                for (int x = 1; x < kKeyTile; ++x) top = fmaxf(top, s[x]);
+                // the reference moves when p would pass 2^kSlack
+                const bool moves = top > m && !((top - m) * sc <= kSlack);
+                if (__any_sync(0xffffffffu, moves && m != -INFINITY)) {
+                    const float f = moves && m != -INFINITY ? exp2_fast((m - top) * sc) : 1.0f;
+                    // the previous product has added to O
+                    wait(c.o_full[h], (n_s - 1) & 1);
+                    l *= f;
+#pragma unroll
+                    for (int x = 0; x < D; x += 32) {
+                        float o[32];
+                        tm_load(o, o_at + x);
+                        tm_wait<32>(o);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] *= f;
+                        tm_store(o_at + x, reinterpret_cast<const uint32_t*>(o));
+                    }
+                    tc_wait_st();
+                }
+                if (moves) m = top;  // O and l are zero as long as m is -infinity
+                const float ref = m == -INFINITY ? 0.0f : m;
+                const float2 neg = make_float2(-ref, -ref), cc = make_float2(sc, sc);
+                float2 sum = make_float2(0.0f, 0.0f);
+                uint32_t p[kKeyTile / 2];
+                uint32_t p_low[BF16 ? kKeyTile / 2 : 1];
+#pragma unroll
+                for (int x = 0; x < kKeyTile / 2; ++x) {
+                    // subtracted before it is scaled: exact for the largest scores too
+                    float2 e = mul2(add2(make_float2(s[2 * x], s[2 * x + 1]), neg), cc);
+                    e.x = exp2_fast(e.x);
+                    e.y = exp2_fast(e.y);
+                    sum = add2(sum, e);
+                    p[x] = pack2<BF16>(e.x, e.y);
+                    if constexpr (BF16) p_low[x] = pack2<true>(e.x - bf16_low(p[x]), e.y - bf16_high(p[x]));
+                }
+                tm_store(s_at, p);
+                tm_store(s_at + 32, p + 32);
+                if constexpr (BF16) {
+                    tm_store(s_at + 64, p_low);
+                    tm_store(s_at + 96, p_low + 32);
+                }
+                l += sum.x + sum.y;
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_ptr(&c.p_full[h]));
+            }
+
+            // ------------------------------------------------------- results
+            wait(c.o_full[h], (n_s - 1) & 1);
+            const bool mine = row < n_rows;
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int64_t at = int64_t(2 * blockIdx.x + (first && w.tile > 0 ? 0 : 1)) * kChunkRows + h * 128 + row;
+            uint16_t* out = static_cast<uint16_t*>(a.out) + (w.q.begin + token) * a.out_token_stride + head * a.out_head_stride;
+#pragma unroll
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                tm_load(o, o_at + x);
+                tm_wait<32>(o);
+                if (mine && whole) {
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8)
+                        *reinterpret_cast<uint4*>(out + x + y) =
+                            make_uint4(pack2<BF16>(o[y] * inv, o[y + 1] * inv), pack2<BF16>(o[y + 2] * inv, o[y + 3] * inv),
+                                       pack2<BF16>(o[y + 4] * inv, o[y + 5] * inv), pack2<BF16>(o[y + 6] * inv, o[y + 7] * inv));
+                } else if (mine) {
+#pragma unroll
+                    for (int y = 0; y < 32; y += 4)
+                        *reinterpret_cast<float4*>(ws.o + at * D + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            if (mine) {
+                if (!whole)
+                    ws.ml[at] = make_float2(m, l);
+                else if (a.lse != nullptr)
+                    a.lse[int64_t(w.q.begin + token) * a.q_heads + head] = l > 0.0f ? m * a.scale + logf(l) : -INFINITY;
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *(volatile int*)&c.gave_up) atomicExch(&g_gave_up, 1);
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+template <int D, bool BF16>
+int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const AttnWorkspace& ws,
+                 const ChunkPlan& plan) {
+    if (!ensure_smem(reinterpret_cast<const void*>(attention_chunk_kernel<D, BF16>), Chunk<D>::SMEM)) return NQ_ERR_CUDA;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kAttnGrid);
+    cfg.blockDim = dim3(kThreadsChunk);
+    cfg.dynamicSmemBytes = Chunk<D>::SMEM;
+    cfg.stream = a.stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attention_chunk_kernel<D, BF16>, a, km, vm, ws, plan) == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+}
+
+template <bool BF16>
+int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const AttnWorkspace& ws,
+                 const ChunkPlan& plan) {
+    switch (a.head_dim) {
+        case 64: return launch_chunk<64, BF16>(a, km, vm, ws, plan);
+        case 96: return launch_chunk<96, BF16>(a, km, vm, ws, plan);
+        default: return launch_chunk<128, BF16>(a, km, vm, ws, plan);
+    }
+}
+
+}  // namespace
+
+uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim) {
+    uint64_t bytes = 0;
+    chunk_plan(nullptr, chunk_pairs(tokens, group, requests), &bytes);
+    return attn_workspace(nullptr, kChunkRows, head_dim).total + bytes;
+}
+
+int launch_attention_chunk(const AttnArgs& a) {
+    CUtensorMap km, vm;
+    if (!make_pool_maps(a, &km, &vm)) return NQ_ERR_CUDA;
+    const AttnWorkspace ws = attn_workspace(a.workspace, kChunkRows, a.head_dim);
+    uint64_t bytes = 0;
+    const int64_t pairs = chunk_pairs(a.tokens, a.group, a.requests);
+    const ChunkPlan plan = chunk_plan(static_cast<char*>(a.workspace) + ws.total, pairs, &bytes);
+    attention_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a, plan, pairs);
+    if (cudaGetLastError() != cudaSuccess) return NQ_ERR_CUDA;
+    const int st = a.bf16 ? launch_chunk<true>(a, km, vm, ws, plan) : launch_chunk<false>(a, km, vm, ws, plan);
+    return st == NQ_OK ? launch_attention_join(a, kChunkRows) : st;
+}
+
+int chunk_gave_up(int* seen) {
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(seen, g_gave_up, sizeof(int)) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(int)) != cudaSuccess)
+        return NQ_ERR_CUDA;
+    return NQ_OK;
+}
+
+}  // namespace nq

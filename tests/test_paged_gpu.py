@@ -581,3 +581,8 @@ def test_step_in_a_cuda_graph(nq):
         # lengths start at zero: a request's first row sees its own key alone
         first = int(m.q_start[1]) if lens[0] == 0 else 0
         assert torch.equal(out[first], V[first].repeat_interleave(2, 0))
+
+
+def test_no_wait_was_given_up(nq):
+    """After everything above: no kernel gave up a wait for its loads."""
+    nq.paged_status()
