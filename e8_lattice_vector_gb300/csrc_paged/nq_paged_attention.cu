@@ -26,8 +26,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const AttnSplit s = ws.split[b];
     if (s.last_block < 0) return;
     const Request q = load_request(a, s.request);
-    const int64_t row0 = int64_t(s.row_tile) * rows;
-    const int n_rows = int(min(int64_t(q.n) * a.group - row0, int64_t(rows)));
+    const int row0 = s.row_tile * rows, n_rows = min(q.n * a.group - row0, rows);
     const int pieces = s.last_block - b + 1;
     const float sc = a.scale * kLog2e;
     const int D = a.head_dim;
@@ -67,8 +66,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
                 acc.w += o.w;
             }
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            const int64_t gi = row0 + row;
-            const int t = q.begin + int(gi / a.group), h = s.head * a.group + int(gi % a.group);
+            const int t = q.begin + (row0 + row) / a.group, h = s.head * a.group + (row0 + row) % a.group;
             uint2 packed;
             packed.x = pack2<BF16>(acc.x * inv, acc.y * inv);
             packed.y = pack2<BF16>(acc.z * inv, acc.w * inv);
@@ -91,6 +89,7 @@ int check_attention(const nq_attention* a, const nq_pool* pool) {
     if (!(a->scale > 0.0f) || !std::isfinite(a->scale)) return NQ_ERR_ARG;
     // positions and tile ends stay within 32 bits
     if (int64_t(a->table_cols) * pool->page_size > INT_MAX - 65536) return NQ_ERR_ARG;
+    if (int64_t(a->tokens) * a->q_heads > INT_MAX - 65536) return NQ_ERR_ARG;
     if (a->requests > 1 && a->table_stride < a->table_cols) return NQ_ERR_ARG;
     if (!paged_stride_ok(a->q_token_stride, a->tokens, 0) || !paged_stride_ok(a->q_head_stride, a->q_heads, 0) ||
         !paged_stride_ok(a->out_token_stride, a->tokens, 0) || !paged_stride_ok(a->out_head_stride, a->q_heads, 0))

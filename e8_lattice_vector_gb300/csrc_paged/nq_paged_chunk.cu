@@ -67,22 +67,21 @@ inline ChunkPlan chunk_plan(char* p, int64_t pairs, uint64_t* total) {
 }
 
 __device__ __forceinline__ int row_tiles_of(const AttnArgs& a, const Request& q) {
-    return int((int64_t(q.n) * a.group + kChunkRows - 1) / kChunkRows);
+    return (q.n * a.group + kChunkRows - 1) / kChunkRows;
 }
 
 // The rows and keys of one row tile.
 struct RowTile {
-    int64_t row0;
-    int n_rows, lo, hi;  // keys [lo, hi) are seen by some row
+    int row0, n_rows, lo, hi;  // keys [lo, hi) are seen by some row
     int first, count;    // key tiles, at least one so that rows without keys are written too
 };
 __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& a, const Request& q, int row_tile) {
     RowTile t;
-    t.row0 = int64_t(row_tile) * kChunkRows;
-    t.n_rows = int(min(int64_t(q.n) * a.group - t.row0, int64_t(kChunkRows)));
+    t.row0 = row_tile * kChunkRows;
+    t.n_rows = min(q.n * a.group - t.row0, kChunkRows);
     const int base = q.kv - q.n;
-    t.lo = keys_from(a, base + int(t.row0 / a.group));
-    t.hi = keys_to(a, q.kv, base + int((t.row0 + t.n_rows - 1) / a.group));
+    t.lo = keys_from(a, base + t.row0 / a.group);
+    t.hi = keys_to(a, q.kv, base + (t.row0 + t.n_rows - 1) / a.group);
     t.first = min(t.lo, t.hi) / kKeyTile;
     t.count = max((t.hi + kKeyTile - 1) / kKeyTile - t.first, 1);
     return t;
@@ -179,6 +178,11 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// 16 bytes to shared memory, or zeros when bytes = 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // Shared-memory operand: 128-byte swizzle, `lead` and `stride` in 16-byte units.
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
     return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t(lead) << 16 | uint64_t(stride) << 32 | uint64_t(1) << 46 |
@@ -259,7 +263,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 struct ChunkControl {
     uint64_t full[8], empty[8];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t live[kLiveRing];  // per key tile: which of its pages are loaded
     uint32_t tmem;
     int gave_up;
@@ -328,7 +332,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             mbar_init(smem_ptr(&c.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_ptr(&c.q_full[i]), 4);
+            mbar_init(smem_ptr(&c.q_full[i]), 1);
+            mbar_init(smem_ptr(&c.q_free[i]), 1);
             mbar_init(smem_ptr(&c.s_full[i]), 1);
             mbar_init(smem_ptr(&c.p_full[i]), 4);
             mbar_init(smem_ptr(&c.o_full[i]), 1);
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 go = __all_sync(0xffffffffu, go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up));
                 tc_fence_after();
             };
-            auto scores = [&](int h, int st) {  // S_h = Q_h K^T
+            auto scores = [&](int h, int st, bool last) {  // S_h = Q_h K^T; the last of a row tile frees Q
                 if (lane == 0) {
                     const uint64_t qd = tc_desc(q0 + h * C::TILE, 1, 64), kd = tc_desc(ring0 + st * C::TILE, 1, 64);
 #pragma unroll
@@ -415,6 +420,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         tc_mma(tmem + h * 128, qd + step, kd + step, s_idesc, k > 0);
                     }
                     tc_commit(smem_ptr(&c.s_full[h]));
+                    if (last) tc_commit(smem_ptr(&c.q_free[h]));
                 }
                 __syncwarp();
             };
@@ -424,7 +430,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 for (int h = 0; h < halves; ++h) {
                     await(c.q_full[h], q_phase >> h & 1);
                     q_phase ^= 1u << h;
-                    if (go) scores(h, n % STAGES);
+                    if (go) scores(h, n % STAGES, take == 1);
                 }
                 if (go && lane == 0) tc_commit(smem_ptr(&c.empty[n % STAGES]));
                 ++n;
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                             tc_commit(smem_ptr(&c.o_full[h]));
                         }
                         __syncwarp();
-                        if (more) scores(h, kst);
+                        if (more) scores(h, kst, i + 2 == take);
                     }
                     if (go && lane == 0) {
                         tc_commit(smem_ptr(&c.empty[vst]));
@@ -482,6 +488,37 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (late) *(volatile int*)&c.gave_up = 1;
             }
             __syncwarp();
+        } else {
+            // ----------------------------------------- Q of half `warp - 10`
+            // As soon as the last scores of a row tile are there its Q is not read any more: the next one's loads run
+            // beside the last tile's exponentials, its product and the results.
+            const int h = warp - 10;
+            int pieces = 0;  // of this half so far
+            bool go = true;
+            while (go && w.left > 0) {
+                const int n_rows = min(w.t.n_rows - h * 128, 128), row0 = w.t.row0 + h * 128;
+                if (n_rows > 0) {
+                    if (pieces > 0)
+                        go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.q_free[h]), (pieces - 1) & 1, &c.gave_up));
+                    if (!go) break;
+                    constexpr int VECS = D / 8;                 // 16-byte pieces of a row
+#pragma unroll 4
+                    for (int i = lane; i < 128 * VECS; i += 32) {
+                        const int rr = i / VECS, ch = i - rr * VECS;
+                        const int gi = row0 + min(rr, n_rows - 1), t = gi / a.group, hd = w.head * a.group + gi - t * a.group;
+                        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (w.q.begin + t) * a.q_token_stride +
+                                              hd * a.q_head_stride + ch * 8;
+                        copy16(smem_ptr(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
+                               src, rr < n_rows ? 16 : 0);
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_ptr(&c.q_full[h]));
+                    ++pieces;
+                }
+                w.next(a);
+            }
         }
     } else {
         // ------------------------------------------- softmax of one half
@@ -510,30 +547,12 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 tiles += take;
                 continue;
             }
-            const int64_t row0 = w.t.row0 + h * 128;
-            // ------------------------------------------------ Q of this half
-            for (int i = row; i < 128 * (D / 8); i += 128) {
-                const int rr = i / (D / 8), ch = i - rr * (D / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (rr < n_rows) {
-                    const int64_t gi = row0 + rr;
-                    const int t = int(gi / a.group), hd = w.head * a.group + int(gi - int64_t(t) * a.group);
-                    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                             (w.q.begin + t) * a.q_token_stride + hd * a.q_head_stride + ch * 8));
-                }
-                *reinterpret_cast<uint4*>(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
-            }
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_ptr(&c.q_full[h]));
-
-            const int64_t gi = row0 + min(row, n_rows - 1);
-            const int token = int(gi / a.group), head = w.head * a.group + int(gi - int64_t(token) * a.group);
-            const int base = w.q.kv - w.q.n;
+            const int row0 = w.t.row0 + h * 128, base = w.q.kv - w.q.n;
+            const int gi = row0 + min(row, n_rows - 1), token = gi / a.group, head = w.head * a.group + gi - token * a.group;
             const int lo = keys_from(a, base + token), hi = keys_to(a, w.q.kv, base + token);
             // keys [all_lo, all_hi) are seen by every row of the half
-            const int all_lo = keys_from(a, base + int((row0 + n_rows - 1) / a.group));
-            const int all_hi = keys_to(a, w.q.kv, base + int(row0 / a.group));
+            const int all_lo = keys_from(a, base + (row0 + n_rows - 1) / a.group);
+            const int all_hi = keys_to(a, w.q.kv, base + row0 / a.group);
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
             float m = -INFINITY, l = 0.0f;
@@ -551,9 +570,16 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     for (int x = 0; x < kKeyTile; ++x)
                         if (x < from || x >= to || !(live >> (x >> a.page_shift) & 1u)) s[x] = -INFINITY;
                 }
-                float top = s[0];
+                float tops[8];  // eight chains: one would be all latency
 #pragma unroll
-                for (int x = 1; x < kKeyTile; ++x) top = fmaxf(top, s[x]);
+                for (int x = 0; x < 8; ++x) tops[x] = s[x];
+#pragma unroll
+                for (int x = 8; x < kKeyTile; ++x) tops[x & 7] = fmaxf(tops[x & 7], s[x]);
+#pragma unroll
+                for (int x = 4; x > 0; x >>= 1)
+#pragma unroll
+                    for (int y = 0; y < x; ++y) tops[y] = fmaxf(tops[y], tops[y + x]);
+                const float top = tops[0];
                 // the reference moves when p would pass 2^kSlack
                 const bool moves = top > m && !((top - m) * sc <= kSlack);
                 if (__any_sync(0xffffffffu, moves && m != -INFINITY)) {
@@ -575,25 +601,26 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (moves) m = top;  // O and l are zero as long as m is -infinity
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const float2 neg = make_float2(-ref, -ref), cc = make_float2(sc, sc);
-                float2 sum = make_float2(0.0f, 0.0f);
-                uint32_t p[kKeyTile / 2];
-                uint32_t p_low[BF16 ? kKeyTile / 2 : 1];
+                float2 sums[4];
 #pragma unroll
-                for (int x = 0; x < kKeyTile / 2; ++x) {
-                    // subtracted before it is scaled: exact for the largest scores too
-                    float2 e = mul2(add2(make_float2(s[2 * x], s[2 * x + 1]), neg), cc);
-                    e.x = exp2_fast(e.x);
-                    e.y = exp2_fast(e.y);
-                    sum = add2(sum, e);
-                    p[x] = pack2<BF16>(e.x, e.y);
-                    if constexpr (BF16) p_low[x] = pack2<true>(e.x - bf16_low(p[x]), e.y - bf16_high(p[x]));
+                for (int x = 0; x < 4; ++x) sums[x] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int x0 = 0; x0 < kKeyTile / 2; x0 += 32) {
+                    uint32_t p[32], p_low[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        // subtracted before it is scaled: exact for the largest scores too
+                        float2 e = mul2(add2(make_float2(s[2 * (x0 + x)], s[2 * (x0 + x) + 1]), neg), cc);
+                        e.x = exp2_fast(e.x);
+                        e.y = exp2_fast(e.y);
+                        sums[x & 3] = add2(sums[x & 3], e);
+                        p[x] = pack2<BF16>(e.x, e.y);
+                        if constexpr (BF16) p_low[x] = pack2<true>(e.x - bf16_low(p[x]), e.y - bf16_high(p[x]));
+                    }
+                    tm_store(s_at + x0, p);
+                    if constexpr (BF16) tm_store(s_at + 64 + x0, p_low);
                 }
-                tm_store(s_at, p);
-                tm_store(s_at + 32, p + 32);
-                if constexpr (BF16) {
-                    tm_store(s_at + 64, p_low);
-                    tm_store(s_at + 96, p_low + 32);
-                }
+                const float2 sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
                 l += sum.x + sum.y;
                 tc_wait_st();
                 tc_fence_before();

@@ -77,7 +77,7 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const Request& q) {
     Span s;
-    s.row_tiles = int((int64_t(q.n) * a.group + kSmallRows - 1) / kSmallRows);
+    s.row_tiles = (q.n * a.group + kSmallRows - 1) / kSmallRows;
     const int lo = min(keys_from(a, q.kv - q.n), q.kv);
     s.first = lo / kKeyTile;
     s.count = max((q.kv + kKeyTile - 1) / kKeyTile - s.first, 1);
@@ -207,9 +207,8 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
         bool go = true;
         while (go && w.left > 0) {
             const int take = w.take();
-            const int p0 = w.q.kv - w.q.n + int(int64_t(w.row_tile) * kSmallRows / a.group);
-            const int p1 = w.q.kv - w.q.n +
-                           int((min(int64_t(w.row_tile + 1) * kSmallRows, int64_t(w.q.n) * a.group) - 1) / a.group);
+            const int p0 = w.q.kv - w.q.n + w.row_tile * kSmallRows / a.group;
+            const int p1 = w.q.kv - w.q.n + (min((w.row_tile + 1) * kSmallRows, w.q.n * a.group) - 1) / a.group;
             const int lo = keys_from(a, p0), hi = keys_to(a, w.q.kv, p1);
             for (int i = 0; i < take; ++i, ++n) {
                 const int key0 = (w.s.first + w.tile + i) * kKeyTile;
@@ -254,8 +253,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
     bool first = true;
     for (; w.left > 0; first = false) {
         const int take = w.take();
-        const int64_t rows_all = int64_t(w.q.n) * a.group, row0 = int64_t(w.row_tile) * kSmallRows;
-        const int n_rows = int(min(rows_all - row0, int64_t(kSmallRows)));
+        const int row0 = w.row_tile * kSmallRows, n_rows = min(w.q.n * a.group - row0, kSmallRows);
         const int pbase = w.q.kv - w.q.n;
         // rows of the tile: positions and the fragments of q
         int pos2[2];
@@ -263,8 +261,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = rq + 8 * e;
-            const int64_t gi = row0 + min(row, n_rows - 1);
-            const int t = int(gi / a.group), h = w.head * a.group + int(gi - int64_t(t) * a.group);
+            const int gi = row0 + min(row, n_rows - 1), t = gi / a.group, h = w.head * a.group + gi - t * a.group;
             pos2[e] = pbase + t;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
                                                                     (w.q.begin + t) * a.q_token_stride +
@@ -275,7 +272,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
                 qf[k][e + 2] = __ldg(src + 8 * k + cq + 4);
             }
         }
-        const int p_min = pbase + int(row0 / a.group), p_max = pbase + int((row0 + n_rows - 1) / a.group);
+        const int p_min = pbase + row0 / a.group, p_max = pbase + (row0 + n_rows - 1) / a.group;
         const int lo = keys_from(a, p_min), hi = keys_to(a, w.q.kv, p_max);
         // keys [all_lo, all_hi) are seen by every row
         const int all_lo = keys_from(a, p_max), all_hi = keys_to(a, w.q.kv, p_min);
@@ -417,8 +414,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             sum += c.m[v][row] == -INFINITY ? 0.0f : c.l[v][row] * exp2_fast((c.m[v][row] - top) * sc);
         const bool whole = w.tile == 0 && take == w.s.count;
         const int slot = 2 * blockIdx.x + (first && w.tile > 0 ? 0 : 1);
-        const int64_t gi = row0 + row;
-        const int t = w.q.begin + int(gi / a.group), h = w.head * a.group + int(gi % a.group);
+        const int t = w.q.begin + (row0 + row) / a.group, h = w.head * a.group + (row0 + row) % a.group;
 #pragma unroll
         for (int x = 0; x < D; x += 64) {
             if (x) named_barrier<1, kConsumers>();  // the first 64 columns are read
