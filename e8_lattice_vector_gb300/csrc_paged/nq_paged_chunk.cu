@@ -24,6 +24,7 @@ __device__ int g_gave_up;  // set when a wait was given up
 constexpr int kThreadsChunk = 384;  // two warpgroups for the halves; load, product and two spare warps
 constexpr int kPlanThreads = 1024;
 constexpr float kSlack = 8.0f;  // in powers of two
+constexpr float kExactRef = 1048576.0f;  // references up to 2^20: off by 2^-5 from m sc at most
 
 template <int D>
 struct Chunk {
@@ -178,36 +179,57 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
+// A place in the ring and the parity of its use.
+template <int STAGES>
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 // 16 bytes to shared memory, or zeros when bytes = 0.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Shared-memory operand: 128-byte swizzle, `lead` and `stride` in 16-byte units.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return uint64_t((addr & 0x3ffffu) >> 4) | uint64_t(lead) << 16 | uint64_t(stride) << 32 | uint64_t(1) << 46 |
-           uint64_t(2) << 61;
-}
+// Shared-memory operands, 128-byte swizzle: the low word holds the address and the leading offset, the high word the stride
+// between groups of eight rows (1024 bytes), the version and the swizzle; both in 16-byte units.
+constexpr uint32_t kDescHigh = 64u | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t tc_desc(uint32_t addr, uint32_t lead) { return (addr & 0x3ffffu) >> 4 | lead << 16; }
 // Instruction descriptor: fp32 accumulator, both operands bf16 or fp16, 128 x N; B with N innermost when `b_n_major`.
 template <bool BF16>
 __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_n_major) {
     return 1u << 4 | (BF16 ? 1u : 0u) << 7 | (BF16 ? 1u : 0u) << 10 | (b_n_major ? 1u : 0u) << 16 | uint32_t(n >> 3) << 17 |
            uint32_t(128 >> 4) << 24;
 }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(add)), "n"(kDescHigh)
         : "memory");
 }
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(add)), "n"(kDescHigh)
         : "memory");
 }
 
@@ -230,14 +252,20 @@ __device__ __forceinline__ void tm_wait(float* r) {
 #pragma unroll
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
 }
-__device__ __forceinline__ void tm_store(uint32_t addr, const uint32_t* u) {
+// 16 columns: with 128 scores held there is no room for more at a time.
+__device__ __forceinline__ void tm_load16(float* r, uint32_t addr) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* u) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
         ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-          "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
-          "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
-          "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31]), "r"(addr)
+          "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(addr)
         : "memory");
 }
 
@@ -250,12 +278,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
-        "mov.b64 {%0, %1}, z;\n\t}"
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
         : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -263,6 +296,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 struct ChunkControl {
     uint64_t full[8], empty[8];
+    uint64_t clean[kLiveRing];  // per key tile: its V has no values that no row sees
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t live[kLiveRing];  // per key tile: which of its pages are loaded
     uint32_t tmem;
@@ -331,6 +365,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             mbar_init(smem_ptr(&c.full[i]), 1);
             mbar_init(smem_ptr(&c.empty[i]), 1);
         }
+        for (int i = 0; i < kLiveRing; ++i) mbar_init(smem_ptr(&c.clean[i]), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_ptr(&c.q_full[i]), 1);
             mbar_init(smem_ptr(&c.q_free[i]), 1);
@@ -402,18 +437,22 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
         } else if (warp == 9) {
             // ----------------------------------------------------- products
-            constexpr uint32_t s_idesc = tc_idesc<BF16>(kKeyTile, false), o_idesc = tc_idesc<BF16>(D, true);
-            const uint32_t ring0 = smem_ptr(ring), q0 = smem_ptr(q_smem);
-            int n = 0, tiles = 0;
-            uint32_t q_phase = 0, p_phase = 0;  // bit h: half h
-            bool go = true;
-            auto await = [&](uint64_t& bar, uint32_t parity) {
-                go = __all_sync(0xffffffffu, go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up));
-                tc_fence_after();
-            };
-            auto scores = [&](int h, int st, bool last) {  // S_h = Q_h K^T; the last of a row tile frees Q
-                if (lane == 0) {
-                    const uint64_t qd = tc_desc(q0 + h * C::TILE, 1, 64), kd = tc_desc(ring0 + st * C::TILE, 1, 64);
+            // One thread, so that nothing between two products waits for a warp.
+            if (elect_one()) {
+                constexpr uint32_t s_idesc = tc_idesc<BF16>(kKeyTile, false), o_idesc = tc_idesc<BF16>(D, true);
+                const uint32_t q_desc = tc_desc(smem_ptr(q_smem), 1), k_desc = tc_desc(smem_ptr(ring), 1);
+                const uint32_t v_desc = tc_desc(smem_ptr(ring), kHalfBytes >> 4);
+                Ring<STAGES> at;
+                Ring<kLiveRing> tile;
+                uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+                bool go = true;
+                auto await = [&](uint64_t& bar, uint32_t parity) {
+                    go = go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up);
+                    tc_fence_after();
+                };
+                auto scores = [&](int h, int st, bool last) {  // S_h = Q_h K^T; the last of a row tile frees Q
+                    uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + st * (C::TILE >> 4);
+                    asm volatile("" : "+r"(qd), "+r"(kd));  // the steps are added here, not kept in registers
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t step = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
@@ -421,46 +460,30 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     }
                     tc_commit(smem_ptr(&c.s_full[h]));
                     if (last) tc_commit(smem_ptr(&c.q_free[h]));
-                }
-                __syncwarp();
-            };
-            while (go && w.left > 0) {
-                const int take = w.take(), halves = w.t.n_rows > 128 ? 2 : 1;
-                await(c.full[n % STAGES], (n / STAGES) & 1);
-                for (int h = 0; h < halves; ++h) {
-                    await(c.q_full[h], q_phase >> h & 1);
-                    q_phase ^= 1u << h;
-                    if (go) scores(h, n % STAGES, take == 1);
-                }
-                if (go && lane == 0) tc_commit(smem_ptr(&c.empty[n % STAGES]));
-                ++n;
-                for (int i = 0; go && i < take; ++i, ++tiles) {
-                    const int vst = n % STAGES, kst = (n + 1) % STAGES;
-                    await(c.full[vst], (n / STAGES) & 1);
-                    ++n;
-                    const bool more = i + 1 < take;
-                    if (more) await(c.full[kst], (n / STAGES) & 1);
-                    const int key0 = (w.t.first + w.tile + i) * kKeyTile;
-                    const int ppt = max(kKeyTile >> a.page_shift, 1);
-                    const uint32_t live = *(volatile uint32_t*)&c.live[tiles % kLiveRing], all = uint32_t((1ull << ppt) - 1);
-                    if (key0 < w.t.lo || key0 + kKeyTile > w.t.hi || live != all) {
-                        // values that no row sees may be anything, and 0 * NaN is NaN: their rows are cleared
-                        for (int r0 = 0; r0 < kKeyTile; r0 += 2) {
-                            const int r = r0 + (lane >> 4), half = (lane >> 3) & 1;
-                            const bool seen = key0 + r >= w.t.lo && key0 + r < w.t.hi && (live >> (r >> a.page_shift) & 1u);
-                            if (!seen && half < HALVES)
-                                *reinterpret_cast<uint4*>(ring + vst * C::TILE + half * kHalfBytes + r * 128 + (lane & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                        proxy_fence();
-                        __syncwarp();
-                    }
+                };
+                while (go && w.left > 0) {
+                    const int take = w.take(), halves = w.t.n_rows > 128 ? 2 : 1;
+                    await(c.full[at.stage], at.phase);
                     for (int h = 0; h < halves; ++h) {
-                        await(c.p_full[h], p_phase >> h & 1);
-                        p_phase ^= 1u << h;
-                        if (!go) break;
-                        if (lane == 0) {  // O_h += P_h V
-                            const uint64_t vd = tc_desc(ring0 + vst * C::TILE, kHalfBytes >> 4, 64);
+                        await(c.q_full[h], q_phase[h]);
+                        q_phase[h] ^= 1;
+                        if (go) scores(h, at.stage, take == 1);
+                    }
+                    if (go) tc_commit(smem_ptr(&c.empty[at.stage]));
+                    at.step();
+                    for (int i = 0; go && i < take; ++i, tile.step()) {
+                        const Ring<STAGES> v = at;
+                        at.step();
+                        const bool more = i + 1 < take;
+                        await(c.clean[tile.stage], tile.phase);
+                        if (more) await(c.full[at.stage], at.phase);
+                        for (int h = 0; h < halves; ++h) {
+                            await(c.p_full[h], p_phase[h]);
+                            p_phase[h] ^= 1;
+                            if (!go) break;
+                            // O_h += P_h V
+                            uint32_t vd = v_desc + v.stage * (C::TILE >> 4);
+                            asm volatile("" : "+r"(vd));
                             const uint32_t o = tmem + 256 + h * 128, p = tmem + h * 128;
 #pragma unroll
                             for (int k = 0; k < kKeyTile / 16; ++k) {
@@ -468,56 +491,87 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                                 if constexpr (BF16) tc_mma_ta(o, p + 64 + 8 * k, vd + 128 * k, o_idesc, true);
                             }
                             tc_commit(smem_ptr(&c.o_full[h]));
+                            if (more) scores(h, at.stage, i + 2 == take);
                         }
-                        __syncwarp();
-                        if (more) scores(h, kst, i + 2 == take);
+                        if (go) tc_commit(smem_ptr(&c.empty[v.stage]));
+                        if (more) {
+                            if (go) tc_commit(smem_ptr(&c.empty[at.stage]));
+                            at.step();
+                        }
                     }
-                    if (go && lane == 0) {
-                        tc_commit(smem_ptr(&c.empty[vst]));
-                        if (more) tc_commit(smem_ptr(&c.empty[kst]));
-                    }
-                    if (more) ++n;
+                    w.next(a);
                 }
-                w.next(a);
-            }
-            // no product is in flight when tensor memory is freed
-            if (lane == 0) {
+                // no product is in flight when tensor memory is freed
                 int late = 0;
                 tc_commit(smem_ptr(&c.drained));
                 mbar_wait(smem_ptr(&c.drained), 0, &late);
                 if (late) *(volatile int*)&c.gave_up = 1;
             }
             __syncwarp();
-        } else {
-            // ----------------------------------------- Q of half `warp - 10`
+        } else if (warp == 10) {
+            // ------------------------------------------------------------ Q
             // As soon as the last scores of a row tile are there its Q is not read any more: the next one's loads run
             // beside the last tile's exponentials, its product and the results.
-            const int h = warp - 10;
-            int pieces = 0;  // of this half so far
+            uint32_t pieces[2] = {0, 0};
             bool go = true;
-            while (go && w.left > 0) {
-                const int n_rows = min(w.t.n_rows - h * 128, 128), row0 = w.t.row0 + h * 128;
-                if (n_rows > 0) {
-                    if (pieces > 0)
-                        go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.q_free[h]), (pieces - 1) & 1, &c.gave_up));
+            for (; go && w.left > 0; w.next(a)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int n_rows = min(w.t.n_rows - h * 128, 128), row0 = w.t.row0 + h * 128;
+                    if (n_rows <= 0) break;
+                    if (pieces[h] > 0)
+                        go = go && __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up));
+                    ++pieces[h];
                     if (!go) break;
-                    constexpr int VECS = D / 8;                 // 16-byte pieces of a row
+                    // lane: piece lane % PER of rows lane / PER, + STEP, ...; the head and token of a row move on by additions
+                    constexpr int PER = HALVES * 8, STEP = 32 / PER;
+                    const int ch = lane % PER, first_row = row0 + lane / PER;
+                    int t = first_row / a.group, hd = first_row - t * a.group;
+                    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (w.q.begin + t) * a.q_token_stride +
+                                          (w.head * a.group + hd) * a.q_head_stride + ch * 8;
+                    const uint32_t dst = smem_ptr(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes);
+                    const int64_t wrap = a.q_token_stride - a.group * a.q_head_stride;
 #pragma unroll 4
-                    for (int i = lane; i < 128 * VECS; i += 32) {
-                        const int rr = i / VECS, ch = i - rr * VECS;
-                        const int gi = row0 + min(rr, n_rows - 1), t = gi / a.group, hd = w.head * a.group + gi - t * a.group;
-                        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (w.q.begin + t) * a.q_token_stride +
-                                              hd * a.q_head_stride + ch * 8;
-                        copy16(smem_ptr(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)),
-                               src, rr < n_rows ? 16 : 0);
+                    for (int rr = lane / PER; rr < 128; rr += STEP) {
+                        if (8 * ch < D) copy16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), rr < n_rows ? src : a.q, rr < n_rows ? 16 : 0);
+                        src += STEP * a.q_head_stride;
+                        for (hd += STEP; hd >= a.group; hd -= a.group) src += wrap;
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     proxy_fence();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_ptr(&c.q_full[h]));
-                    ++pieces;
                 }
-                w.next(a);
+            }
+        } else {
+            // ----------------------------------------------- clearing of V
+            // Values that no row sees may be anything, and 0 * NaN is NaN: their rows are cleared before the product.
+            Ring<STAGES> at;
+            Ring<kLiveRing> tile;
+            const int ppt = max(kKeyTile >> a.page_shift, 1);
+            const uint32_t all = uint32_t((1ull << ppt) - 1);
+            bool go = true;
+            for (; go && w.left > 0; w.next(a)) {
+                const int take = w.take();
+                for (int i = 0; go && i < take; ++i, tile.step()) {
+                    at.step();  // past K
+                    go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.full[at.stage]), at.phase, &c.gave_up));
+                    const int key0 = (w.t.first + w.tile + i) * kKeyTile;
+                    const uint32_t live = *(volatile uint32_t*)&c.live[tile.stage];
+                    if (key0 < w.t.lo || key0 + kKeyTile > w.t.hi || live != all) {
+                        for (int r0 = 0; r0 < kKeyTile; r0 += 2) {
+                            const int r = r0 + (lane >> 4), half = (lane >> 3) & 1;
+                            const bool seen = key0 + r >= w.t.lo && key0 + r < w.t.hi && (live >> (r >> a.page_shift) & 1u);
+                            if (!seen && half < HALVES)
+                                *reinterpret_cast<uint4*>(ring + at.stage * C::TILE + half * kHalfBytes + r * 128 + (lane & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        proxy_fence();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(smem_ptr(&c.clean[tile.stage]));
+                    at.step();
+                }
             }
         }
     } else {
@@ -555,14 +609,21 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int all_hi = keys_to(a, w.q.kv, base + row0 / a.group);
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
-            float m = -INFINITY, l = 0.0f;
+            // p = 2^(s sc + neg).  The reference is the fp32 number nearest to m sc, and rest = m sc - reference (exact); a
+            // huge one (far) would leave no digits for the difference, there s - m is taken first and the reference is m sc.
+            float m = -INFINITY, l = 0.0f, neg = 0.0f, rest = 0.0f;
+            bool far = false;
             for (int i = 0; i < take; ++i, ++n_s, ++tiles) {
                 const int key0 = (w.t.first + w.tile + i) * kKeyTile;
                 wait(c.s_full[h], n_s & 1);
                 const uint32_t live = *(volatile uint32_t*)&c.live[tiles % kLiveRing];
                 float s[kKeyTile];
+                float tops[4];  // four chains: one would be all latency
 #pragma unroll
-                for (int x = 0; x < 4; ++x) tm_load(s + 32 * x, s_at + 32 * x);
+                for (int x0 = 0; x0 < kKeyTile; x0 += 64) {
+                    tm_load(s + x0, s_at + x0);
+                    tm_load(s + x0 + 32, s_at + x0 + 32);
+                }
                 tm_wait<kKeyTile>(s);
                 if (key0 < all_lo || key0 + kKeyTile > all_hi || live != all) {
                     const int from = lo - key0, to = hi - key0;
@@ -570,55 +631,62 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     for (int x = 0; x < kKeyTile; ++x)
                         if (x < from || x >= to || !(live >> (x >> a.page_shift) & 1u)) s[x] = -INFINITY;
                 }
-                float tops[8];  // eight chains: one would be all latency
 #pragma unroll
-                for (int x = 0; x < 8; ++x) tops[x] = s[x];
+                for (int x = 0; x < 4; ++x) tops[x] = fmaxf(s[2 * x], s[2 * x + 1]);
 #pragma unroll
-                for (int x = 8; x < kKeyTile; ++x) tops[x & 7] = fmaxf(tops[x & 7], s[x]);
-#pragma unroll
-                for (int x = 4; x > 0; x >>= 1)
-#pragma unroll
-                    for (int y = 0; y < x; ++y) tops[y] = fmaxf(tops[y], tops[y + x]);
-                const float top = tops[0];
+                for (int x = 8; x < kKeyTile; x += 2) tops[x / 2 & 3] = max3(tops[x / 2 & 3], s[x], s[x + 1]);
+                const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]);
                 // the reference moves when p would pass 2^kSlack
                 const bool moves = top > m && !((top - m) * sc <= kSlack);
-                if (__any_sync(0xffffffffu, moves && m != -INFINITY)) {
-                    const float f = moves && m != -INFINITY ? exp2_fast((m - top) * sc) : 1.0f;
-                    // the previous product has added to O
-                    wait(c.o_full[h], (n_s - 1) & 1);
-                    l *= f;
+                if (__any_sync(0xffffffffu, moves)) {
+                    const float m_new = moves ? top : m, scaled = m_new * sc;
+                    const bool huge = fabsf(scaled) > kExactRef;
+                    const float rest_new = moves && !huge ? __fmaf_rn(m_new, sc, -scaled) : moves ? 0.0f : rest;
+                    if (__any_sync(0xffffffffu, moves && m != -INFINITY)) {
+                        const float f = moves && m != -INFINITY ? exp2_fast(__fmaf_rn(m - m_new, sc, rest_new - rest)) : 1.0f;
+                        wait(c.o_full[h], (n_s - 1) & 1);  // the previous product has added to O
+                        l *= f;
 #pragma unroll
-                    for (int x = 0; x < D; x += 32) {
-                        float o[32];
-                        tm_load(o, o_at + x);
-                        tm_wait<32>(o);
+                        for (int x = 0; x < D; x += 16) {
+                            float o[16];
+                            tm_load16(o, o_at + x);
+                            tm_wait<16>(o);
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] *= f;
-                        tm_store(o_at + x, reinterpret_cast<const uint32_t*>(o));
+                            for (int y = 0; y < 16; ++y) o[y] *= f;
+                            tm_store16(o_at + x, reinterpret_cast<const uint32_t*>(o));
+                        }
+                        tc_wait_st();
                     }
-                    tc_wait_st();
+                    if (moves) {  // O and l are zero as long as m is -infinity
+                        m = m_new;
+                        rest = rest_new;
+                        neg = huge ? 0.0f : -scaled;
+                        far = huge;
+                    }
                 }
-                if (moves) m = top;  // O and l are zero as long as m is -infinity
-                const float ref = m == -INFINITY ? 0.0f : m;
-                const float2 neg = make_float2(-ref, -ref), cc = make_float2(sc, sc);
+                if (__any_sync(0xffffffffu, far)) {  // a reference too large for one fp32 number: subtract first
+                    const float by = far ? m : 0.0f;
+#pragma unroll
+                    for (int x = 0; x < kKeyTile; ++x) s[x] -= by;
+                }
+                const float2 neg2 = make_float2(neg, neg), cc = make_float2(sc, sc);
                 float2 sums[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) sums[x] = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int x0 = 0; x0 < kKeyTile / 2; x0 += 32) {
-                    uint32_t p[32], p_low[32];
+                for (int x0 = 0; x0 < kKeyTile / 2; x0 += 16) {
+                    uint32_t p[16], p_low[16];
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        // subtracted before it is scaled: exact for the largest scores too
-                        float2 e = mul2(add2(make_float2(s[2 * (x0 + x)], s[2 * (x0 + x) + 1]), neg), cc);
+                    for (int x = 0; x < 16; ++x) {
+                        float2 e = fma2(make_float2(s[2 * (x0 + x)], s[2 * (x0 + x) + 1]), cc, neg2);
                         e.x = exp2_fast(e.x);
                         e.y = exp2_fast(e.y);
                         sums[x & 3] = add2(sums[x & 3], e);
                         p[x] = pack2<BF16>(e.x, e.y);
                         if constexpr (BF16) p_low[x] = pack2<true>(e.x - bf16_low(p[x]), e.y - bf16_high(p[x]));
                     }
-                    tm_store(s_at + x0, p);
-                    if constexpr (BF16) tm_store(s_at + 64 + x0, p_low);
+                    tm_store16(s_at + x0, p);
+                    if constexpr (BF16) tm_store16(s_at + 64 + x0, p_low);
                 }
                 const float2 sum = add2(add2(sums[0], sums[1]), add2(sums[2], sums[3]));
                 l += sum.x + sum.y;
@@ -631,7 +699,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // ------------------------------------------------------- results
             wait(c.o_full[h], (n_s - 1) & 1);
             const bool mine = row < n_rows;
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const float to_m = exp2_fast(-rest);  // from the reference to m
+            l *= to_m;
+            const float inv = whole ? (l > 0.0f ? to_m / l : 0.0f) : to_m;
             const int64_t at = int64_t(2 * blockIdx.x + (first && w.tile > 0 ? 0 : 1)) * kChunkRows + h * 128 + row;
             uint16_t* out = static_cast<uint16_t*>(a.out) + (w.q.begin + token) * a.out_token_stride + head * a.out_head_stride;
 #pragma unroll
@@ -648,7 +718,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 } else if (mine) {
 #pragma unroll
                     for (int y = 0; y < 32; y += 4)
-                        *reinterpret_cast<float4*>(ws.o + at * D + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                        *reinterpret_cast<float4*>(ws.o + at * D + x + y) = 
+                            make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv);
                 }
                 __syncwarp();
             }
