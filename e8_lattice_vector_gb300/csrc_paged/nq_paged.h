@@ -42,6 +42,22 @@ inline int check_pool(const nq_pool* p) {
 // Streaming multiprocessors of the current device, 0 when it cannot be queried.
 int paged_sm_count();
 
+// Division of n < 2^31 by a number fixed for the call: n / d = (umulhi(n, mul) + n) >> shift with 2^shift >= d and
+// mul = floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery's division by invariant integers).
+struct FastDiv {
+    uint32_t mul, shift;
+    static FastDiv by(uint32_t d) {
+        FastDiv f;
+        f.shift = 0;
+        while ((uint64_t(1) << f.shift) < d) ++f.shift;
+        f.mul = uint32_t((((uint64_t(1) << f.shift) - d) << 32) / d + 1);
+        return f;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int of(int n) const { return int((__umulhi(uint32_t(n), mul) + uint32_t(n)) >> shift); }
+#endif
+};
+
 // What the attention kernels know of a call.
 struct AttnArgs {
     const void* q;
@@ -57,6 +73,8 @@ struct AttnArgs {
     int64_t page_stride, head_stride, slot_stride;
     int tokens, q_heads, kv_heads, group, requests, table_cols, page_shift, pages, head_dim, causal, window;
     int bf16;
+    int out_by_32;  // rows of out start on 32-byte boundaries
+    FastDiv by_group;
     float scale;
     cudaStream_t stream;
 };

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
                 acc.w += o.w;
             }
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            const int t = q.begin + (row0 + row) / a.group, h = s.head * a.group + (row0 + row) % a.group;
+            const int token = a.by_group.of(row0 + row), t = q.begin + token, h = s.head * a.group + row0 + row - token * a.group;
             uint2 packed;
             packed.x = pack2<BF16>(acc.x * inv, acc.y * inv);
             packed.y = pack2<BF16>(acc.z * inv, acc.w * inv);
@@ -219,6 +219,9 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
     x.causal = a->causal;
     x.window = a->window;
     x.bf16 = pool->dtype == NQ_BF16;
+    x.out_by_32 = nq::paged_aligned(out, 32) && (a->tokens == 1 || a->out_token_stride % 16 == 0) &&
+                  (a->q_heads == 1 || a->out_head_stride % 16 == 0);
+    x.by_group = nq::FastDiv::by(uint32_t(x.group));
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
     return nq::few_rows(a, x.group) ? nq::launch_attention_small(x) : nq::launch_attention_chunk(x);

@@ -81,8 +81,8 @@ __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& a, const Request&
     t.row0 = row_tile * kChunkRows;
     t.n_rows = min(q.n * a.group - t.row0, kChunkRows);
     const int base = q.kv - q.n;
-    t.lo = keys_from(a, base + t.row0 / a.group);
-    t.hi = keys_to(a, q.kv, base + (t.row0 + t.n_rows - 1) / a.group);
+    t.lo = keys_from(a, base + a.by_group.of(t.row0));
+    t.hi = keys_to(a, q.kv, base + a.by_group.of(t.row0 + t.n_rows - 1));
     t.first = min(t.lo, t.hi) / kKeyTile;
     t.count = max((t.hi + kKeyTile - 1) / kKeyTile - t.first, 1);
     return t;
@@ -269,6 +269,15 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* u) {
         : "memory");
 }
 
+// 32 bytes to a 32-byte boundary.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* u) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+// The lowest n bits, n of any sign and size.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+
 // Pairs of fp32 in one operation.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     float2 r;
@@ -297,7 +306,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct ChunkControl {
     uint64_t full[8], empty[8];
     uint64_t clean[kLiveRing];  // per key tile: its V has no values that no row sees
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t live[kLiveRing];  // per key tile: which of its pages are loaded
     uint32_t tmem;
     int gave_up;
@@ -367,8 +376,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         }
         for (int i = 0; i < kLiveRing; ++i) mbar_init(smem_ptr(&c.clean[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_ptr(&c.q_full[i]), 1);
-            mbar_init(smem_ptr(&c.q_free[i]), 1);
+            mbar_init(smem_ptr(&c.q_full[i]), 4);
             mbar_init(smem_ptr(&c.s_full[i]), 1);
             mbar_init(smem_ptr(&c.p_full[i]), 4);
             mbar_init(smem_ptr(&c.o_full[i]), 1);
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     go = go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up);
                     tc_fence_after();
                 };
-                auto scores = [&](int h, int st, bool last) {  // S_h = Q_h K^T; the last of a row tile frees Q
+                auto scores = [&](int h, int st) {  // S_h = Q_h K^T
                     uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + st * (C::TILE >> 4);
                     asm volatile("" : "+r"(qd), "+r"(kd));  // the steps are added here, not kept in registers
 #pragma unroll
@@ -459,7 +467,6 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         tc_mma(tmem + h * 128, qd + step, kd + step, s_idesc, k > 0);
                     }
                     tc_commit(smem_ptr(&c.s_full[h]));
-                    if (last) tc_commit(smem_ptr(&c.q_free[h]));
                 };
                 while (go && w.left > 0) {
                     const int take = w.take(), halves = w.t.n_rows > 128 ? 2 : 1;
@@ -467,7 +474,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     for (int h = 0; h < halves; ++h) {
                         await(c.q_full[h], q_phase[h]);
                         q_phase[h] ^= 1;
-                        if (go) scores(h, at.stage, take == 1);
+                        if (go) scores(h, at.stage);
                     }
                     if (go) tc_commit(smem_ptr(&c.empty[at.stage]));
                     at.step();
@@ -491,7 +498,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                                 if constexpr (BF16) tc_mma_ta(o, p + 64 + 8 * k, vd + 128 * k, o_idesc, true);
                             }
                             tc_commit(smem_ptr(&c.o_full[h]));
-                            if (more) scores(h, at.stage, i + 2 == take);
+                            if (more) scores(h, at.stage);
                         }
                         if (go) tc_commit(smem_ptr(&c.empty[v.stage]));
                         if (more) {
@@ -509,41 +516,6 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
             __syncwarp();
         } else if (warp == 10) {
-            // ------------------------------------------------------------ Q
-            // As soon as the last scores of a row tile are there its Q is not read any more: the next one's loads run
-            // beside the last tile's exponentials, its product and the results.
-            uint32_t pieces[2] = {0, 0};
-            bool go = true;
-            for (; go && w.left > 0; w.next(a)) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n_rows = min(w.t.n_rows - h * 128, 128), row0 = w.t.row0 + h * 128;
-                    if (n_rows <= 0) break;
-                    if (pieces[h] > 0)
-                        go = go && __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up));
-                    ++pieces[h];
-                    if (!go) break;
-                    // lane: piece lane % PER of rows lane / PER, + STEP, ...; the head and token of a row move on by additions
-                    constexpr int PER = HALVES * 8, STEP = 32 / PER;
-                    const int ch = lane % PER, first_row = row0 + lane / PER;
-                    int t = first_row / a.group, hd = first_row - t * a.group;
-                    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (w.q.begin + t) * a.q_token_stride +
-                                          (w.head * a.group + hd) * a.q_head_stride + ch * 8;
-                    const uint32_t dst = smem_ptr(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes);
-                    const int64_t wrap = a.q_token_stride - a.group * a.q_head_stride;
-#pragma unroll 4
-                    for (int rr = lane / PER; rr < 128; rr += STEP) {
-                        if (8 * ch < D) copy16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), rr < n_rows ? src : a.q, rr < n_rows ? 16 : 0);
-                        src += STEP * a.q_head_stride;
-                        for (hd += STEP; hd >= a.group; hd -= a.group) src += wrap;
-                    }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    proxy_fence();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_ptr(&c.q_full[h]));
-                }
-            }
-        } else {
             // ----------------------------------------------- clearing of V
             // Values that no row sees may be anything, and 0 * NaN is NaN: their rows are cleared before the product.
             Ring<STAGES> at;
@@ -573,6 +545,16 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     at.step();
                 }
             }
+        } else if (lane == 0) {
+            // -------- the row tile that this block begins and does not end
+            AttnSplit split{0, 0, 0, -1};
+            for (; w.left > 0; w.next(a)) {
+                const int take = w.take();
+                if (w.tile == 0 && take < w.t.count)
+                    split = AttnSplit{w.r, w.row_tile, w.head,
+                                      share_holding(start.total, start.end - 1 + (w.t.count - take))};
+            }
+            ws.split[blockIdx.x] = split;
         }
     } else {
         // ------------------------------------------- softmax of one half
@@ -586,27 +568,49 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             __syncwarp();
             tc_fence_after();
         };
+        // Q of a piece into this half's place: 16 copies a thread, a row's pieces on neighbouring threads
+        auto load_q = [&](const ChunkWalk& x) {
+            constexpr int PER = HALVES * 8, STEP = 128 / PER;
+            const int n_rows = min(x.t.n_rows - h * 128, 128), row0 = x.t.row0 + h * 128, ch = row % PER;
+            const uint16_t* q = static_cast<const uint16_t*>(a.q) + int64_t(x.q.begin) * a.q_token_stride + ch * 8;
+            const uint32_t dst = smem_ptr(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes);
+            if (8 * ch < D) {
+#pragma unroll
+                for (int rr = row / PER; rr < 128; rr += STEP) {
+                    const int gi = row0 + min(rr, n_rows - 1), t = a.by_group.of(gi), hd = x.head * a.group + gi - t * a.group;
+                    copy16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), q + t * a.q_token_stride + hd * a.q_head_stride,
+                           rr < n_rows ? 16 : 0);
+                }
+            }
+        };
+        auto q_loaded = [&] {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_ptr(&c.q_full[h]));
+        };
         int n_s = 0;      // tiles of this half so far
         int tiles = 0;    // tiles of the block so far
-        bool first = true;
-        if (threadIdx.x == 0) ws.split[blockIdx.x].last_block = -1;
-        for (; w.left > 0; first = false, w.next(a)) {
+        bool first = true, loading = false;  // loading: this piece's Q is on its way
+        ChunkWalk ahead;
+        for (; w.left > 0; first = false, w = ahead) {
             const int take = w.take();
             const bool whole = w.tile == 0 && take == w.t.count;
-            if (threadIdx.x == 0 && w.tile == 0 && !whole)
-                ws.split[blockIdx.x] = AttnSplit{w.r, w.row_tile, w.head,
-                                                 share_holding(start.total, start.end - 1 + (w.t.count - take))};
+            ahead = w;
+            ahead.next(a);
             const int n_rows = min(w.t.n_rows - h * 128, 128);
             if (n_rows <= 0) {  // the product warp skips this half too
                 tiles += take;
                 continue;
             }
+            if (!loading) load_q(w);
+            q_loaded();
             const int row0 = w.t.row0 + h * 128, base = w.q.kv - w.q.n;
-            const int gi = row0 + min(row, n_rows - 1), token = gi / a.group, head = w.head * a.group + gi - token * a.group;
+            const int gi = row0 + min(row, n_rows - 1), token = a.by_group.of(gi), head = w.head * a.group + gi - token * a.group;
             const int lo = keys_from(a, base + token), hi = keys_to(a, w.q.kv, base + token);
             // keys [all_lo, all_hi) are seen by every row of the half
-            const int all_lo = keys_from(a, base + (row0 + n_rows - 1) / a.group);
-            const int all_hi = keys_to(a, w.q.kv, base + row0 / a.group);
+            const int all_lo = keys_from(a, base + a.by_group.of(row0 + n_rows - 1));
+            const int all_hi = keys_to(a, w.q.kv, base + a.by_group.of(row0));
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
             // p = 2^(s sc + neg).  The reference is the fp32 number nearest to m sc, and rest = m sc - reference (exact); a
@@ -628,8 +632,17 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (key0 < all_lo || key0 + kKeyTile > all_hi || live != all) {
                     const int from = lo - key0, to = hi - key0;
 #pragma unroll
-                    for (int x = 0; x < kKeyTile; ++x)
-                        if (x < from || x >= to || !(live >> (x >> a.page_shift) & 1u)) s[x] = -INFINITY;
+                    for (int x0 = 0; x0 < kKeyTile; x0 += 32) {
+                        // a bit for each of 32 keys that this row sees
+                        uint32_t see = low_bits(to - x0) & ~low_bits(from - x0);
+                        const int shift = a.page_shift;
+                        if (!(live >> (x0 >> shift) & 1u)) see &= shift == 4 ? 0xffff0000u : 0u;
+                        if (shift == 4 && !(live >> ((x0 >> 4) + 1) & 1u)) see &= 0xffffu;
+                        if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            if (!(see & 1u << x)) s[x0 + x] = -INFINITY;
+                    }
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) tops[x] = fmaxf(s[2 * x], s[2 * x + 1]);
@@ -697,6 +710,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
 
             // ------------------------------------------------------- results
+            // The last scores have been read, and with them Q for the last time: the next piece's Q loads meanwhile.
+            loading = ahead.left > 0 && ahead.t.n_rows > h * 128;
+            if (loading) load_q(ahead);
             wait(c.o_full[h], (n_s - 1) & 1);
             const bool mine = row < n_rows;
             const float to_m = exp2_fast(-rest);  // from the reference to m
@@ -704,25 +720,30 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const float inv = whole ? (l > 0.0f ? to_m / l : 0.0f) : to_m;
             const int64_t at = int64_t(2 * blockIdx.x + (first && w.tile > 0 ? 0 : 1)) * kChunkRows + h * 128 + row;
             uint16_t* out = static_cast<uint16_t*>(a.out) + (w.q.begin + token) * a.out_token_stride + head * a.out_head_stride;
+            float o[D];
 #pragma unroll
-            for (int x = 0; x < D; x += 32) {
-                float o[32];
-                tm_load(o, o_at + x);
-                tm_wait<32>(o);
-                if (mine && whole) {
+            for (int x = 0; x < D; x += 32) tm_load(o + x, o_at + x);
+            tm_wait<D>(o);
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8)
-                        *reinterpret_cast<uint4*>(out + x + y) =
-                            make_uint4(pack2<BF16>(o[y] * inv, o[y + 1] * inv), pack2<BF16>(o[y + 2] * inv, o[y + 3] * inv),
-                                       pack2<BF16>(o[y + 4] * inv, o[y + 5] * inv), pack2<BF16>(o[y + 6] * inv, o[y + 7] * inv));
-                } else if (mine) {
+            for (int x = 0; x < D; ++x) o[x] *= inv;
+            if (mine && whole) {
 #pragma unroll
-                    for (int y = 0; y < 32; y += 4)
-                        *reinterpret_cast<float4*>(ws.o + at * D + x + y) = 
-                            make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv);
+                for (int x = 0; x < D; x += 16) {
+                    uint32_t p[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) p[y] = pack2<BF16>(o[x + 2 * y], o[x + 2 * y + 1]);
+                    if (a.out_by_32) {
+                        store32(out + x, p);
+                    } else {
+                        *reinterpret_cast<uint4*>(out + x) = make_uint4(p[0], p[1], p[2], p[3]);
+                        *reinterpret_cast<uint4*>(out + x + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+                    }
                 }
-                __syncwarp();
+            } else if (mine) {
+#pragma unroll
+                for (int x = 0; x < D; x += 8) store32(ws.o + at * D + x, reinterpret_cast<const uint32_t*>(o + x));
             }
+            __syncwarp();
             tc_fence_before();
             if (mine) {
                 if (!whole)

@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
         bool go = true;
         while (go && w.left > 0) {
             const int take = w.take();
-            const int p0 = w.q.kv - w.q.n + w.row_tile * kSmallRows / a.group;
-            const int p1 = w.q.kv - w.q.n + (min((w.row_tile + 1) * kSmallRows, w.q.n * a.group) - 1) / a.group;
+            const int p0 = w.q.kv - w.q.n + a.by_group.of(w.row_tile * kSmallRows);
+            const int p1 = w.q.kv - w.q.n + a.by_group.of(min((w.row_tile + 1) * kSmallRows, w.q.n * a.group) - 1);
             const int lo = keys_from(a, p0), hi = keys_to(a, w.q.kv, p1);
             for (int i = 0; i < take; ++i, ++n) {
                 const int key0 = (w.s.first + w.tile + i) * kKeyTile;
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = rq + 8 * e;
-            const int gi = row0 + min(row, n_rows - 1), t = gi / a.group, h = w.head * a.group + gi - t * a.group;
+            const int gi = row0 + min(row, n_rows - 1), t = a.by_group.of(gi), h = w.head * a.group + gi - t * a.group;
             pos2[e] = pbase + t;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
                                                                     (w.q.begin + t) * a.q_token_stride +
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
                 qf[k][e + 2] = __ldg(src + 8 * k + cq + 4);
             }
         }
-        const int p_min = pbase + row0 / a.group, p_max = pbase + (row0 + n_rows - 1) / a.group;
+        const int p_min = pbase + a.by_group.of(row0), p_max = pbase + a.by_group.of(row0 + n_rows - 1);
         const int lo = keys_from(a, p_min), hi = keys_to(a, w.q.kv, p_max);
         // keys [all_lo, all_hi) are seen by every row
         const int all_lo = keys_from(a, p_max), all_hi = keys_to(a, w.q.kv, p_min);
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             sum += c.m[v][row] == -INFINITY ? 0.0f : c.l[v][row] * exp2_fast((c.m[v][row] - top) * sc);
         const bool whole = w.tile == 0 && take == w.s.count;
         const int slot = 2 * blockIdx.x + (first && w.tile > 0 ? 0 : 1);
-        const int t = w.q.begin + (row0 + row) / a.group, h = w.head * a.group + (row0 + row) % a.group;
+        const int token = a.by_group.of(row0 + row), t = w.q.begin + token, h = w.head * a.group + row0 + row - token * a.group;
 #pragma unroll
         for (int x = 0; x < D; x += 64) {
             if (x) named_barrier<1, kConsumers>();  // the first 64 columns are read
