@@ -36,10 +36,16 @@ struct Chunk {
 };
 constexpr int kLiveRing = 8;  // tiles whose page masks are kept; the loads are at most five tiles ahead of a half
 
-// Where a block's share begins.
+// A row tile costs about this many key tiles on top of its own: its Q, the first scores, the results.  Shares are equal in
+// key tiles plus these, or the block whose share is many short row tiles (the beginning of a prompt) would be the last
+// to end.  Not counted when a share has few tiles: there a block's idle time is worth more than an even cost.
+constexpr int kRowTileCost = 3, kCostFrom = 16;
+
+// Where a block's share begins: `unit` counts the row tile's cost, then its key tiles.
 struct ChunkStart {
-    int request, row_tile, head, tile;
+    int request, row_tile, head, unit;
     long long begin, end, total;
+    int cost;
 };
 
 struct ChunkPlan {
@@ -151,19 +157,21 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     }
     if (threadIdx.x == 0) plan.tile_sum[pairs] = tiles;
     __syncthreads();
+    const int cost = tiles >= (long long)kCostFrom * kAttnGrid ? kRowTileCost : 0;
+    const long long per_pair = (long long)cost * a.kv_heads, units = tiles + per_pair * pairs;
     for (int b = threadIdx.x; b < kAttnGrid; b += kPlanThreads)
-        if (share_begin(tiles, b) >= tiles) plan.start[b] = ChunkStart{0, 0, 0, 0, tiles, tiles, tiles};
+        if (share_begin(units, b) >= units) plan.start[b] = ChunkStart{0, 0, 0, 0, units, units, units, cost};
     for (long long p = threadIdx.x; p < pairs; p += kPlanThreads) {
-        const long long from = plan.tile_sum[p], to = plan.tile_sum[p + 1];
+        const long long from = plan.tile_sum[p] + per_pair * p, to = plan.tile_sum[p + 1] + per_pair * (p + 1);
         const int count = int((to - from) / a.kv_heads);
-        int b = share_holding(tiles, from);
-        if (share_begin(tiles, b) < from) ++b;
+        int b = share_holding(units, from);
+        if (share_begin(units, b) < from) ++b;
         for (; b < kAttnGrid; ++b) {
-            const long long begin = share_begin(tiles, b);
+            const long long begin = share_begin(units, b);
             if (begin >= to) break;
             const long long at = begin - from;
             plan.start[b] = ChunkStart{plan.pair_request[p], plan.pair_row_tile[p], int(at / count), int(at % count),
-                                       begin, share_begin(tiles, b + 1), tiles};
+                                       begin, share_begin(units, b + 1), units, cost};
         }
     }
 }
@@ -314,46 +322,55 @@ struct ChunkControl {
 
 // Walks the pieces of a block's share.
 struct ChunkWalk {
-    int r, row_tile, head, tile;
-    long long left;
+    int r, row_tile, head, unit, cost;
+    long long left;  // units
     Request q;
     int row_tiles;
     RowTile t;
+    int tile, take;  // the piece: key tiles [tile, tile + take) of the row tile; take > 0 while left > 0
 
     __device__ __forceinline__ void begin(const AttnArgs& a, const ChunkStart& s) {
         r = s.request;
         row_tile = s.row_tile;
         head = s.head;
-        tile = s.tile;
+        unit = s.unit;
+        cost = s.cost;
         left = s.end - s.begin;
         if (left > 0) {
             q = load_request(a, r);
             row_tiles = row_tiles_of(a, q);
             t = row_tile_of(a, q, row_tile);
+            if (!piece()) next(a);
         }
     }
-    __device__ __forceinline__ int take() const { return int(min((long long)(t.count - tile), left)); }
+    __device__ __forceinline__ bool piece() {
+        const int end = int(min((long long)(t.count + cost), unit + left));
+        tile = max(unit - cost, 0);
+        take = end - cost - tile;
+        return take > 0;
+    }
     __device__ __forceinline__ void next(const AttnArgs& a) {
-        const int n = take();
-        left -= n;
-        tile += n;
-        if (tile < t.count) return;  // left == 0
-        tile = 0;
-        if (++head < a.kv_heads) return;
-        head = 0;
-        if (left <= 0) return;
-        if (++row_tile >= row_tiles) {
-            row_tile = 0;
-            do {
-                if (++r >= a.requests) {  // not reached while the lengths stay as they were summed
-                    left = 0;
-                    return;
+        do {
+            const int n = int(min((long long)(t.count + cost - unit), left));
+            left -= n;
+            if (left <= 0) return;
+            unit = 0;
+            if (++head >= a.kv_heads) {
+                head = 0;
+                if (++row_tile >= row_tiles) {
+                    row_tile = 0;
+                    do {
+                        if (++r >= a.requests) {  // not reached while the lengths stay as they were summed
+                            left = 0;
+                            return;
+                        }
+                        q = load_request(a, r);
+                        row_tiles = row_tiles_of(a, q);
+                    } while (row_tiles == 0);
                 }
-                q = load_request(a, r);
-                row_tiles = row_tiles_of(a, q);
-            } while (row_tiles == 0);
-        }
-        t = row_tile_of(a, q, row_tile);
+                t = row_tile_of(a, q, row_tile);
+            }
+        } while (!piece());
     }
 };
 
@@ -410,7 +427,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             int n = 0, tiles = 0;
             bool go = true;
             while (go && w.left > 0) {
-                const int take = w.take();
+                const int take = w.take;
                 for (int i = 0; go && i < take; ++i, ++tiles) {
                     const int k0 = (w.t.first + w.tile + i) * kKeyTile + (pg << a.page_shift);
                     int page = -1;
@@ -469,7 +486,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     tc_commit(smem_ptr(&c.s_full[h]));
                 };
                 while (go && w.left > 0) {
-                    const int take = w.take(), halves = w.t.n_rows > 128 ? 2 : 1;
+                    const int take = w.take, halves = w.t.n_rows > 128 ? 2 : 1;
                     await(c.full[at.stage], at.phase);
                     for (int h = 0; h < halves; ++h) {
                         await(c.q_full[h], q_phase[h]);
@@ -524,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const uint32_t all = uint32_t((1ull << ppt) - 1);
             bool go = true;
             for (; go && w.left > 0; w.next(a)) {
-                const int take = w.take();
+                const int take = w.take;
                 for (int i = 0; go && i < take; ++i, tile.step()) {
                     at.step();  // past K
                     go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.full[at.stage]), at.phase, &c.gave_up));
@@ -549,8 +566,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // -------- the row tile that this block begins and does not end
             AttnSplit split{0, 0, 0, -1};
             for (; w.left > 0; w.next(a)) {
-                const int take = w.take();
-                if (w.tile == 0 && take < w.t.count)
+                const int take = w.take;
+                if (w.tile == 0 && take < w.t.count)  // the last piece
                     split = AttnSplit{w.r, w.row_tile, w.head,
                                       share_holding(start.total, start.end - 1 + (w.t.count - take))};
             }
@@ -591,10 +608,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         };
         int n_s = 0;      // tiles of this half so far
         int tiles = 0;    // tiles of the block so far
-        bool first = true, loading = false;  // loading: this piece's Q is on its way
+        bool loading = false;  // loading: this piece's Q is on its way
         ChunkWalk ahead;
-        for (; w.left > 0; first = false, w = ahead) {
-            const int take = w.take();
+        for (; w.left > 0; w = ahead) {
+            const int take = w.take;
             const bool whole = w.tile == 0 && take == w.t.count;
             ahead = w;
             ahead.next(a);
@@ -718,7 +735,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const float to_m = exp2_fast(-rest);  // from the reference to m
             l *= to_m;
             const float inv = whole ? (l > 0.0f ? to_m / l : 0.0f) : to_m;
-            const int64_t at = int64_t(2 * blockIdx.x + (first && w.tile > 0 ? 0 : 1)) * kChunkRows + h * 128 + row;
+            const int64_t at = int64_t(2 * blockIdx.x + (w.tile > 0 ? 0 : 1)) * kChunkRows + h * 128 + row;
             uint16_t* out = static_cast<uint16_t*>(a.out) + (w.q.begin + token) * a.out_token_stride + head * a.out_head_stride;
             float o[D];
 #pragma unroll
