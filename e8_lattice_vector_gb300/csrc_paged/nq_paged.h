@@ -75,6 +75,7 @@ struct AttnArgs {
     int bf16;
     int out_by_32;  // rows of out start on 32-byte boundaries
     FastDiv by_group;
+    int half_tokens;  // tokens whose rows fit one half of the large kernel's row tile (0: a group of more than 128 heads)
     float scale;
     cudaStream_t stream;
 };
@@ -112,17 +113,20 @@ inline AttnWorkspace attn_workspace(void* base, int rows, int head_dim) {
 
 // Rows of q (times the heads that share a KV head) per tile of the small kernel.
 constexpr int kSmallRows = 16;
-// ... and of the large one.
+// ... and of the large one: two halves of 128, each filled with the rows of whole tokens.
 constexpr int kChunkRows = 256;
 
 // TMA maps of the two pools: boxes of 64 columns x min(page_size, 128) slots, 128-byte swizzle.  false on failure.
 bool make_pool_maps(const AttnArgs& a, CUtensorMap* k, CUtensorMap* v);
+// TMA map of q: boxes of 64 columns x a group's heads x a half's tokens, 128-byte swizzle.
+bool make_query_map(const AttnArgs& a, CUtensorMap* q);
 
 int launch_attention_small(const AttnArgs& a);
 int launch_attention_chunk(const AttnArgs& a);
 uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim);
-// Joins the pieces of split row tiles of `rows` rows (launched after either kernel, as its dependent).
-int launch_attention_join(const AttnArgs& a, int rows);
+// Joins the pieces of split row tiles (launched after either kernel, as its dependent).  A row tile has `tile_rows` rows;
+// the workspace has `slot_rows` for it, row i at i / half_rows * 128 + i % half_rows.
+int launch_attention_join(const AttnArgs& a, int slot_rows, int tile_rows, int half_rows);
 
 // Whether a kernel gave up a wait since the last call.
 int small_gave_up(int* seen);

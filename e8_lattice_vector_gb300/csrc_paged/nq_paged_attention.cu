@@ -14,24 +14,27 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 
-// Block (b, y): the row tile that block b of the attention kernel began and did not end, its rows y, y + gridDim.y, ...
-// Every warp finds the pieces' common maximum, takes every eighth piece, and the eight sums meet in shared
-// memory, in an order that depends on the lengths alone.
-template <bool BF16>
+// Block (b, y): the row tile that block b of the attention kernel began and did not end.  SPREAD warps share a row: each
+// takes every SPREAD-th piece, and the sums meet in shared memory, in an order that depends on the lengths alone.  Few rows
+// have many pieces (up to one from every block) and take all eight warps each; many rows take a warp each.
+template <bool BF16, int SPREAD>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    attention_join_kernel(const AttnArgs a, const AttnWorkspace ws, int rows) {
+    attention_join_kernel(const AttnArgs a, const AttnWorkspace ws, int slot_rows, int tile_rows, int half_rows) {
+    constexpr int ROWS = kJoinWarps / SPREAD;  // rows at a time
     __shared__ float4 part[kJoinWarps][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, share = warp % SPREAD;
     pdl_wait();
     const AttnSplit s = ws.split[b];
     if (s.last_block < 0) return;
     const Request q = load_request(a, s.request);
-    const int row0 = s.row_tile * rows, n_rows = min(q.n * a.group - row0, rows);
+    const int row0 = s.row_tile * tile_rows, n_rows = min(q.n * a.group - row0, tile_rows);
     const int pieces = s.last_block - b + 1;
     const float sc = a.scale * kLog2e;
     const int D = a.head_dim;
-    for (int row = blockIdx.y; row < n_rows; row += gridDim.y) {
-        auto at = [&](int i) { return int64_t(i == 0 ? 2 * b + 1 : 2 * (b + i)) * rows + row; };
+    for (int first = blockIdx.y * ROWS; first < n_rows; first += gridDim.y * ROWS) {
+        const int row = min(first + warp / SPREAD, n_rows - 1);
+        const int half = row >= half_rows, slot_row = half * 128 + row - half * half_rows;
+        auto at = [&](int i) { return int64_t(i == 0 ? 2 * b + 1 : 2 * (b + i)) * slot_rows + slot_row; };
         float top = -INFINITY, sum = 0.0f;
         for (int i = lane; i < pieces; i += 32) top = fmaxf(top, ws.ml[at(i)].x);
 #pragma unroll
@@ -45,7 +48,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (4 * lane < D) {
 #pragma unroll 4
-            for (int i = warp; i < pieces; i += kJoinWarps) {
+            for (int i = share; i < pieces; i += SPREAD) {
                 const float m = ws.ml[at(i)].x;
                 const float4 o = *reinterpret_cast<const float4*>(ws.o + at(i) * D + 4 * lane);
                 const float f = m == -INFINITY ? 0.0f : exp2_fast((m - top) * sc);
@@ -55,28 +58,41 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
                 acc.w = fmaf(o.w, f, acc.w);
             }
         }
-        part[warp][lane] = acc;
-        __syncthreads();
-        if (warp == 0 && 4 * lane < D) {
-            for (int v = 1; v < kJoinWarps; ++v) {
-                const float4 o = part[v][lane];
-                acc.x += o.x;
-                acc.y += o.y;
-                acc.z += o.z;
-                acc.w += o.w;
+        if constexpr (SPREAD > 1) {
+            part[warp][lane] = acc;
+            __syncthreads();
+            if (share == 0) {
+#pragma unroll
+                for (int v = 1; v < SPREAD; ++v) {
+                    const float4 o = part[warp + v][lane];
+                    acc.x += o.x;
+                    acc.y += o.y;
+                    acc.z += o.z;
+                    acc.w += o.w;
+                }
             }
+            __syncthreads();  // part is read
+        }
+        if (share == 0 && first + warp / SPREAD < n_rows) {
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
             const int token = a.by_group.of(row0 + row), t = q.begin + token, h = s.head * a.group + row0 + row - token * a.group;
             uint2 packed;
             packed.x = pack2<BF16>(acc.x * inv, acc.y * inv);
             packed.y = pack2<BF16>(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_token_stride + h * a.out_head_stride +
-                                      4 * lane) = packed;
+            if (4 * lane < D)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_token_stride + h * a.out_head_stride +
+                                          4 * lane) = packed;
             if (lane == 0 && a.lse != nullptr)
                 a.lse[int64_t(t) * a.q_heads + h] = sum > 0.0f ? top * a.scale + logf(sum) : -INFINITY;
         }
-        __syncthreads();  // part is read
     }
+}
+
+template <int SPREAD>
+cudaError_t launch_join(const cudaLaunchConfig_t& cfg, const AttnArgs& a, const AttnWorkspace& ws, int slot_rows,
+                        int tile_rows, int half_rows) {
+    return a.bf16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, SPREAD>, a, ws, slot_rows, tile_rows, half_rows)
+                  : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, SPREAD>, a, ws, slot_rows, tile_rows, half_rows);
 }
 
 int check_attention(const nq_attention* a, const nq_pool* pool) {
@@ -97,12 +113,13 @@ int check_attention(const nq_attention* a, const nq_pool* pool) {
     return NQ_OK;
 }
 
-// Whether a request's rows for one KV head fit a tile of the small kernel.
+// The small kernel's calls: a request's rows for one KV head fit its tile, or a token's rows do not fit a half of
+// the large one's.
 bool few_rows(const nq_attention* a, int group) {
-    return int64_t(std::min(a->max_q, a->tokens)) * group <= kSmallRows;
+    return int64_t(std::min(a->max_q, a->tokens)) * group <= kSmallRows || group > 128;
 }
 
-bool make_pool_map(const AttnArgs& a, const void* base, CUtensorMap* map) {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -113,6 +130,11 @@ bool make_pool_map(const AttnArgs& a, const void* base, CUtensorMap* map) {
             q == cudaDriverEntryPointSuccess)
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
+    return encode;
+}
+
+bool make_pool_map(const AttnArgs& a, const void* base, CUtensorMap* map) {
+    const auto encode = tensor_map_encoder();
     if (!encode) return false;
     const int page_size = 1 << a.page_shift;
     const cuuint64_t dims[4] = {cuuint64_t(a.head_dim), cuuint64_t(page_size), cuuint64_t(a.kv_heads), cuuint64_t(a.pages)};
@@ -134,20 +156,34 @@ bool make_pool_maps(const AttnArgs& a, CUtensorMap* k, CUtensorMap* v) {
     return make_pool_map(a, a.k_pages, k) && make_pool_map(a, a.v_pages, v);
 }
 
-int launch_attention_join(const AttnArgs& a, int rows) {
-    const AttnWorkspace ws = attn_workspace(a.workspace, rows, a.head_dim);
+bool make_query_map(const AttnArgs& a, CUtensorMap* q) {
+    const auto encode = tensor_map_encoder();
+    if (!encode) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(a.head_dim), cuuint64_t(a.q_heads), cuuint64_t(a.tokens)};
+    const cuuint64_t strides[2] = {cuuint64_t(a.q_heads > 1 ? a.q_head_stride : a.head_dim) * 2,
+                                   cuuint64_t(a.tokens > 1 ? a.q_token_stride : a.head_dim) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(a.group), cuuint32_t(a.half_tokens)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(q, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(a.q),
+                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int launch_attention_join(const AttnArgs& a, int slot_rows, int tile_rows, int half_rows) {
+    const AttnWorkspace ws = attn_workspace(a.workspace, slot_rows, a.head_dim);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    // a block per row, up to 16
-    cfg.gridDim = dim3(kAttnGrid, unsigned(std::min<int64_t>(std::max<int64_t>(int64_t(a.tokens) * a.group, 1), 16)));
+    const bool few = slot_rows <= kSmallRows;
+    const int64_t rows = std::min<int64_t>(int64_t(a.tokens) * a.group, tile_rows);
+    cfg.gridDim = dim3(kAttnGrid, unsigned(few ? rows : (rows + kJoinWarps - 1) / kJoinWarps));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = a.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true>, a, ws, rows)
-                                 : cudaLaunchKernelEx(&cfg, attention_join_kernel<false>, a, ws, rows);
+    const cudaError_t e = few ? launch_join<kJoinWarps>(cfg, a, ws, slot_rows, tile_rows, half_rows)
+                              : launch_join<1>(cfg, a, ws, slot_rows, tile_rows, half_rows);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
@@ -222,6 +258,7 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
     x.out_by_32 = nq::paged_aligned(out, 32) && (a->tokens == 1 || a->out_token_stride % 16 == 0) &&
                   (a->q_heads == 1 || a->out_head_stride % 16 == 0);
     x.by_group = nq::FastDiv::by(uint32_t(x.group));
+    x.half_tokens = 128 / x.group;
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
     return nq::few_rows(a, x.group) ? nq::launch_attention_small(x) : nq::launch_attention_chunk(x);

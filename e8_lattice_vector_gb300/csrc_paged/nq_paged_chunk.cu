@@ -1,16 +1,17 @@
 // nq_paged_chunk.cu -- attention of many rows per request over the paged cache (prompt chunks, whole prompts).
 //
-// A row tile is 256 rows (tokens times the query heads that share a KV head), two halves of 128.  For each tile of 128
-// keys and each half, on the tensor cores (tcgen05, accumulators in tensor memory):
+// Rows are tokens times the `group` query heads that share a KV head.  A half is as many whole tokens as fit 128 rows, a row
+// tile two halves.  For each tile of 128 keys and each half, on the tensor cores (tcgen05, accumulators in tensor memory):
 //   S = Q K^T                    128 x 128, fp32
 //   P = exp2((S - m) c)          by a warpgroup, a thread per row: no exchange between threads
 //   O = O f + P V                P from tensor memory, where it takes the place of S
 // m is a reference that follows the running maximum only when that has grown by more than 2^8 in P (kSlack): O is
 // rescaled on those few tiles, and on the others the tensor cores add to it undisturbed.  P stays below 2^8, and
-// its sum below 2^31 for any length.
+// its sum below 2^39 for any length.
 //
-// The two halves alternate on the tensor cores: while one half's exponentials are taken, the other half's
-// products run.  One warp loads (TMA, one box per page and 64 columns), one issues the products.
+// The two halves alternate on the tensor cores: while one half's exponentials are taken, the other half's products run.  A
+// row tile with rows for one half only is given to both, each taking every other key tile; the two sums meet
+// in tensor memory.  One warp loads K and V (TMA, one box per page and 64 columns), one loads Q, one issues the products.
 //
 // Shares: the row tiles' key tiles, in order, in equal parts over 152 blocks; a launch of one block finds where each part
 // begins.  Row tiles that end up in several blocks are joined by a second launch.
@@ -55,7 +56,7 @@ struct ChunkPlan {
     int* pair_row_tile;    // [pairs]
 };
 
-inline int64_t chunk_pairs(int64_t tokens, int group, int requests) { return tokens * group / kChunkRows + requests; }
+inline int64_t chunk_pairs(int64_t tokens, int half_tokens, int requests) { return tokens / (2 * half_tokens) + requests; }
 
 inline ChunkPlan chunk_plan(char* p, int64_t pairs, uint64_t* total) {
     ChunkPlan c;
@@ -74,21 +75,23 @@ inline ChunkPlan chunk_plan(char* p, int64_t pairs, uint64_t* total) {
 }
 
 __device__ __forceinline__ int row_tiles_of(const AttnArgs& a, const Request& q) {
-    return (q.n * a.group + kChunkRows - 1) / kChunkRows;
+    return (q.n + 2 * a.half_tokens - 1) / (2 * a.half_tokens);
 }
 
-// The rows and keys of one row tile.
+// The tokens and keys of one row tile.
 struct RowTile {
-    int row0, n_rows, lo, hi;  // keys [lo, hi) are seen by some row
-    int first, count;    // key tiles, at least one so that rows without keys are written too
+    int token0, n, lo, hi;  // n tokens; keys [lo, hi) are seen by some of them
+    int first, count;       // key tiles, at least one so that rows without keys are written too
+    bool shared;            // one half's tokens, for both halves
 };
 __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& a, const Request& q, int row_tile) {
     RowTile t;
-    t.row0 = row_tile * kChunkRows;
-    t.n_rows = min(q.n * a.group - t.row0, kChunkRows);
-    const int base = q.kv - q.n;
-    t.lo = keys_from(a, base + a.by_group.of(t.row0));
-    t.hi = keys_to(a, q.kv, base + a.by_group.of(t.row0 + t.n_rows - 1));
+    t.token0 = row_tile * 2 * a.half_tokens;
+    t.n = min(q.n - t.token0, 2 * a.half_tokens);
+    t.shared = t.n <= a.half_tokens;
+    const int p0 = q.kv - q.n + t.token0;
+    t.lo = keys_from(a, p0);
+    t.hi = keys_to(a, q.kv, p0 + t.n - 1);
     t.first = min(t.lo, t.hi) / kKeyTile;
     t.count = max((t.hi + kKeyTile - 1) / kKeyTile - t.first, 1);
     return t;
@@ -159,21 +162,28 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     __syncthreads();
     const int cost = tiles >= (long long)kCostFrom * kAttnGrid ? kRowTileCost : 0;
     const long long per_pair = (long long)cost * a.kv_heads, units = tiles + per_pair * pairs;
-    for (int b = threadIdx.x; b < kAttnGrid; b += kPlanThreads)
-        if (share_begin(units, b) >= units) plan.start[b] = ChunkStart{0, 0, 0, 0, units, units, units, cost};
-    for (long long p = threadIdx.x; p < pairs; p += kPlanThreads) {
-        const long long from = plan.tile_sum[p] + per_pair * p, to = plan.tile_sum[p + 1] + per_pair * (p + 1);
-        const int count = int((to - from) / a.kv_heads);
-        int b = share_holding(units, from);
-        if (share_begin(units, b) < from) ++b;
-        for (; b < kAttnGrid; ++b) {
-            const long long begin = share_begin(units, b);
-            if (begin >= to) break;
-            const long long at = begin - from;
-            plan.start[b] = ChunkStart{plan.pair_request[p], plan.pair_row_tile[p], int(at / count), int(at % count),
-                                       begin, share_begin(units, b + 1), units, cost};
+    const int b = threadIdx.x;
+    if (b >= kAttnGrid) return;
+    const Shares shares(units);
+    const long long begin = shares.begin(b);
+    ChunkStart start{0, 0, 0, 0, begin, shares.begin(b + 1), units, cost};
+    if (begin < units) {
+        long long lo = 0, hi = pairs;  // the last pair that begins at or before it
+        while (hi - lo > 1) {
+            const long long mid = (lo + hi) >> 1;
+            if (plan.tile_sum[mid] + per_pair * mid <= begin)
+                lo = mid;
+            else
+                hi = mid;
         }
+        const long long from = plan.tile_sum[lo] + per_pair * lo, to = plan.tile_sum[lo + 1] + per_pair * (lo + 1);
+        const int count = int(to - from) / a.kv_heads, at = int(begin - from);
+        start.request = plan.pair_request[lo];
+        start.row_tile = plan.pair_row_tile[lo];
+        start.head = at / count;
+        start.unit = at - start.head * count;
     }
+    plan.start[b] = start;
 }
 
 // ------------------------------------------------------------------- tcgen05
@@ -207,9 +217,12 @@ struct Ring {
     }
 };
 
-// 16 bytes to shared memory, or zeros when bytes = 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Box [tokens of a half][heads of a group][64 columns] of q -> swizzled shared memory.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int head, int token) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(head), "r"(token)
+        : "memory");
 }
 
 // Shared-memory operands, 128-byte swizzle: the low word holds the address and the leading offset, the high word the stride
@@ -314,10 +327,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct ChunkControl {
     uint64_t full[8], empty[8];
     uint64_t clean[kLiveRing];  // per key tile: its V has no values that no row sees
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], drained;
     uint32_t live[kLiveRing];  // per key tile: which of its pages are loaded
     uint32_t tmem;
     int gave_up;
+    float m[128], l[128], to_m[128];  // a shared row tile's second half, for the first
 };
 
 // Walks the pieces of a block's share.
@@ -349,6 +363,17 @@ struct ChunkWalk {
         take = end - cost - tile;
         return take > 0;
     }
+    // Tokens of half h, and its key tiles of the piece: a shared row tile's every other one; else those up to the half's last
+    // key (at least one: its results are written in any case).
+    __device__ __forceinline__ int tokens_of(const AttnArgs& a, int h) const {
+        return t.shared ? t.n : min(t.n - h * a.half_tokens, a.half_tokens);
+    }
+    __device__ __forceinline__ int tiles_of(const AttnArgs& a, int h) const {
+        if (t.shared) return (take + 1 - h) >> 1;
+        if (h == 1) return take;
+        const int hi = keys_to(a, q.kv, q.kv - q.n + t.token0 + a.half_tokens - 1);
+        return min(max((hi + kKeyTile - 1) / kKeyTile - t.first - tile, 1), take);
+    }
     __device__ __forceinline__ void next(const AttnArgs& a) {
         do {
             const int n = int(min((long long)(t.count + cost - unit), left));
@@ -377,7 +402,8 @@ struct ChunkWalk {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreadsChunk, 1)
     attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
-                           const __grid_constant__ CUtensorMap v_map, const AttnWorkspace ws, const ChunkPlan plan) {
+                           const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map,
+                           const AttnWorkspace ws, const ChunkPlan plan) {
     using C = Chunk<D>;
     constexpr int HALVES = C::HALVES, STAGES = C::STAGES;
     extern __shared__ char smem_raw[];
@@ -393,7 +419,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         }
         for (int i = 0; i < kLiveRing; ++i) mbar_init(smem_ptr(&c.clean[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_ptr(&c.q_full[i]), 4);
+            mbar_init(smem_ptr(&c.q_full[i]), 1);
+            mbar_init(smem_ptr(&c.q_free[i]), 1);
             mbar_init(smem_ptr(&c.s_full[i]), 1);
             mbar_init(smem_ptr(&c.p_full[i]), 4);
             mbar_init(smem_ptr(&c.o_full[i]), 1);
@@ -403,6 +430,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         c.gave_up = 0;
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
+        tma_prefetch_map(&q_map);
     }
     if (warp == 9) {  // all 512 columns: one block per multiprocessor
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_ptr(&c.tmem)) : "memory");
@@ -467,7 +495,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 constexpr uint32_t s_idesc = tc_idesc<BF16>(kKeyTile, false), o_idesc = tc_idesc<BF16>(D, true);
                 const uint32_t q_desc = tc_desc(smem_ptr(q_smem), 1), k_desc = tc_desc(smem_ptr(ring), 1);
                 const uint32_t v_desc = tc_desc(smem_ptr(ring), kHalfBytes >> 4);
-                Ring<STAGES> at;
+                Ring<STAGES> k, v;  // of the next K and V; the ring holds K0 V0 K1 V1 ...
+                v.step();
                 Ring<kLiveRing> tile;
                 uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
                 bool go = true;
@@ -475,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     go = go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up);
                     tc_fence_after();
                 };
-                auto scores = [&](int h, int st) {  // S_h = Q_h K^T
+                auto scores = [&](int h, int st, bool last) {  // S_h = Q_h K^T; the last of a piece frees Q
                     uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + st * (C::TILE >> 4);
                     asm volatile("" : "+r"(qd), "+r"(kd));  // the steps are added here, not kept in registers
 #pragma unroll
@@ -484,24 +513,29 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         tc_mma(tmem + h * 128, qd + step, kd + step, s_idesc, k > 0);
                     }
                     tc_commit(smem_ptr(&c.s_full[h]));
+                    if (last) tc_commit(smem_ptr(&c.q_free[h]));
                 };
-                while (go && w.left > 0) {
-                    const int take = w.take, halves = w.t.n_rows > 128 ? 2 : 1;
-                    await(c.full[at.stage], at.phase);
-                    for (int h = 0; h < halves; ++h) {
-                        await(c.q_full[h], q_phase[h]);
-                        q_phase[h] ^= 1;
-                        if (go) scores(h, at.stage);
+                for (; go && w.left > 0; w.next(a)) {
+                    const int take = w.take, count[2] = {w.tiles_of(a, 0), w.tiles_of(a, 1)};
+                    const int ahead = w.t.shared ? 2 : 1;  // key tiles between a half's products
+                    for (int i = 0; go && i < ahead && i < take; ++i) {
+                        await(c.full[k.stage], k.phase);
+                        for (int h = w.t.shared ? i : 0; h < (w.t.shared ? i + 1 : 2); ++h) {
+                            await(c.q_full[h], q_phase[h]);
+                            q_phase[h] ^= 1;
+                            if (go) scores(h, k.stage, count[h] == 1);
+                        }
+                        if (go) tc_commit(smem_ptr(&c.empty[k.stage]));
+                        k.step();
+                        k.step();
                     }
-                    if (go) tc_commit(smem_ptr(&c.empty[at.stage]));
-                    at.step();
-                    for (int i = 0; go && i < take; ++i, tile.step()) {
-                        const Ring<STAGES> v = at;
-                        at.step();
-                        const bool more = i + 1 < take;
+                    for (int i = 0; go && i < take; ++i, tile.step(), v.step(), v.step()) {
+                        const bool more = i + ahead < take;
                         await(c.clean[tile.stage], tile.phase);
-                        if (more) await(c.full[at.stage], at.phase);
-                        for (int h = 0; h < halves; ++h) {
+                        if (more) await(c.full[k.stage], k.phase);
+                        for (int h = w.t.shared ? i & 1 : 0; h < (w.t.shared ? (i & 1) + 1 : 2); ++h) {
+                            const int at = w.t.shared ? i >> 1 : i;  // of this half's tiles
+                            if (at >= count[h]) continue;
                             await(c.p_full[h], p_phase[h]);
                             p_phase[h] ^= 1;
                             if (!go) break;
@@ -510,20 +544,20 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                             asm volatile("" : "+r"(vd));
                             const uint32_t o = tmem + 256 + h * 128, p = tmem + h * 128;
 #pragma unroll
-                            for (int k = 0; k < kKeyTile / 16; ++k) {
-                                tc_mma_ta(o, p + 8 * k, vd + 128 * k, o_idesc, i > 0 || k > 0);
-                                if constexpr (BF16) tc_mma_ta(o, p + 64 + 8 * k, vd + 128 * k, o_idesc, true);
+                            for (int x = 0; x < kKeyTile / 16; ++x) {
+                                tc_mma_ta(o, p + 8 * x, vd + 128 * x, o_idesc, at > 0 || x > 0);
+                                if constexpr (BF16) tc_mma_ta(o, p + 64 + 8 * x, vd + 128 * x, o_idesc, true);
                             }
                             tc_commit(smem_ptr(&c.o_full[h]));
-                            if (more) scores(h, at.stage);
+                            if (at + 1 < count[h]) scores(h, k.stage, at + 2 == count[h]);
                         }
                         if (go) tc_commit(smem_ptr(&c.empty[v.stage]));
                         if (more) {
-                            if (go) tc_commit(smem_ptr(&c.empty[at.stage]));
-                            at.step();
+                            if (go) tc_commit(smem_ptr(&c.empty[k.stage]));
+                            k.step();
+                            k.step();
                         }
                     }
-                    w.next(a);
                 }
                 // no product is in flight when tensor memory is freed
                 int late = 0;
@@ -563,14 +597,32 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 }
             }
         } else if (lane == 0) {
-            // -------- the row tile that this block begins and does not end
+            // ------------------ Q, and the row tile that this block begins and does not end
             AttnSplit split{0, 0, 0, -1};
-            for (; w.left > 0; w.next(a)) {
-                const int take = w.take;
-                if (w.tile == 0 && take < w.t.count)  // the last piece
+            uint32_t pieces[2] = {0, 0};
+            bool go = true;
+            for (; go && w.left > 0; w.next(a)) {
+                if (w.tile == 0 && w.take < w.t.count)  // the last piece
                     split = AttnSplit{w.r, w.row_tile, w.head,
-                                      share_holding(start.total, start.end - 1 + (w.t.count - take))};
+                                      share_holding(start.total, start.end - 1 + (w.t.count - w.take))};
+                for (int h = 0; h < 2; ++h) {
+                    if (w.tiles_of(a, h) == 0) break;
+                    // As soon as the piece's last scores are there its Q is not read any more: the next one's loads run beside
+                    // the last tile's exponentials, its product and the results.
+                    if (pieces[h] > 0) go = go && mbar_wait(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up);
+                    if (!go) break;
+                    ++pieces[h];
+                    const uint32_t full = smem_ptr(&c.q_full[h]);
+                    mbar_arrive_tx(full, uint32_t(HALVES * a.half_tokens * a.group) * 128u);
+                    for (int x = 0; x < HALVES; ++x)
+                        tma_load_rows(smem_ptr(q_smem + h * C::TILE + x * kHalfBytes), &q_map, full, 64 * x, w.head * a.group,
+                                      w.q.begin + w.t.token0 + (w.t.shared ? 0 : h * a.half_tokens));
+                }
             }
+            int late = 0;
+            for (int h = 0; h < 2; ++h)
+                if (pieces[h] > 0) mbar_wait(smem_ptr(&c.q_full[h]), (pieces[h] - 1) & 1, &late);
+            if (late) *(volatile int*)&c.gave_up = 1;
             ws.split[blockIdx.x] = split;
         }
     } else {
@@ -585,59 +637,31 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             __syncwarp();
             tc_fence_after();
         };
-        // Q of a piece into this half's place: 16 copies a thread, a row's pieces on neighbouring threads
-        auto load_q = [&](const ChunkWalk& x) {
-            constexpr int PER = HALVES * 8, STEP = 128 / PER;
-            const int n_rows = min(x.t.n_rows - h * 128, 128), row0 = x.t.row0 + h * 128, ch = row % PER;
-            const uint16_t* q = static_cast<const uint16_t*>(a.q) + int64_t(x.q.begin) * a.q_token_stride + ch * 8;
-            const uint32_t dst = smem_ptr(q_smem + h * C::TILE + (ch >> 3) * kHalfBytes);
-            if (8 * ch < D) {
-#pragma unroll
-                for (int rr = row / PER; rr < 128; rr += STEP) {
-                    const int gi = row0 + min(rr, n_rows - 1), t = a.by_group.of(gi), hd = x.head * a.group + gi - t * a.group;
-                    copy16(dst + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4), q + t * a.q_token_stride + hd * a.q_head_stride,
-                           rr < n_rows ? 16 : 0);
-                }
-            }
-        };
-        auto q_loaded = [&] {
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_ptr(&c.q_full[h]));
-        };
-        int n_s = 0;      // tiles of this half so far
-        int tiles = 0;    // tiles of the block so far
-        bool loading = false;  // loading: this piece's Q is on its way
-        ChunkWalk ahead;
-        for (; w.left > 0; w = ahead) {
-            const int take = w.take;
-            const bool whole = w.tile == 0 && take == w.t.count;
-            ahead = w;
-            ahead.next(a);
-            const int n_rows = min(w.t.n_rows - h * 128, 128);
-            if (n_rows <= 0) {  // the product warp skips this half too
-                tiles += take;
-                continue;
-            }
-            if (!loading) load_q(w);
-            q_loaded();
-            const int row0 = w.t.row0 + h * 128, base = w.q.kv - w.q.n;
-            const int gi = row0 + min(row, n_rows - 1), token = a.by_group.of(gi), head = w.head * a.group + gi - token * a.group;
+        const int row_token = a.by_group.of(row), row_head = row - row_token * a.group;
+        int n_s = 0;    // tiles of this half so far
+        int tiles = 0;  // tiles of the block before this piece
+        for (; w.left > 0; tiles += w.take, w.next(a)) {
+            const int count = w.tiles_of(a, h);
+            if (w.t.shared && count == 0) continue;
+            const bool whole = w.tile == 0 && w.take == w.t.count;
+            const int n_tokens = w.tokens_of(a, h), token0 = w.t.token0 + (w.t.shared ? 0 : h * a.half_tokens);
+            const bool mine = row_token < n_tokens;
+            const int token = token0 + min(row_token, n_tokens - 1), head = w.head * a.group + row_head;
+            const int base = w.q.kv - w.q.n;
             const int lo = keys_from(a, base + token), hi = keys_to(a, w.q.kv, base + token);
             // keys [all_lo, all_hi) are seen by every row of the half
-            const int all_lo = keys_from(a, base + a.by_group.of(row0 + n_rows - 1));
-            const int all_hi = keys_to(a, w.q.kv, base + a.by_group.of(row0));
+            const int all_lo = keys_from(a, base + token0 + n_tokens - 1), all_hi = keys_to(a, w.q.kv, base + token0);
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
             // p = 2^(s sc + neg).  The reference is the fp32 number nearest to m sc, and rest = m sc - reference (exact); a
             // huge one (far) would leave no digits for the difference, there s - m is taken first and the reference is m sc.
             float m = -INFINITY, l = 0.0f, neg = 0.0f, rest = 0.0f;
             bool far = false;
-            for (int i = 0; i < take; ++i, ++n_s, ++tiles) {
+            for (int j = 0; j < count; ++j, ++n_s) {
+                const int i = w.t.shared ? 2 * j + h : j;  // of the piece's tiles
                 const int key0 = (w.t.first + w.tile + i) * kKeyTile;
                 wait(c.s_full[h], n_s & 1);
-                const uint32_t live = *(volatile uint32_t*)&c.live[tiles % kLiveRing];
+                const uint32_t live = *(volatile uint32_t*)&c.live[(tiles + i) % kLiveRing];
                 float s[kKeyTile];
                 float tops[4];  // four chains: one would be all latency
 #pragma unroll
@@ -727,41 +751,73 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
 
             // ------------------------------------------------------- results
-            // The last scores have been read, and with them Q for the last time: the next piece's Q loads meanwhile.
-            loading = ahead.left > 0 && ahead.t.n_rows > h * 128;
-            if (loading) load_q(ahead);
             wait(c.o_full[h], (n_s - 1) & 1);
-            const bool mine = row < n_rows;
-            const float to_m = exp2_fast(-rest);  // from the reference to m
+            float to_m = exp2_fast(-rest);  // from the reference to m
             l *= to_m;
-            const float inv = whole ? (l > 0.0f ? to_m / l : 0.0f) : to_m;
+            const bool both = w.t.shared && w.take > 1;
+            float to_other = 0.0f;  // the other half's part in the result
+            if (both) {
+                if (h == 1) {
+                    c.m[row] = m;
+                    c.l[row] = l;
+                    c.to_m[row] = to_m;
+                    tc_fence_before();
+                    named_barrier<1, 256>();
+                    named_barrier<2, 256>();  // the first half has read O
+                    continue;
+                }
+                named_barrier<1, 256>();
+                tc_fence_after();
+                const float m1 = c.m[row], top = fmaxf(m, m1);
+                const float f0 = m == -INFINITY ? 0.0f : exp2_fast((m - top) * sc);
+                const float f1 = m1 == -INFINITY ? 0.0f : exp2_fast((m1 - top) * sc);
+                l = l * f0 + c.l[row] * f1;
+                to_m *= f0;
+                to_other = c.to_m[row] * f1;
+                m = top;
+            }
+            if (whole) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                to_m *= inv;
+                to_other *= inv;
+            }
             const int64_t at = int64_t(2 * blockIdx.x + (w.tile > 0 ? 0 : 1)) * kChunkRows + h * 128 + row;
             uint16_t* out = static_cast<uint16_t*>(a.out) + (w.q.begin + token) * a.out_token_stride + head * a.out_head_stride;
-            float o[D];
 #pragma unroll
-            for (int x = 0; x < D; x += 32) tm_load(o + x, o_at + x);
-            tm_wait<D>(o);
+            for (int x0 = 0; x0 < D; x0 += 32) {
+                float o[32];
+                tm_load(o, o_at + x0);
+                tm_wait<32>(o);
 #pragma unroll
-            for (int x = 0; x < D; ++x) o[x] *= inv;
-            if (mine && whole) {
+                for (int x = 0; x < 32; ++x) o[x] *= to_m;
+                if (both) {
+                    float o1[32];
+                    tm_load(o1, o_at + 128 + x0);
+                    tm_wait<32>(o1);
 #pragma unroll
-                for (int x = 0; x < D; x += 16) {
-                    uint32_t p[8];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) p[y] = pack2<BF16>(o[x + 2 * y], o[x + 2 * y + 1]);
-                    if (a.out_by_32) {
-                        store32(out + x, p);
-                    } else {
-                        *reinterpret_cast<uint4*>(out + x) = make_uint4(p[0], p[1], p[2], p[3]);
-                        *reinterpret_cast<uint4*>(out + x + 8) = make_uint4(p[4], p[5], p[6], p[7]);
-                    }
+                    for (int x = 0; x < 32; ++x) o[x] = __fmaf_rn(o1[x], to_other, o[x]);
                 }
-            } else if (mine) {
+                if (mine && whole) {
 #pragma unroll
-                for (int x = 0; x < D; x += 8) store32(ws.o + at * D + x, reinterpret_cast<const uint32_t*>(o + x));
+                    for (int x = 0; x < 32; x += 16) {
+                        uint32_t p[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) p[y] = pack2<BF16>(o[x + 2 * y], o[x + 2 * y + 1]);
+                        if (a.out_by_32) {
+                            store32(out + x0 + x, p);
+                        } else {
+                            *reinterpret_cast<uint4*>(out + x0 + x) = make_uint4(p[0], p[1], p[2], p[3]);
+                            *reinterpret_cast<uint4*>(out + x0 + x + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+                        }
+                    }
+                } else if (mine) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8) store32(ws.o + at * D + x0 + x, reinterpret_cast<const uint32_t*>(o + x));
+                }
+                __syncwarp();
             }
-            __syncwarp();
             tc_fence_before();
+            if (both) named_barrier<2, 256>();
             if (mine) {
                 if (!whole)
                     ws.ml[at] = make_float2(m, l);
@@ -779,8 +835,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 }
 
 template <int D, bool BF16>
-int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const AttnWorkspace& ws,
-                 const ChunkPlan& plan) {
+int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
+                 const AttnWorkspace& ws, const ChunkPlan& plan) {
     if (!ensure_smem(reinterpret_cast<const void*>(attention_chunk_kernel<D, BF16>), Chunk<D>::SMEM)) return NQ_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -792,16 +848,16 @@ int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm
     cfg.stream = a.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_chunk_kernel<D, BF16>, a, km, vm, ws, plan) == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, attention_chunk_kernel<D, BF16>, a, km, vm, qm, ws, plan) == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
 template <bool BF16>
-int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const AttnWorkspace& ws,
-                 const ChunkPlan& plan) {
+int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
+                 const AttnWorkspace& ws, const ChunkPlan& plan) {
     switch (a.head_dim) {
-        case 64: return launch_chunk<64, BF16>(a, km, vm, ws, plan);
-        case 96: return launch_chunk<96, BF16>(a, km, vm, ws, plan);
-        default: return launch_chunk<128, BF16>(a, km, vm, ws, plan);
+        case 64: return launch_chunk<64, BF16>(a, km, vm, qm, ws, plan);
+        case 96: return launch_chunk<96, BF16>(a, km, vm, qm, ws, plan);
+        default: return launch_chunk<128, BF16>(a, km, vm, qm, ws, plan);
     }
 }
 
@@ -809,21 +865,21 @@ int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm
 
 uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim) {
     uint64_t bytes = 0;
-    chunk_plan(nullptr, chunk_pairs(tokens, group, requests), &bytes);
+    chunk_plan(nullptr, chunk_pairs(tokens, 128 / group, requests), &bytes);
     return attn_workspace(nullptr, kChunkRows, head_dim).total + bytes;
 }
 
 int launch_attention_chunk(const AttnArgs& a) {
-    CUtensorMap km, vm;
-    if (!make_pool_maps(a, &km, &vm)) return NQ_ERR_CUDA;
+    CUtensorMap km, vm, qm;
+    if (!make_pool_maps(a, &km, &vm) || !make_query_map(a, &qm)) return NQ_ERR_CUDA;
     const AttnWorkspace ws = attn_workspace(a.workspace, kChunkRows, a.head_dim);
     uint64_t bytes = 0;
-    const int64_t pairs = chunk_pairs(a.tokens, a.group, a.requests);
+    const int64_t pairs = chunk_pairs(a.tokens, a.half_tokens, a.requests);
     const ChunkPlan plan = chunk_plan(static_cast<char*>(a.workspace) + ws.total, pairs, &bytes);
     attention_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a, plan, pairs);
     if (cudaGetLastError() != cudaSuccess) return NQ_ERR_CUDA;
-    const int st = a.bf16 ? launch_chunk<true>(a, km, vm, ws, plan) : launch_chunk<false>(a, km, vm, ws, plan);
-    return st == NQ_OK ? launch_attention_join(a, kChunkRows) : st;
+    const int st = a.bf16 ? launch_chunk<true>(a, km, vm, qm, ws, plan) : launch_chunk<false>(a, km, vm, qm, ws, plan);
+    return st == NQ_OK ? launch_attention_join(a, kChunkRows, 2 * a.half_tokens * a.group, a.half_tokens * a.group) : st;
 }
 
 int chunk_gave_up(int* seen) {

@@ -121,23 +121,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // -------------------------------------------------------------------- shares
 
-// The first of block b's tiles: `total` tiles over the first min(total, kAttnGrid) blocks, sizes differing by one.
-__device__ __forceinline__ long long share_begin(long long total, int b) {
-    const long long parts = min(total, (long long)kAttnGrid);
-    if (b >= parts) return total;
-    return total / parts * b + total % parts * b / parts;
-}
-// The block whose share holds tile `at` (< total).
-__device__ __forceinline__ int share_holding(long long total, long long at) {
-    int lo = 0, hi = kAttnGrid - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (share_begin(total, mid + 1) > at)
-            hi = mid;
-        else
-            lo = mid + 1;
+// `total` tiles over the first min(total, kAttnGrid) blocks, sizes differing by one: block b's begin at
+// floor(total b / parts).
+struct Shares {
+    long long total, each;
+    uint32_t parts, more;  // total = each * parts + more
+    __device__ __forceinline__ explicit Shares(long long t) : total(t) {
+        parts = uint32_t(min(max(t, 1LL), (long long)kAttnGrid));
+        each = t / parts;
+        more = uint32_t(t - each * parts);
     }
-    return lo;
+    __device__ __forceinline__ long long begin(uint32_t b) const {
+        return b >= parts ? total : each * b + more * b / parts;
+    }
+};
+// The block whose share holds tile `at` (< total): the last b with total b / parts < at + 1.
+__device__ __forceinline__ int share_holding(long long total, long long at) {
+    const long long parts = min(total, (long long)kAttnGrid);
+    return int(((at + 1) * parts - 1) / total);
 }
 
 // ------------------------------------------------------------------- lengths

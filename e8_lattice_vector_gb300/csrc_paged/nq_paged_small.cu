@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
         if (w < warp) before += c.warp_sum[w];
         total += c.warp_sum[w];
     }
-    const long long pos = share_begin(total, blockIdx.x), end = share_begin(total, blockIdx.x + 1);
+    const Shares shares(total);
+    const long long pos = shares.begin(blockIdx.x), end = shares.begin(blockIdx.x + 1);
     if (pos < end && pos >= before && pos < before + mine) {
         long long at = pos - before;
         int r = r0;
@@ -485,7 +486,7 @@ int launch_attention_small(const AttnArgs& a) {
     if (!make_pool_maps(a, &km, &vm)) return NQ_ERR_CUDA;
     const AttnWorkspace ws = attn_workspace(a.workspace, kSmallRows, a.head_dim);
     const int st = a.bf16 ? launch_small<true>(a, km, vm, ws) : launch_small<false>(a, km, vm, ws);
-    return st == NQ_OK ? launch_attention_join(a, kSmallRows) : st;
+    return st == NQ_OK ? launch_attention_join(a, kSmallRows, kSmallRows, kSmallRows) : st;
 }
 
 int small_gave_up(int* seen) {
