@@ -93,7 +93,7 @@ struct AttnSplit {  // per block: the row tile that it began and did not end, or
 struct AttnWorkspace {
     AttnSplit* split;  // [kAttnGrid]
     float2* ml;        // [kAttnGrid * 2][rows]: running maximum (unscaled score), sum
-    float* o;          // [kAttnGrid * 2][rows][head_dim]
+    float* o;          // [kAttnGrid * 2][rows][head_dim]; the large kernel: [kAttnGrid * 4][head_dim / 8][128][8]
     uint64_t total;
 };
 

@@ -35,6 +35,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const int row = min(first + warp / SPREAD, n_rows - 1);
         const int half = row >= half_rows, slot_row = half * 128 + row - half * half_rows;
         auto at = [&](int i) { return int64_t(i == 0 ? 2 * b + 1 : 2 * (b + i)) * slot_rows + slot_row; };
+        // the large kernel's rows are stored 8 columns of a half's 128 rows together
+        auto o_at = [&](int i) {
+            if constexpr (SPREAD > 1) return at(i) * D + 4 * lane;
+            return (at(i) - (slot_row & 127)) * D + (lane >> 1) * 1024 + (slot_row & 127) * 8 + 4 * (lane & 1);
+        };
         float top = -INFINITY, sum = 0.0f;
         for (int i = lane; i < pieces; i += 32) top = fmaxf(top, ws.ml[at(i)].x);
 #pragma unroll
@@ -50,7 +55,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 #pragma unroll 4
             for (int i = share; i < pieces; i += SPREAD) {
                 const float m = ws.ml[at(i)].x;
-                const float4 o = *reinterpret_cast<const float4*>(ws.o + at(i) * D + 4 * lane);
+                const float4 o = *reinterpret_cast<const float4*>(ws.o + o_at(i));
                 const float f = m == -INFINITY ? 0.0f : exp2_fast((m - top) * sc);
                 acc.x = fmaf(o.x, f, acc.x);
                 acc.y = fmaf(o.y, f, acc.y);

@@ -290,6 +290,12 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* u) {
         : "memory");
 }
 
+// m sc - the reference taken for it (exact).
+__device__ __forceinline__ float beyond_reference(float m, float sc) {
+    const float scaled = m * sc;
+    return fabsf(scaled) > kExactRef ? 0.0f : __fmaf_rn(m, sc, -scaled);
+}
+
 // 32 bytes to a 32-byte boundary.
 __device__ __forceinline__ void store32(void* dst, const uint32_t* u) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
@@ -324,15 +330,33 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // -------------------------------------------------------------------- kernel
 
+constexpr int kPieceRing = 4;
+
+// One piece of a block's share: key tiles [key0 / 128, + take) of one row tile and KV head.
+struct __align__(16) Piece {
+    int take;           // 0: no more pieces
+    int count[2];       // tiles of each half: every other one when shared; else those up to the half's last key
+    int shared;         // one half's tokens, for both halves
+    int row, n, pos;    // first token's row in q, tokens, position of the first
+    int kv, key0, lo, hi;
+    int head, request;
+    int slot;           // workspace slot for the results, -1: the piece is the whole row tile
+    int pad[2];
+};
+
 struct ChunkControl {
     uint64_t full[8], empty[8];
     uint64_t clean[kLiveRing];  // per key tile: its V has no values that no row sees
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t piece_full[kPieceRing], piece_free[kPieceRing];
+    uint64_t merge_full, merge_free;
+    Piece piece[kPieceRing];
     uint32_t live[kLiveRing];  // per key tile: which of its pages are loaded
     uint32_t tmem;
     int gave_up;
-    float m[128], l[128], to_m[128];  // a shared row tile's second half, for the first
+    float m[128], l[128];  // a shared row tile's second half, for the first
 };
+constexpr int kPieceReaders = 11;  // eight softmax warps, loads, products, clearing
 
 // Walks the pieces of a block's share.
 struct ChunkWalk {
@@ -363,11 +387,7 @@ struct ChunkWalk {
         take = end - cost - tile;
         return take > 0;
     }
-    // Tokens of half h, and its key tiles of the piece: a shared row tile's every other one; else those up to the half's last
-    // key (at least one: its results are written in any case).
-    __device__ __forceinline__ int tokens_of(const AttnArgs& a, int h) const {
-        return t.shared ? t.n : min(t.n - h * a.half_tokens, a.half_tokens);
-    }
+    // Half h's key tiles of the piece (at least one unless shared: its results are written in any case).
     __device__ __forceinline__ int tiles_of(const AttnArgs& a, int h) const {
         if (t.shared) return (take + 1 - h) >> 1;
         if (h == 1) return take;
@@ -425,6 +445,12 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             mbar_init(smem_ptr(&c.p_full[i]), 4);
             mbar_init(smem_ptr(&c.o_full[i]), 1);
         }
+        for (int i = 0; i < kPieceRing; ++i) {
+            mbar_init(smem_ptr(&c.piece_full[i]), 1);
+            mbar_init(smem_ptr(&c.piece_free[i]), kPieceReaders);
+        }
+        mbar_init(smem_ptr(&c.merge_full), 4);
+        mbar_init(smem_ptr(&c.merge_free), 4);
         mbar_init(smem_ptr(&c.drained), 1);
         mbar_init_fence();
         c.gave_up = 0;
@@ -442,9 +468,22 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&c.tmem);
     pdl_wait();  // the plan is written
-    const ChunkStart start = plan.start[blockIdx.x];
-    ChunkWalk w;
-    w.begin(a, start);
+
+    // The next piece, for a whole warp or one thread; false at the end, or when a wait was given up.
+    auto next_piece = [&](Ring<kPieceRing>& at, Piece& p, bool one_thread) {
+        bool ok = mbar_wait(smem_ptr(&c.piece_full[at.stage]), at.phase, &c.gave_up);
+        if (!one_thread) ok = __all_sync(0xffffffffu, ok);
+        const int4* src = reinterpret_cast<const int4*>(&c.piece[at.stage]);
+        int4* dst = reinterpret_cast<int4*>(&p);
+#pragma unroll
+        for (int i = 0; i < int(sizeof(Piece) / 16); ++i) dst[i] = src[i];
+        if (!one_thread) __syncwarp();
+        if (one_thread || lane == 0) mbar_arrive(smem_ptr(&c.piece_free[at.stage]));
+        at.step();
+        return ok && p.take > 0;
+    };
+    Ring<kPieceRing> piece_at;
+    Piece w;
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -452,34 +491,38 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // -------------------------------------------------------- loads
             const int ppt = max(kKeyTile >> a.page_shift, 1), rows = min(1 << a.page_shift, kKeyTile);
             const int pg = lane % ppt, half = lane / ppt;  // a lane for each page and 64 columns
+            Ring<STAGES> at;
             int n = 0, tiles = 0;
             bool go = true;
-            while (go && w.left > 0) {
-                const int take = w.take;
-                for (int i = 0; go && i < take; ++i, ++tiles) {
-                    const int k0 = (w.t.first + w.tile + i) * kKeyTile + (pg << a.page_shift);
-                    int page = -1;
-                    if (half < HALVES && k0 < w.t.hi && k0 + rows > w.t.lo)
-                        page = a.table[w.r * a.table_stride + (k0 >> a.page_shift)];
+            while (go && next_piece(piece_at, w, false)) {
+                const int32_t* table = a.table + w.request * a.table_stride;
+                auto page_of = [&](int i) {  // this lane's page of tile i, -1: none
+                    const int k0 = w.key0 + i * kKeyTile + (pg << a.page_shift);
+                    return half < HALVES && i < w.take && k0 < w.hi && k0 + rows > w.lo ? table[k0 >> a.page_shift] : -1;
+                };
+                int page = page_of(0);
+                for (int i = 0; go && i < w.take; ++i, ++tiles) {
+                    const int next = page_of(i + 1);  // on its way while this tile waits for room
+                    const int slot0 = (w.key0 + i * kKeyTile + (pg << a.page_shift)) & ((1 << a.page_shift) - 1);
                     const bool load = page >= 0 && page < a.pages;
                     const uint32_t mask = __ballot_sync(0xffffffffu, load && half == 0);
-                    for (int is_v = 0; is_v < 2; ++is_v, ++n) {
-                        const int st = n % STAGES;
+#pragma unroll 1
+                    for (int is_v = 0; is_v < 2; ++is_v, ++n, at.step()) {
                         if (n >= STAGES)
-                            go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.empty[st]), (n / STAGES - 1) & 1, &c.gave_up));
+                            go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.empty[at.stage]), at.phase ^ 1, &c.gave_up));
                         if (!go) break;
-                        const uint32_t full = smem_ptr(&c.full[st]);
+                        const uint32_t full = smem_ptr(&c.full[at.stage]);
                         if (lane == 0) {
                             if (!is_v) *(volatile uint32_t*)&c.live[tiles % kLiveRing] = mask;
                             mbar_arrive_tx(full, uint32_t(__popc(mask)) * uint32_t(rows) * 128u * HALVES);
                         }
                         __syncwarp();
                         if (load)
-                            tma_load_box(smem_ptr(ring + st * C::TILE + half * kHalfBytes + pg * rows * 128),
-                                         is_v ? &v_map : &k_map, full, half * 64, k0 & ((1 << a.page_shift) - 1), w.head, page);
+                            tma_load_box(smem_ptr(ring + at.stage * C::TILE + half * kHalfBytes + pg * rows * 128),
+                                         is_v ? &v_map : &k_map, full, half * 64, slot0, w.head, page);
                     }
+                    page = next;
                 }
-                w.next(a);
             }
             // no copy is left in flight when the block ends, after a wait that was given up too
             if (lane == 0) {
@@ -490,7 +533,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
         } else if (warp == 9) {
             // ----------------------------------------------------- products
-            // One thread, so that nothing between two products waits for a warp.
+            // One thread, so that nothing between two products waits for a warp, and one loop with each product in one place: the
+            // code that it runs between two pieces would otherwise come from beyond the instruction caches, which the
+            // softmax warps keep for themselves (7000 cycles a piece instead of 1000).
             if (elect_one()) {
                 constexpr uint32_t s_idesc = tc_idesc<BF16>(kKeyTile, false), o_idesc = tc_idesc<BF16>(D, true);
                 const uint32_t q_desc = tc_desc(smem_ptr(q_smem), 1), k_desc = tc_desc(smem_ptr(ring), 1);
@@ -504,54 +549,54 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     go = go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up);
                     tc_fence_after();
                 };
-                auto scores = [&](int h, int st, bool last) {  // S_h = Q_h K^T; the last of a piece frees Q
-                    uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + st * (C::TILE >> 4);
-                    asm volatile("" : "+r"(qd), "+r"(kd));  // the steps are added here, not kept in registers
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t step = (k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2;
-                        tc_mma(tmem + h * 128, qd + step, kd + step, s_idesc, k > 0);
-                    }
-                    tc_commit(smem_ptr(&c.s_full[h]));
-                    if (last) tc_commit(smem_ptr(&c.q_free[h]));
-                };
-                for (; go && w.left > 0; w.next(a)) {
-                    const int take = w.take, count[2] = {w.tiles_of(a, 0), w.tiles_of(a, 1)};
-                    const int ahead = w.t.shared ? 2 : 1;  // key tiles between a half's products
-                    for (int i = 0; go && i < ahead && i < take; ++i) {
-                        await(c.full[k.stage], k.phase);
-                        for (int h = w.t.shared ? i : 0; h < (w.t.shared ? i + 1 : 2); ++h) {
-                            await(c.q_full[h], q_phase[h]);
-                            q_phase[h] ^= 1;
-                            if (go) scores(h, k.stage, count[h] == 1);
-                        }
-                        if (go) tc_commit(smem_ptr(&c.empty[k.stage]));
-                        k.step();
-                        k.step();
-                    }
-                    for (int i = 0; go && i < take; ++i, tile.step(), v.step(), v.step()) {
-                        const bool more = i + ahead < take;
-                        await(c.clean[tile.stage], tile.phase);
+                while (go && next_piece(piece_at, w, true)) {
+                    const int ahead = w.shared ? 2 : 1;  // key tiles between a half's products
+#pragma unroll 1
+                    for (int i = -ahead; go && i < w.take; ++i) {  // the product with V of tile i, the scores of tile i + ahead
+                        const bool more = i + ahead < w.take;
                         if (more) await(c.full[k.stage], k.phase);
-                        for (int h = w.t.shared ? i & 1 : 0; h < (w.t.shared ? (i & 1) + 1 : 2); ++h) {
-                            const int at = w.t.shared ? i >> 1 : i;  // of this half's tiles
-                            if (at >= count[h]) continue;
-                            await(c.p_full[h], p_phase[h]);
-                            p_phase[h] ^= 1;
-                            if (!go) break;
-                            // O_h += P_h V
-                            uint32_t vd = v_desc + v.stage * (C::TILE >> 4);
-                            asm volatile("" : "+r"(vd));
-                            const uint32_t o = tmem + 256 + h * 128, p = tmem + h * 128;
+                        if (i >= 0) await(c.clean[tile.stage], tile.phase);
+#pragma unroll 1
+                        for (int h = w.shared ? i & 1 : 0; go && h < (w.shared ? (i & 1) + 1 : 2); ++h) {
+                            const int count = h ? w.count[1] : w.count[0];
+                            const int of_v = w.shared ? i >> 1 : i, of_k = w.shared ? (i + 2) >> 1 : i + 1;  // of the half's tiles
+                            const uint32_t p = tmem + h * 128;
+                            if (i >= 0 && of_v < count) {  // O_h += P_h V
+                                await(c.p_full[h], h ? p_phase[1] : p_phase[0]);
+                                (h ? p_phase[1] : p_phase[0]) ^= 1;
+                                if (!go) break;
+                                uint32_t vd = v_desc + v.stage * (C::TILE >> 4);
+                                asm volatile("" : "+r"(vd));  // the steps are added here, not kept in registers
 #pragma unroll
-                            for (int x = 0; x < kKeyTile / 16; ++x) {
-                                tc_mma_ta(o, p + 8 * x, vd + 128 * x, o_idesc, at > 0 || x > 0);
-                                if constexpr (BF16) tc_mma_ta(o, p + 64 + 8 * x, vd + 128 * x, o_idesc, true);
+                                for (int x = 0; x < kKeyTile / 16; ++x) {
+                                    tc_mma_ta(p + 256, p + 8 * x, vd + 128 * x, o_idesc, of_v > 0 || x > 0);
+                                    if constexpr (BF16) tc_mma_ta(p + 256, p + 64 + 8 * x, vd + 128 * x, o_idesc, true);
+                                }
+                                tc_commit(smem_ptr(&c.o_full[h]));
                             }
-                            tc_commit(smem_ptr(&c.o_full[h]));
-                            if (at + 1 < count[h]) scores(h, k.stage, at + 2 == count[h]);
+                            if (more && of_k < count) {  // S_h = Q_h K^T; the last of a piece frees Q
+                                if (of_k == 0) {
+                                    await(c.q_full[h], h ? q_phase[1] : q_phase[0]);
+                                    (h ? q_phase[1] : q_phase[0]) ^= 1;
+                                    if (!go) break;
+                                }
+                                uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + k.stage * (C::TILE >> 4);
+                                asm volatile("" : "+r"(qd), "+r"(kd));
+#pragma unroll
+                                for (int x = 0; x < D / 16; ++x) {
+                                    const uint32_t step = (x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2;
+                                    tc_mma(p, qd + step, kd + step, s_idesc, x > 0);
+                                }
+                                tc_commit(smem_ptr(&c.s_full[h]));
+                                if (of_k + 1 == count) tc_commit(smem_ptr(&c.q_free[h]));
+                            }
                         }
-                        if (go) tc_commit(smem_ptr(&c.empty[v.stage]));
+                        if (i >= 0) {
+                            if (go) tc_commit(smem_ptr(&c.empty[v.stage]));
+                            v.step();
+                            v.step();
+                            tile.step();
+                        }
                         if (more) {
                             if (go) tc_commit(smem_ptr(&c.empty[k.stage]));
                             k.step();
@@ -574,17 +619,16 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
             bool go = true;
-            for (; go && w.left > 0; w.next(a)) {
-                const int take = w.take;
-                for (int i = 0; go && i < take; ++i, tile.step()) {
+            while (go && next_piece(piece_at, w, false)) {
+                for (int i = 0; go && i < w.take; ++i, tile.step()) {
                     at.step();  // past K
                     go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.full[at.stage]), at.phase, &c.gave_up));
-                    const int key0 = (w.t.first + w.tile + i) * kKeyTile;
+                    const int key0 = w.key0 + i * kKeyTile;
                     const uint32_t live = *(volatile uint32_t*)&c.live[tile.stage];
-                    if (key0 < w.t.lo || key0 + kKeyTile > w.t.hi || live != all) {
+                    if (key0 < w.lo || key0 + kKeyTile > w.hi || live != all) {
                         for (int r0 = 0; r0 < kKeyTile; r0 += 2) {
                             const int r = r0 + (lane >> 4), half = (lane >> 3) & 1;
-                            const bool seen = key0 + r >= w.t.lo && key0 + r < w.t.hi && (live >> (r >> a.page_shift) & 1u);
+                            const bool seen = key0 + r >= w.lo && key0 + r < w.hi && (live >> (r >> a.page_shift) & 1u);
                             if (!seen && half < HALVES)
                                 *reinterpret_cast<uint4*>(ring + at.stage * C::TILE + half * kHalfBytes + r * 128 + (lane & 7) * 16) =
                                     make_uint4(0, 0, 0, 0);
@@ -597,16 +641,45 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 }
             }
         } else if (lane == 0) {
-            // ------------------ Q, and the row tile that this block begins and does not end
+            // -------- the pieces, their Q, and the row tile that this block begins and does not end
+            const ChunkStart start = plan.start[blockIdx.x];
+            ChunkWalk x;
+            x.begin(a, start);
             AttnSplit split{0, 0, 0, -1};
             uint32_t pieces[2] = {0, 0};
             bool go = true;
-            for (; go && w.left > 0; w.next(a)) {
-                if (w.tile == 0 && w.take < w.t.count)  // the last piece
-                    split = AttnSplit{w.r, w.row_tile, w.head,
-                                      share_holding(start.total, start.end - 1 + (w.t.count - w.take))};
+            for (int n = 0; go; ++n) {
+                if (n >= kPieceRing)
+                    go = mbar_wait(smem_ptr(&c.piece_free[piece_at.stage]), piece_at.phase ^ 1, &c.gave_up);
+                if (!go) break;
+                if (x.left <= 0) w.take = 0;
+                if (x.left > 0) {
+                    const bool whole = x.tile == 0 && x.take == x.t.count;
+                    w.take = x.take;
+                    w.count[0] = x.tiles_of(a, 0);
+                    w.count[1] = x.tiles_of(a, 1);
+                    w.shared = x.t.shared;
+                    w.row = x.q.begin + x.t.token0;
+                    w.n = x.t.n;
+                    w.pos = x.q.kv - x.q.n + x.t.token0;
+                    w.kv = x.q.kv;
+                    w.key0 = (x.t.first + x.tile) * kKeyTile;
+                    w.lo = x.t.lo;
+                    w.hi = x.t.hi;
+                    w.head = x.head;
+                    w.request = x.r;
+                    w.slot = whole ? -1 : x.tile > 0 ? 0 : 1;
+                    if (!whole && x.tile == 0)  // the last piece
+                        split = AttnSplit{x.r, x.row_tile, x.head,
+                                          share_holding(start.total, start.end - 1 + (x.t.count - x.take))};
+                }
+                c.piece[piece_at.stage] = w;
+                mbar_arrive(smem_ptr(&c.piece_full[piece_at.stage]));
+                piece_at.step();
+                if (x.left <= 0) break;
+                x.next(a);  // before the wait for room for Q
                 for (int h = 0; h < 2; ++h) {
-                    if (w.tiles_of(a, h) == 0) break;
+                    if (w.count[h] == 0) break;
                     // As soon as the piece's last scores are there its Q is not read any more: the next one's loads run beside
                     // the last tile's exponentials, its product and the results.
                     if (pieces[h] > 0) go = go && mbar_wait(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up);
@@ -614,9 +687,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     ++pieces[h];
                     const uint32_t full = smem_ptr(&c.q_full[h]);
                     mbar_arrive_tx(full, uint32_t(HALVES * a.half_tokens * a.group) * 128u);
-                    for (int x = 0; x < HALVES; ++x)
-                        tma_load_rows(smem_ptr(q_smem + h * C::TILE + x * kHalfBytes), &q_map, full, 64 * x, w.head * a.group,
-                                      w.q.begin + w.t.token0 + (w.t.shared ? 0 : h * a.half_tokens));
+                    for (int y = 0; y < HALVES; ++y)
+                        tma_load_rows(smem_ptr(q_smem + h * C::TILE + y * kHalfBytes), &q_map, full, 64 * y, w.head * a.group,
+                                      w.row + (w.shared ? 0 : h * a.half_tokens));
                 }
             }
             int late = 0;
@@ -640,17 +713,16 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         const int row_token = a.by_group.of(row), row_head = row - row_token * a.group;
         int n_s = 0;    // tiles of this half so far
         int tiles = 0;  // tiles of the block before this piece
-        for (; w.left > 0; tiles += w.take, w.next(a)) {
-            const int count = w.tiles_of(a, h);
-            if (w.t.shared && count == 0) continue;
-            const bool whole = w.tile == 0 && w.take == w.t.count;
-            const int n_tokens = w.tokens_of(a, h), token0 = w.t.token0 + (w.t.shared ? 0 : h * a.half_tokens);
+        uint32_t merges = 0;
+        for (; next_piece(piece_at, w, false); tiles += w.take) {
+            const int count = h ? w.count[1] : w.count[0];
+            if (count == 0) continue;
+            const int first = w.shared ? 0 : h * a.half_tokens, n_tokens = min(w.n - first, a.half_tokens);
             const bool mine = row_token < n_tokens;
-            const int token = token0 + min(row_token, n_tokens - 1), head = w.head * a.group + row_head;
-            const int base = w.q.kv - w.q.n;
-            const int lo = keys_from(a, base + token), hi = keys_to(a, w.q.kv, base + token);
+            const int token = first + min(row_token, n_tokens - 1), head = w.head * a.group + row_head;
+            const int lo = keys_from(a, w.pos + token), hi = keys_to(a, w.kv, w.pos + token);
             // keys [all_lo, all_hi) are seen by every row of the half
-            const int all_lo = keys_from(a, base + token0 + n_tokens - 1), all_hi = keys_to(a, w.q.kv, base + token0);
+            const int all_lo = keys_from(a, w.pos + first + n_tokens - 1), all_hi = keys_to(a, w.kv, w.pos + first);
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
             // p = 2^(s sc + neg).  The reference is the fp32 number nearest to m sc, and rest = m sc - reference (exact); a
@@ -658,8 +730,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             float m = -INFINITY, l = 0.0f, neg = 0.0f, rest = 0.0f;
             bool far = false;
             for (int j = 0; j < count; ++j, ++n_s) {
-                const int i = w.t.shared ? 2 * j + h : j;  // of the piece's tiles
-                const int key0 = (w.t.first + w.tile + i) * kKeyTile;
+                const int i = w.shared ? 2 * j + h : j;  // of the piece's tiles
+                const int key0 = w.key0 + i * kKeyTile;
                 wait(c.s_full[h], n_s & 1);
                 const uint32_t live = *(volatile uint32_t*)&c.live[(tiles + i) % kLiveRing];
                 float s[kKeyTile];
@@ -695,7 +767,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (__any_sync(0xffffffffu, moves)) {
                     const float m_new = moves ? top : m, scaled = m_new * sc;
                     const bool huge = fabsf(scaled) > kExactRef;
-                    const float rest_new = moves && !huge ? __fmaf_rn(m_new, sc, -scaled) : moves ? 0.0f : rest;
+                    const float rest_new = beyond_reference(m_new, sc);
                     if (__any_sync(0xffffffffu, moves && m != -INFINITY)) {
                         const float f = moves && m != -INFINITY ? exp2_fast(__fmaf_rn(m - m_new, sc, rest_new - rest)) : 1.0f;
                         wait(c.o_full[h], (n_s - 1) & 1);  // the previous product has added to O
@@ -754,26 +826,25 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             wait(c.o_full[h], (n_s - 1) & 1);
             float to_m = exp2_fast(-rest);  // from the reference to m
             l *= to_m;
-            const bool both = w.t.shared && w.take > 1;
+            const bool both = w.shared && w.take > 1, whole = w.slot < 0;
             float to_other = 0.0f;  // the other half's part in the result
             if (both) {
                 if (h == 1) {
                     c.m[row] = m;
                     c.l[row] = l;
-                    c.to_m[row] = to_m;
                     tc_fence_before();
-                    named_barrier<1, 256>();
-                    named_barrier<2, 256>();  // the first half has read O
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_ptr(&c.merge_full));
+                    wait(c.merge_free, merges++ & 1);  // the first half has read O
                     continue;
                 }
-                named_barrier<1, 256>();
-                tc_fence_after();
+                wait(c.merge_full, merges++ & 1);
                 const float m1 = c.m[row], top = fmaxf(m, m1);
                 const float f0 = m == -INFINITY ? 0.0f : exp2_fast((m - top) * sc);
                 const float f1 = m1 == -INFINITY ? 0.0f : exp2_fast((m1 - top) * sc);
                 l = l * f0 + c.l[row] * f1;
                 to_m *= f0;
-                to_other = c.to_m[row] * f1;
+                to_other = exp2_fast(-beyond_reference(m1, sc)) * f1;
                 m = top;
             }
             if (whole) {
@@ -781,49 +852,50 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 to_m *= inv;
                 to_other *= inv;
             }
-            const int64_t at = int64_t(2 * blockIdx.x + (w.tile > 0 ? 0 : 1)) * kChunkRows + h * 128 + row;
-            uint16_t* out = static_cast<uint16_t*>(a.out) + (w.q.begin + token) * a.out_token_stride + head * a.out_head_stride;
+            const int piece = (2 * blockIdx.x + w.slot) * 2 + h;  // a piece's half in the workspace
+            uint16_t* out = static_cast<uint16_t*>(a.out) + int64_t(w.row + token) * a.out_token_stride + head * a.out_head_stride;
+            float o[D];
 #pragma unroll
-            for (int x0 = 0; x0 < D; x0 += 32) {
-                float o[32];
-                tm_load(o, o_at + x0);
-                tm_wait<32>(o);
+            for (int x = 0; x < D; x += 32) tm_load(o + x, o_at + x);
+            tm_wait<D>(o);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] *= to_m;
-                if (both) {
-                    float o1[32];
-                    tm_load(o1, o_at + 128 + x0);
-                    tm_wait<32>(o1);
+            for (int x = 0; x < D; ++x) o[x] *= to_m;
+            if (both) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = __fmaf_rn(o1[x], to_other, o[x]);
+                for (int x0 = 0; x0 < D; x0 += 16) {
+                    float o1[16];
+                    tm_load16(o1, o_at + 128 + x0);
+                    tm_wait<16>(o1);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) o[x0 + x] = __fmaf_rn(o1[x], to_other, o[x0 + x]);
                 }
-                if (mine && whole) {
-#pragma unroll
-                    for (int x = 0; x < 32; x += 16) {
-                        uint32_t p[8];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) p[y] = pack2<BF16>(o[x + 2 * y], o[x + 2 * y + 1]);
-                        if (a.out_by_32) {
-                            store32(out + x0 + x, p);
-                        } else {
-                            *reinterpret_cast<uint4*>(out + x0 + x) = make_uint4(p[0], p[1], p[2], p[3]);
-                            *reinterpret_cast<uint4*>(out + x0 + x + 8) = make_uint4(p[4], p[5], p[6], p[7]);
-                        }
-                    }
-                } else if (mine) {
-#pragma unroll
-                    for (int x = 0; x < 32; x += 8) store32(ws.o + at * D + x0 + x, reinterpret_cast<const uint32_t*>(o + x));
-                }
-                __syncwarp();
             }
             tc_fence_before();
-            if (both) named_barrier<2, 256>();
-            if (mine) {
-                if (!whole)
-                    ws.ml[at] = make_float2(m, l);
-                else if (a.lse != nullptr)
-                    a.lse[int64_t(w.q.begin + token) * a.q_heads + head] = l > 0.0f ? m * a.scale + logf(l) : -INFINITY;
+            __syncwarp();
+            if (both && lane == 0) mbar_arrive(smem_ptr(&c.merge_free));
+            if (mine && whole) {
+#pragma unroll
+                for (int x = 0; x < D; x += 16) {
+                    uint32_t p[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) p[y] = pack2<BF16>(o[x + 2 * y], o[x + 2 * y + 1]);
+                    if (a.out_by_32) {
+                        store32(out + x, p);
+                    } else {
+                        *reinterpret_cast<uint4*>(out + x) = make_uint4(p[0], p[1], p[2], p[3]);
+                        *reinterpret_cast<uint4*>(out + x + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+                    }
+                }
+                if (a.lse != nullptr)
+                    a.lse[int64_t(w.row + token) * a.q_heads + head] = l > 0.0f ? m * a.scale + logf(l) : -INFINITY;
+            } else if (mine) {
+                // 8 columns of the 128 rows together, so that a warp writes 1 KB in one piece
+#pragma unroll
+                for (int x = 0; x < D; x += 8)
+                    store32(ws.o + (int64_t(piece) * D + x) * 128 + row * 8, reinterpret_cast<const uint32_t*>(o + x));
+                ws.ml[piece * 128 + row] = make_float2(m, l);
             }
+            __syncwarp();
         }
     }
     __syncthreads();
