@@ -32,10 +32,10 @@ struct Chunk {
     static constexpr int HALVES = D > 64 ? 2 : 1;  // 64-column halves of a tile
     static constexpr int TILE = HALVES * kHalfBytes;
     static constexpr int Q = 2 * TILE;
-    static constexpr int STAGES = (224 * 1024 - Q) / TILE > 8 ? 8 : (224 * 1024 - Q) / TILE;
+    static constexpr int STAGES = (224 * 1024 - Q) / TILE;  // 5, or 12 of half the size
     static constexpr int SMEM = 1024 + Q + STAGES * TILE;
 };
-constexpr int kLiveRing = 8;  // tiles whose page masks are kept; the loads are at most five tiles ahead of a half
+constexpr int kLiveRing = 8;  // tiles whose page masks are kept; the loads are at most six tiles ahead of a half
 
 // A row tile costs about this many key tiles on top of its own: its Q, the first scores, the results.  Shares are equal in
 // key tiles plus these, or the block whose share is many short row tiles (the beginning of a prompt) would be the last
@@ -215,6 +215,12 @@ struct Ring {
             phase ^= 1;
         }
     }
+    __device__ __forceinline__ void back() {
+        if (--stage < 0) {
+            stage = STAGES - 1;
+            phase ^= 1;
+        }
+    }
 };
 
 // Box [tokens of a half][heads of a group][64 columns] of q -> swizzled shared memory.
@@ -345,8 +351,10 @@ struct __align__(16) Piece {
 };
 
 struct ChunkControl {
-    uint64_t full[8], empty[8];
-    uint64_t clean[kLiveRing];  // per key tile: its V has no values that no row sees
+    // Places of the ring, by use; a tile's barriers, by tile: each is waited for in turn by one role, so that a wait is never
+    // two phases from the barrier's own, whatever order the loads end in.
+    uint64_t empty[12];
+    uint64_t k_full[kLiveRing], v_full[kLiveRing], clean[kLiveRing];  // clean: V has no values that no row sees
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], drained;
     uint64_t piece_full[kPieceRing], piece_free[kPieceRing];
     uint64_t merge_full, merge_free;
@@ -434,10 +442,13 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_ptr(&c.full[i]), 1);
             mbar_init(smem_ptr(&c.empty[i]), 1);
         }
-        for (int i = 0; i < kLiveRing; ++i) mbar_init(smem_ptr(&c.clean[i]), 1);
+        for (int i = 0; i < kLiveRing; ++i) {
+            mbar_init(smem_ptr(&c.k_full[i]), 1);
+            mbar_init(smem_ptr(&c.v_full[i]), 1);
+            mbar_init(smem_ptr(&c.clean[i]), 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_ptr(&c.q_full[i]), 1);
             mbar_init(smem_ptr(&c.q_free[i]), 1);
@@ -492,7 +503,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int ppt = max(kKeyTile >> a.page_shift, 1), rows = min(1 << a.page_shift, kKeyTile);
             const int pg = lane % ppt, half = lane / ppt;  // a lane for each page and 64 columns
             Ring<STAGES> at;
-            int n = 0, tiles = 0;
+            Ring<kLiveRing> tile;
+            int n = 0;
             bool go = true;
             while (go && next_piece(piece_at, w, false)) {
                 const int32_t* table = a.table + w.request * a.table_stride;
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     return half < HALVES && i < w.take && k0 < w.hi && k0 + rows > w.lo ? table[k0 >> a.page_shift] : -1;
                 };
                 int page = page_of(0);
-                for (int i = 0; go && i < w.take; ++i, ++tiles) {
+                for (int i = 0; go && i < w.take; ++i) {
                     const int next = page_of(i + 1);  // on its way while this tile waits for room
                     const int slot0 = (w.key0 + i * kKeyTile + (pg << a.page_shift)) & ((1 << a.page_shift) - 1);
                     const bool load = page >= 0 && page < a.pages;
@@ -511,9 +523,9 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         if (n >= STAGES)
                             go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.empty[at.stage]), at.phase ^ 1, &c.gave_up));
                         if (!go) break;
-                        const uint32_t full = smem_ptr(&c.full[at.stage]);
+                        const uint32_t full = smem_ptr(is_v ? &c.v_full[tile.stage] : &c.k_full[tile.stage]);
                         if (lane == 0) {
-                            if (!is_v) *(volatile uint32_t*)&c.live[tiles % kLiveRing] = mask;
+                            if (!is_v) *(volatile uint32_t*)&c.live[tile.stage] = mask;
                             mbar_arrive_tx(full, uint32_t(__popc(mask)) * uint32_t(rows) * 128u * HALVES);
                         }
                         __syncwarp();
@@ -522,13 +534,19 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                                          is_v ? &v_map : &k_map, full, half * 64, slot0, w.head, page);
                     }
                     page = next;
+                    if (go) tile.step();
                 }
             }
-            // no copy is left in flight when the block ends, after a wait that was given up too
+            // No copy is left in flight when the block ends, after a wait that was given up too: the last tiles' barriers (the
+            // earlier ones have been waited for, or their places would not have been free).
             if (lane == 0) {
                 int late = 0;
-                for (int i = max(n - STAGES, 0); i < n; ++i)
-                    mbar_wait(smem_ptr(&c.full[i % STAGES]), (i / STAGES) & 1, &late);
+                Ring<kLiveRing> last = tile;
+                for (int i = 0; i < min((n + 1) / 2, STAGES / 2 + 2); ++i) {
+                    if (i > 0 || n % 2 == 0) last.back();
+                    mbar_wait(smem_ptr(&c.k_full[last.stage]), last.phase, &late);
+                    if (i > 0 || n % 2 == 0) mbar_wait(smem_ptr(&c.v_full[last.stage]), last.phase, &late);
+                }
                 if (late) *(volatile int*)&c.gave_up = 1;
             }
         } else if (warp == 9) {
@@ -542,7 +560,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const uint32_t v_desc = tc_desc(smem_ptr(ring), kHalfBytes >> 4);
                 Ring<STAGES> k, v;  // of the next K and V; the ring holds K0 V0 K1 V1 ...
                 v.step();
-                Ring<kLiveRing> tile;
+                Ring<kLiveRing> k_tile, tile;
                 uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
                 bool go = true;
                 auto await = [&](uint64_t& bar, uint32_t parity) {
@@ -554,7 +572,6 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll 1
                     for (int i = -ahead; go && i < w.take; ++i) {  // the product with V of tile i, the scores of tile i + ahead
                         const bool more = i + ahead < w.take;
-                        if (more) await(c.full[k.stage], k.phase);
                         if (i >= 0) await(c.clean[tile.stage], tile.phase);
 #pragma unroll 1
                         for (int h = w.shared ? i & 1 : 0; go && h < (w.shared ? (i & 1) + 1 : 2); ++h) {
@@ -574,6 +591,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                                 }
                                 tc_commit(smem_ptr(&c.o_full[h]));
                             }
+                            const bool last = w.shared || h == 1;  // of the halves that read this V and K
+                            if (i >= 0 && last) tc_commit(smem_ptr(&c.empty[v.stage]));
+                            if (more && (w.shared || h == 0)) await(c.k_full[k_tile.stage], k_tile.phase);
+                            if (!go) break;
                             if (more && of_k < count) {  // S_h = Q_h K^T; the last of a piece frees Q
                                 if (of_k == 0) {
                                     await(c.q_full[h], h ? q_phase[1] : q_phase[0]);
@@ -590,15 +611,15 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                                 tc_commit(smem_ptr(&c.s_full[h]));
                                 if (of_k + 1 == count) tc_commit(smem_ptr(&c.q_free[h]));
                             }
+                            if (more && last) tc_commit(smem_ptr(&c.empty[k.stage]));
                         }
                         if (i >= 0) {
-                            if (go) tc_commit(smem_ptr(&c.empty[v.stage]));
                             v.step();
                             v.step();
                             tile.step();
                         }
                         if (more) {
-                            if (go) tc_commit(smem_ptr(&c.empty[k.stage]));
+                            k_tile.step();
                             k.step();
                             k.step();
                         }
@@ -622,7 +643,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             while (go && next_piece(piece_at, w, false)) {
                 for (int i = 0; go && i < w.take; ++i, tile.step()) {
                     at.step();  // past K
-                    go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.full[at.stage]), at.phase, &c.gave_up));
+                    go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.v_full[tile.stage]), tile.phase, &c.gave_up));
                     const int key0 = w.key0 + i * kKeyTile;
                     const uint32_t live = *(volatile uint32_t*)&c.live[tile.stage];
                     if (key0 < w.lo || key0 + kKeyTile > w.hi || live != all) {
@@ -898,6 +919,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             __syncwarp();
         }
     }
+    __syncwarp();
     __syncthreads();
     if (threadIdx.x == 0 && *(volatile int*)&c.gave_up) atomicExch(&g_gave_up, 1);
     if (warp == 9) {

@@ -586,3 +586,13 @@ def test_step_in_a_cuda_graph(nq):
 def test_no_wait_was_given_up(nq):
     """After everything above: no kernel gave up a wait for its loads."""
     nq.paged_status()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,window", [(128, 0), (128, 700), (64, 700), (96, 0)])
+@pytest.mark.parametrize("new", [5, 20, 50])
+def test_attention_many_pieces_in_every_block(nq, dtype, D, window, new):
+    """Blocks that work through several row tiles, whole ones and parts, of one half's rows and of two."""
+    rng = np.random.default_rng(new)
+    lens = [(int(c), int(n)) for c, n in zip(rng.integers(300, 2500, 60), rng.integers(1, new + 1, 60))]
+    Step(lens, 16, 4, D, 32, dtype, seed=new).check(nq, window=window)
