@@ -87,7 +87,9 @@ struct AttnArgs {
 constexpr int kAttnGrid = 152;
 
 struct AttnSplit {  // per block: the row tile that it began and did not end, or last_block = -1
-    int request, row_tile, head, last_block;
+    int begin;         // row of q where the request's (small kernel) or the row tile's (large kernel) tokens begin
+    int row0, n_rows;  // the row tile's rows, counted from there
+    int head, last_block;
 };
 
 struct AttnWorkspace {
@@ -124,9 +126,9 @@ bool make_query_map(const AttnArgs& a, CUtensorMap* q);
 int launch_attention_small(const AttnArgs& a);
 int launch_attention_chunk(const AttnArgs& a);
 uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim);
-// Joins the pieces of split row tiles (launched after either kernel, as its dependent).  A row tile has `tile_rows` rows;
-// the workspace has `slot_rows` for it, row i at i / half_rows * 128 + i % half_rows.
-int launch_attention_join(const AttnArgs& a, int slot_rows, int tile_rows, int half_rows);
+// Joins the pieces of split row tiles (launched after either kernel, as its dependent).  The workspace has `slot_rows` rows
+// for a row tile, its row i at i / half_rows * 128 + i % half_rows.
+int launch_attention_join(const AttnArgs& a, int slot_rows, int half_rows);
 
 // Whether a kernel gave up a wait since the last call.
 int small_gave_up(int* seen);

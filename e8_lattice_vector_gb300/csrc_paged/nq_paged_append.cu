@@ -1,7 +1,8 @@
 // nq_paged_append.cu -- a step's K and V rows into the page pools.
 //
-// A pure copy: every row is read once and written once, 16 bytes a thread.
-// Both types are 16 bits wide, so the kernel moves bits and knows no type.
+// A pure copy: every row is read once and written once, 16 bytes a thread, a token's row_vecs pieces on neighbouring
+// threads.  Both types are 16 bits wide, so the kernel moves bits and knows no type.  Memory-bound: a thread takes PASS tokens
+// so that as many loads are in flight before the first store.
 #include "nq_paged.h"
 
 #include <algorithm>
@@ -19,23 +20,44 @@ struct AppendArgs {
     int tokens, vecs, row_vecs, page_shift;  // vecs: 16-byte pieces of a head's row; row_vecs: of a token's
 };
 
-// blockIdx.y: 0 = K, 1 = V.
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a) {
+// blockIdx.y: 0 = K, 1 = V.  A block takes PASS times `together` tokens, as many as its threads hold rows of (at least one).
+template <int PASS>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendArgs a, int together) {
     const bool is_v = blockIdx.y != 0;
     const uint16_t* src = is_v ? a.v : a.k;
     uint16_t* dst = is_v ? a.v_pages : a.k_pages;
     const int64_t ts = is_v ? a.v_token : a.k_token, hs = is_v ? a.v_head : a.k_head;
-    const int64_t n = int64_t(a.tokens) * a.row_vecs;
-    for (int64_t i = int64_t(blockIdx.x) * kAppendThreads + threadIdx.x; i < n;
-         i += int64_t(gridDim.x) * kAppendThreads) {
-        const int64_t t = i / a.row_vecs;
-        const int x = int(i - t * a.row_vecs), h = x / a.vecs, c = x - h * a.vecs;
-        const int64_t slot = __ldg(a.slots + t);
-        if (slot < 0 || slot >= a.n_slots) continue;
-        const int64_t page = slot >> a.page_shift, off = slot & ((1 << a.page_shift) - 1);
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(src + t * ts + h * hs + 8 * c));
-        *reinterpret_cast<uint4*>(dst + page * a.page_stride + h * a.head_stride + off * a.slot_stride + 8 * c) = w;
+    const int mine = int(threadIdx.x) / a.row_vecs;  // of the tokens taken together
+    if (mine >= together) return;
+    const int64_t t0 = int64_t(blockIdx.x) * PASS * together + mine;
+    for (int x = threadIdx.x - mine * a.row_vecs; x < a.row_vecs; x += kAppendThreads) {
+        const int h = x / a.vecs, c = x - h * a.vecs;
+        int64_t slot[PASS];
+        uint4 w[PASS];
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) {
+            const int64_t t = t0 + i * together;
+            slot[i] = t < a.tokens ? __ldg(a.slots + t) : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) {
+            const int64_t t = min(t0 + i * together, int64_t(a.tokens) - 1);
+            w[i] = __ldg(reinterpret_cast<const uint4*>(src + t * ts + h * hs + 8 * c));
+        }
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) {
+            if (slot[i] < 0 || slot[i] >= a.n_slots) continue;
+            const int64_t page = slot[i] >> a.page_shift, off = slot[i] & ((1 << a.page_shift) - 1);
+            *reinterpret_cast<uint4*>(dst + page * a.page_stride + h * a.head_stride + off * a.slot_stride + 8 * c) = w[i];
+        }
     }
+}
+
+template <int PASS>
+int launch_append(const AppendArgs& a, int together, cudaStream_t stream) {
+    const int64_t blocks = (int64_t(a.tokens) + PASS * together - 1) / (PASS * together);
+    paged_append_kernel<PASS><<<dim3(unsigned(blocks), 2), kAppendThreads, 0, stream>>>(a, together);
+    return cudaGetLastError() == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -56,8 +78,6 @@ extern "C" int nq_paged_append(const void* k, int64_t k_token_stride, int64_t k_
         if (!nq::paged_stride_ok(s, tokens, 0)) return NQ_ERR_ARG;
     for (int64_t s : {k_head_stride, v_head_stride})
         if (!nq::paged_stride_ok(s, pool->kv_heads, 0)) return NQ_ERR_ARG;
-    const int sms = nq::paged_sm_count();
-    if (sms <= 0) return NQ_ERR_CUDA;
     nq::AppendArgs a;
     a.k = static_cast<const uint16_t*>(k);
     a.v = static_cast<const uint16_t*>(v);
@@ -76,8 +96,9 @@ extern "C" int nq_paged_append(const void* k, int64_t k_token_stride, int64_t k_
     a.vecs = pool->head_dim / 8;
     a.row_vecs = pool->kv_heads * a.vecs;
     a.page_shift = nq::paged_page_shift(pool->page_size);
-    const int64_t want = (int64_t(tokens) * a.row_vecs + nq::kAppendThreads - 1) / nq::kAppendThreads;
-    const int grid = int(std::min<int64_t>(want, int64_t(sms) * 64));
-    nq::paged_append_kernel<<<dim3(grid, 2), nq::kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+    const int together = std::max(nq::kAppendThreads / a.row_vecs, 1);
+    // one pass while that does not fill the GPU (152 multiprocessors of eight blocks): then latency counts
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return 2 * (int64_t(tokens) / together) < 152 * 8 ? nq::launch_append<1>(a, together, s)
+                                                      : nq::launch_append<4>(a, together, s);
 }

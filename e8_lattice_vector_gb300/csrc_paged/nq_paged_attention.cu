@@ -19,20 +19,18 @@ constexpr int kJoinWarps = 8;
 // have many pieces (up to one from every block) and take all eight warps each; many rows take a warp each.
 template <bool BF16, int SPREAD>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    attention_join_kernel(const AttnArgs a, const AttnWorkspace ws, int slot_rows, int tile_rows, int half_rows) {
+    attention_join_kernel(const AttnArgs a, const AttnWorkspace ws, int slot_rows, int half_rows) {
     constexpr int ROWS = kJoinWarps / SPREAD;  // rows at a time
     __shared__ float4 part[kJoinWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, share = warp % SPREAD;
     pdl_wait();
     const AttnSplit s = ws.split[b];
     if (s.last_block < 0) return;
-    const Request q = load_request(a, s.request);
-    const int row0 = s.row_tile * tile_rows, n_rows = min(q.n * a.group - row0, tile_rows);
     const int pieces = s.last_block - b + 1;
     const float sc = a.scale * kLog2e;
     const int D = a.head_dim;
-    for (int first = blockIdx.y * ROWS; first < n_rows; first += gridDim.y * ROWS) {
-        const int row = min(first + warp / SPREAD, n_rows - 1);
+    for (int first = blockIdx.y * ROWS; first < s.n_rows; first += gridDim.y * ROWS) {
+        const int row = min(first + warp / SPREAD, s.n_rows - 1);
         const int half = row >= half_rows, slot_row = half * 128 + row - half * half_rows;
         auto at = [&](int i) { return int64_t(i == 0 ? 2 * b + 1 : 2 * (b + i)) * slot_rows + slot_row; };
         // the large kernel's rows are stored 8 columns of a half's 128 rows together
@@ -40,29 +38,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             if constexpr (SPREAD > 1) return at(i) * D + 4 * lane;
             return (at(i) - (slot_row & 127)) * D + (lane >> 1) * 1024 + (slot_row & 127) * 8 + 4 * (lane & 1);
         };
-        float top = -INFINITY, sum = 0.0f;
-        for (int i = lane; i < pieces; i += 32) top = fmaxf(top, ws.ml[at(i)].x);
+        // a lane for each piece, 32 at a time; the first 32 (nearly always all) are kept
+        const float2 none = make_float2(-INFINITY, 0.0f), ml = lane < pieces ? ws.ml[at(lane)] : none;
+        float top = ml.x;
+        for (int i = lane + 32; i < pieces; i += 32) top = fmaxf(top, ws.ml[at(i)].x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        for (int i = lane; i < pieces; i += 32) {
-            const float2 ml = ws.ml[at(i)];
-            if (ml.x != -INFINITY) sum += ml.y * exp2_fast((ml.x - top) * sc);
+        float sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            const float2 x = i0 == 0 ? ml : i0 + lane < pieces ? ws.ml[at(i0 + lane)] : none;
+            const float f = x.x == -INFINITY ? 0.0f : exp2_fast((x.x - top) * sc);
+            sum += x.y * f;
+            const int n = min(pieces - i0, 32);
+#pragma unroll 4
+            for (int i = share; i < n; i += SPREAD) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                if (4 * lane < D) {
+                    const float4 o = *reinterpret_cast<const float4*>(ws.o + o_at(i0 + i));
+                    acc.x = fmaf(o.x, fi, acc.x);
+                    acc.y = fmaf(o.y, fi, acc.y);
+                    acc.z = fmaf(o.z, fi, acc.z);
+                    acc.w = fmaf(o.w, fi, acc.w);
+                }
+            }
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (4 * lane < D) {
-#pragma unroll 4
-            for (int i = share; i < pieces; i += SPREAD) {
-                const float m = ws.ml[at(i)].x;
-                const float4 o = *reinterpret_cast<const float4*>(ws.o + o_at(i));
-                const float f = m == -INFINITY ? 0.0f : exp2_fast((m - top) * sc);
-                acc.x = fmaf(o.x, f, acc.x);
-                acc.y = fmaf(o.y, f, acc.y);
-                acc.z = fmaf(o.z, f, acc.z);
-                acc.w = fmaf(o.w, f, acc.w);
-            }
-        }
         if constexpr (SPREAD > 1) {
             part[warp][lane] = acc;
             __syncthreads();
@@ -78,9 +80,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             }
             __syncthreads();  // part is read
         }
-        if (share == 0 && first + warp / SPREAD < n_rows) {
+        if (share == 0 && first + warp / SPREAD < s.n_rows) {
             const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            const int token = a.by_group.of(row0 + row), t = q.begin + token, h = s.head * a.group + row0 + row - token * a.group;
+            const int token = a.by_group.of(s.row0 + row), t = s.begin + token;
+            const int h = s.head * a.group + s.row0 + row - token * a.group;
             uint2 packed;
             packed.x = pack2<BF16>(acc.x * inv, acc.y * inv);
             packed.y = pack2<BF16>(acc.z * inv, acc.w * inv);
@@ -95,9 +98,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 template <int SPREAD>
 cudaError_t launch_join(const cudaLaunchConfig_t& cfg, const AttnArgs& a, const AttnWorkspace& ws, int slot_rows,
-                        int tile_rows, int half_rows) {
-    return a.bf16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, SPREAD>, a, ws, slot_rows, tile_rows, half_rows)
-                  : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, SPREAD>, a, ws, slot_rows, tile_rows, half_rows);
+                        int half_rows) {
+    return a.bf16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, SPREAD>, a, ws, slot_rows, half_rows)
+                  : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, SPREAD>, a, ws, slot_rows, half_rows);
 }
 
 int check_attention(const nq_attention* a, const nq_pool* pool) {
@@ -174,21 +177,21 @@ bool make_query_map(const AttnArgs& a, CUtensorMap* q) {
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_attention_join(const AttnArgs& a, int slot_rows, int tile_rows, int half_rows) {
+int launch_attention_join(const AttnArgs& a, int slot_rows, int half_rows) {
     const AttnWorkspace ws = attn_workspace(a.workspace, slot_rows, a.head_dim);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     const bool few = slot_rows <= kSmallRows;
-    const int64_t rows = std::min<int64_t>(int64_t(a.tokens) * a.group, tile_rows);
+    const int64_t rows = std::min<int64_t>(int64_t(a.tokens) * a.group, few ? kSmallRows : 2 * half_rows);
     cfg.gridDim = dim3(kAttnGrid, unsigned(few ? rows : (rows + kJoinWarps - 1) / kJoinWarps));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = a.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = few ? launch_join<kJoinWarps>(cfg, a, ws, slot_rows, tile_rows, half_rows)
-                              : launch_join<1>(cfg, a, ws, slot_rows, tile_rows, half_rows);
+    const cudaError_t e = few ? launch_join<kJoinWarps>(cfg, a, ws, slot_rows, half_rows)
+                              : launch_join<1>(cfg, a, ws, slot_rows, half_rows);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 

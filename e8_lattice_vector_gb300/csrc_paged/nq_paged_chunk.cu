@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const ChunkStart start = plan.start[blockIdx.x];
             ChunkWalk x;
             x.begin(a, start);
-            AttnSplit split{0, 0, 0, -1};
+            AttnSplit split{0, 0, 0, 0, -1};
             uint32_t pieces[2] = {0, 0};
             bool go = true;
             for (int n = 0; go; ++n) {
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     w.request = x.r;
                     w.slot = whole ? -1 : x.tile > 0 ? 0 : 1;
                     if (!whole && x.tile == 0)  // the last piece
-                        split = AttnSplit{x.r, x.row_tile, x.head,
+                        split = AttnSplit{w.row, 0, w.n * a.group, x.head,
                                           share_holding(start.total, start.end - 1 + (x.t.count - x.take))};
                 }
                 c.piece[piece_at.stage] = w;
@@ -973,7 +973,7 @@ int launch_attention_chunk(const AttnArgs& a) {
     attention_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a, plan, pairs);
     if (cudaGetLastError() != cudaSuccess) return NQ_ERR_CUDA;
     const int st = a.bf16 ? launch_chunk<true>(a, km, vm, qm, ws, plan) : launch_chunk<false>(a, km, vm, qm, ws, plan);
-    return st == NQ_OK ? launch_attention_join(a, kChunkRows, 2 * a.half_tokens * a.group, a.half_tokens * a.group) : st;
+    return st == NQ_OK ? launch_attention_join(a, kChunkRows, a.half_tokens * a.group) : st;
 }
 
 int chunk_gave_up(int* seen) {

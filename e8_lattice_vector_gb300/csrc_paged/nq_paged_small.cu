@@ -211,12 +211,15 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             const int p0 = w.q.kv - w.q.n + a.by_group.of(w.row_tile * kSmallRows);
             const int p1 = w.q.kv - w.q.n + a.by_group.of(min((w.row_tile + 1) * kSmallRows, w.q.n * a.group) - 1);
             const int lo = keys_from(a, p0), hi = keys_to(a, w.q.kv, p1);
+            const int32_t* table = a.table + w.r * a.table_stride;
+            auto page_of = [&](int i) {  // this lane's page of tile i of the piece, -1: none
+                const int k0 = (w.s.first + w.tile + i) * kKeyTile + (pg << a.page_shift);
+                return rest < 2 * HALVES && i < take && k0 < hi && k0 + rows > lo ? table[k0 >> a.page_shift] : -1;
+            };
+            int page = page_of(0);
             for (int i = 0; i < take; ++i, ++n) {
-                const int key0 = (w.s.first + w.tile + i) * kKeyTile;
-                const int k0 = key0 + (pg << a.page_shift);  // first key of this lane's page within the tile
-                int page = -1;
-                if (k0 < hi && k0 + rows > lo && rest < 2 * HALVES)
-                    page = a.table[w.r * a.table_stride + (k0 >> a.page_shift)];
+                const int next = page_of(i + 1);  // on its way while this tile waits for room
+                const int k0 = (w.s.first + w.tile + i) * kKeyTile + (pg << a.page_shift);
                 const bool load = page >= 0 && page < a.pages;
                 const int st = n % S::STAGES;
                 if (n >= S::STAGES)
@@ -233,6 +236,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
                     const uint32_t dst = smem_ptr(ring + st * S::STAGE + (is_v * HALVES + half) * kHalfBytes + pg * rows * 128);
                     tma_load_box(dst, is_v ? &v_map : &k_map, full, half * 64, k0 & ((1 << a.page_shift) - 1), w.head, page);
                 }
+                page = next;
             }
             w.next(a, a.kv_heads);
         }
@@ -455,7 +459,8 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
         }
         if (threadIdx.x == 0 && w.tile == 0 && !whole) {
             // this block began the row tile: the block of its last tile is the one whose share holds it
-            ws.split[blockIdx.x] = AttnSplit{w.r, w.row_tile, w.head, share_holding(c.total, c.end - 1 + (w.s.count - take))};
+            ws.split[blockIdx.x] =
+                AttnSplit{w.q.begin, row0, n_rows, w.head, share_holding(c.total, c.end - 1 + (w.s.count - take))};
         }
         named_barrier<1, kConsumers>();  // the join buffer and the sums are read
         w.next(a, a.kv_heads);
@@ -486,7 +491,7 @@ int launch_attention_small(const AttnArgs& a) {
     if (!make_pool_maps(a, &km, &vm)) return NQ_ERR_CUDA;
     const AttnWorkspace ws = attn_workspace(a.workspace, kSmallRows, a.head_dim);
     const int st = a.bf16 ? launch_small<true>(a, km, vm, ws) : launch_small<false>(a, km, vm, ws);
-    return st == NQ_OK ? launch_attention_join(a, kSmallRows, kSmallRows, kSmallRows) : st;
+    return st == NQ_OK ? launch_attention_join(a, kSmallRows, kSmallRows) : st;
 }
 
 int small_gave_up(int* seen) {
