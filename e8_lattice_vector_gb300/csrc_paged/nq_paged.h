@@ -73,6 +73,7 @@ struct AttnArgs {
     int64_t page_stride, head_stride, slot_stride;
     int tokens, q_heads, kv_heads, group, requests, table_cols, page_shift, pages, head_dim, causal, window;
     int bf16;
+    int mixed;      // both kernels are launched: the small one takes the requests of at most kSmallRows rows, the large one the others
     int out_by_32;  // rows of out start on 32-byte boundaries
     FastDiv by_group;
     int half_tokens;  // tokens whose rows fit one half of the large kernel's row tile (0: a group of more than 128 heads)
@@ -126,9 +127,9 @@ bool make_query_map(const AttnArgs& a, CUtensorMap* q);
 int launch_attention_small(const AttnArgs& a);
 int launch_attention_chunk(const AttnArgs& a);
 uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim);
-// Joins the pieces of split row tiles (launched after either kernel, as its dependent).  The workspace has `slot_rows` rows
-// for a row tile, its row i at i / half_rows * 128 + i % half_rows.
-int launch_attention_join(const AttnArgs& a, int slot_rows, int half_rows);
+// Join the pieces of split row tiles, launched after the small or the large kernel as its dependent.
+int launch_join_few_rows(const AttnArgs& a, const AttnWorkspace& ws);
+int launch_join_many_rows(const AttnArgs& a, const AttnWorkspace& ws);
 
 // Whether a kernel gave up a wait since the last call.
 int small_gave_up(int* seen);

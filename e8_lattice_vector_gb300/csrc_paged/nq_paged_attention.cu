@@ -14,93 +14,141 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 
-// Block (b, y): the row tile that block b of the attention kernel began and did not end.  SPREAD warps share a row: each
-// takes every SPREAD-th piece, and the sums meet in shared memory, in an order that depends on the lengths alone.  Few rows
-// have many pieces (up to one from every block) and take all eight warps each; many rows take a warp each.
-template <bool BF16, int SPREAD>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    attention_join_kernel(const AttnArgs a, const AttnWorkspace ws, int slot_rows, int half_rows) {
-    constexpr int ROWS = kJoinWarps / SPREAD;  // rows at a time
-    __shared__ float4 part[kJoinWarps][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, share = warp % SPREAD;
-    pdl_wait();
-    const AttnSplit s = ws.split[b];
-    if (s.last_block < 0) return;
-    const int pieces = s.last_block - b + 1;
-    const float sc = a.scale * kLog2e;
-    const int D = a.head_dim;
-    for (int first = blockIdx.y * ROWS; first < s.n_rows; first += gridDim.y * ROWS) {
-        const int row = min(first + warp / SPREAD, s.n_rows - 1);
-        const int half = row >= half_rows, slot_row = half * 128 + row - half * half_rows;
-        auto at = [&](int i) { return int64_t(i == 0 ? 2 * b + 1 : 2 * (b + i)) * slot_rows + slot_row; };
-        // the large kernel's rows are stored 8 columns of a half's 128 rows together
-        auto o_at = [&](int i) {
-            if constexpr (SPREAD > 1) return at(i) * D + 4 * lane;
-            return (at(i) - (slot_row & 127)) * D + (lane >> 1) * 1024 + (slot_row & 127) * 8 + 4 * (lane & 1);
-        };
-        // a lane for each piece, 32 at a time; the first 32 (nearly always all) are kept
-        const float2 none = make_float2(-INFINITY, 0.0f), ml = lane < pieces ? ws.ml[at(lane)] : none;
-        float top = ml.x;
-        for (int i = lane + 32; i < pieces; i += 32) top = fmaxf(top, ws.ml[at(i)].x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int i0 = 0; i0 < pieces; i0 += 32) {
-            const float2 x = i0 == 0 ? ml : i0 + lane < pieces ? ws.ml[at(i0 + lane)] : none;
-            const float f = x.x == -INFINITY ? 0.0f : exp2_fast((x.x - top) * sc);
-            sum += x.y * f;
-            const int n = min(pieces - i0, 32);
-#pragma unroll 4
-            for (int i = share; i < n; i += SPREAD) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                if (4 * lane < D) {
-                    const float4 o = *reinterpret_cast<const float4*>(ws.o + o_at(i0 + i));
-                    acc.x = fmaf(o.x, fi, acc.x);
-                    acc.y = fmaf(o.y, fi, acc.y);
-                    acc.z = fmaf(o.z, fi, acc.z);
-                    acc.w = fmaf(o.w, fi, acc.w);
-                }
-            }
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if constexpr (SPREAD > 1) {
-            part[warp][lane] = acc;
-            __syncthreads();
-            if (share == 0) {
-#pragma unroll
-                for (int v = 1; v < SPREAD; ++v) {
-                    const float4 o = part[warp + v][lane];
-                    acc.x += o.x;
-                    acc.y += o.y;
-                    acc.z += o.z;
-                    acc.w += o.w;
-                }
-            }
-            __syncthreads();  // part is read
-        }
-        if (share == 0 && first + warp / SPREAD < s.n_rows) {
-            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            const int token = a.by_group.of(s.row0 + row), t = s.begin + token;
-            const int h = s.head * a.group + s.row0 + row - token * a.group;
-            uint2 packed;
-            packed.x = pack2<BF16>(acc.x * inv, acc.y * inv);
-            packed.y = pack2<BF16>(acc.z * inv, acc.w * inv);
-            if (4 * lane < D)
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_token_stride + h * a.out_head_stride +
-                                          4 * lane) = packed;
-            if (lane == 0 && a.lse != nullptr)
-                a.lse[int64_t(t) * a.q_heads + h] = sum > 0.0f ? top * a.scale + logf(sum) : -INFINITY;
-        }
-    }
+// A row's pieces: block b's slot 1, then slot 0 of the blocks after it.
+__device__ __forceinline__ int piece_slot(int b, int i) { return i == 0 ? 2 * b + 1 : 2 * (b + i); }
+
+template <bool BF16>
+__device__ __forceinline__ void join_store(const AttnArgs& a, const AttnSplit& s, int row, int lane, float4 acc, float top,
+                                           float sum, bool lse) {
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const int token = a.by_group.of(s.row0 + row), t = s.begin + token;
+    const int h = s.head * a.group + s.row0 + row - token * a.group;
+    uint2 packed;
+    packed.x = pack2<BF16>(acc.x * inv, acc.y * inv);
+    packed.y = pack2<BF16>(acc.z * inv, acc.w * inv);
+    if (4 * lane < a.head_dim)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + t * a.out_token_stride + h * a.out_head_stride + 4 * lane) =
+            packed;
+    if (lse && a.lse != nullptr)
+        a.lse[int64_t(t) * a.q_heads + h] = sum > 0.0f ? top * a.scale + logf(sum) : -INFINITY;
 }
 
-template <int SPREAD>
-cudaError_t launch_join(const cudaLaunchConfig_t& cfg, const AttnArgs& a, const AttnWorkspace& ws, int slot_rows,
-                        int half_rows) {
-    return a.bf16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<true, SPREAD>, a, ws, slot_rows, half_rows)
-                  : cudaLaunchKernelEx(&cfg, attention_join_kernel<false, SPREAD>, a, ws, slot_rows, half_rows);
+// Few rows with many pieces (up to one from every block): block (b, y) takes row y of the row tile that block b of the
+// attention kernel began and did not end.  Each warp takes every eighth piece, and the sums meet in shared memory, in an
+// order that depends on the lengths alone.
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_few_rows_kernel(const AttnArgs a, const AttnWorkspace ws) {
+    __shared__ float4 part[kJoinWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, row = blockIdx.y;
+    pdl_wait();
+    const AttnSplit s = ws.split[b];
+    if (s.last_block < 0 || row >= s.n_rows) return;
+    const int pieces = s.last_block - b + 1, D = a.head_dim;
+    const float sc = a.scale * kLog2e;
+    auto at = [&](int i) { return int64_t(piece_slot(b, i)) * kSmallRows + row; };
+    // a lane for each piece, 32 at a time; the first 32 are kept
+    const float2 none = make_float2(-INFINITY, 0.0f), ml = lane < pieces ? ws.ml[at(lane)] : none;
+    float top = ml.x;
+    for (int i = lane + 32; i < pieces; i += 32) top = fmaxf(top, ws.ml[at(i)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+        const float2 x = i0 == 0 ? ml : i0 + lane < pieces ? ws.ml[at(i0 + lane)] : none;
+        const float f = x.x == -INFINITY ? 0.0f : exp2_fast((x.x - top) * sc);
+        sum += x.y * f;
+        const int n = min(pieces - i0, 32);
+#pragma unroll 4
+        for (int i = warp; i < n; i += kJoinWarps) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (4 * lane < D) {
+                const float4 o = *reinterpret_cast<const float4*>(ws.o + at(i0 + i) * D + 4 * lane);
+                acc.x = fmaf(o.x, fi, acc.x);
+                acc.y = fmaf(o.y, fi, acc.y);
+                acc.z = fmaf(o.z, fi, acc.z);
+                acc.w = fmaf(o.w, fi, acc.w);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    part[warp][lane] = acc;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int v = 1; v < kJoinWarps; ++v) {
+        const float4 o = part[v][lane];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+    }
+    join_store<BF16>(a, s, row, lane, acc, top, sum, lane == 0);
+}
+
+// Many rows with few pieces: a warp for four rows next to each other, whose loads are in flight together (one row a warp took
+// 14 us for 152 row tiles of 256 rows and two pieces, all of it latency).  Eight lanes share a row's maxima and sums.
+constexpr int kJoinRows = 4;
+template <bool BF16>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    join_many_rows_kernel(const AttnArgs a, const AttnWorkspace ws, int half_rows) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+    pdl_wait();
+    const AttnSplit s = ws.split[b];
+    const int first = (int(blockIdx.y) * kJoinWarps + warp) * kJoinRows;
+    if (s.last_block < 0 || first >= s.n_rows) return;
+    const int pieces = s.last_block - b + 1, D = a.head_dim;
+    const float sc = a.scale * kLog2e;
+    // a row's place among the 256 of a slot: the halves' rows begin at 0 and 128
+    auto place = [&](int row) {
+        row = min(row, s.n_rows - 1);
+        return row >= half_rows ? 128 + row - half_rows : row;
+    };
+    const int my_place = place(first + (lane >> 3));
+    const float2 none = make_float2(-INFINITY, 0.0f);
+    auto ml_at = [&](int i) { return i < pieces ? ws.ml[int64_t(piece_slot(b, i)) * kChunkRows + my_place] : none; };
+    const float2 ml = ml_at(lane & 7);
+    float top = ml.x;
+    for (int i = (lane & 7) + 8; i < pieces; i += 8) top = fmaxf(top, ml_at(i).x);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = 0.0f;
+    float4 acc[kJoinRows];
+    const float* o[kJoinRows];  // 8 columns of a half's 128 rows are stored together
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+        const int p = place(first + r);
+        acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        o[r] = ws.o + int64_t(p >> 7) * D * 128 + (lane >> 1) * 1024 + (p & 127) * 8 + 4 * (lane & 1);
+    }
+    for (int i0 = 0; i0 < pieces; i0 += 8) {
+        const float2 x = i0 == 0 ? ml : ml_at(i0 + (lane & 7));
+        const float f = x.x == -INFINITY ? 0.0f : exp2_fast((x.x - top) * sc);
+        sum += x.y * f;
+        const int n = min(pieces - i0, 8);
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) {
+            const int64_t off = int64_t(piece_slot(b, i0 + i)) * kChunkRows * D;
+#pragma unroll
+            for (int r = 0; r < kJoinRows; ++r) {
+                const float fi = __shfl_sync(0xffffffffu, f, 8 * r + i);
+                if (4 * lane >= D) continue;
+                const float4 y = *reinterpret_cast<const float4*>(o[r] + off);
+                acc[r].x = fmaf(y.x, fi, acc[r].x);
+                acc[r].y = fmaf(y.y, fi, acc[r].y);
+                acc[r].z = fmaf(y.z, fi, acc[r].z);
+                acc[r].w = fmaf(y.w, fi, acc[r].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+        const float row_top = __shfl_sync(0xffffffffu, top, 8 * r), row_sum = __shfl_sync(0xffffffffu, sum, 8 * r);
+        if (first + r < s.n_rows) join_store<BF16>(a, s, first + r, lane, acc[r], row_top, row_sum, lane == 8 * r);
+    }
 }
 
 int check_attention(const nq_attention* a, const nq_pool* pool) {
@@ -125,6 +173,14 @@ int check_attention(const nq_attention* a, const nq_pool* pool) {
 // the large one's.
 bool few_rows(const nq_attention* a, int group) {
     return int64_t(std::min(a->max_q, a->tokens)) * group <= kSmallRows || group > 128;
+}
+
+// Whether most requests have far fewer rows than the longest: then the small kernel takes those that fit its tile and the
+// large kernel the others.  The large kernel alone spends tiles of 128 rows on single tokens: a chunk of 512 tokens and 31
+// single tokens over 8000 cached (32 heads on 8, head_dim 128, bf16) took it 249 us, and 221 us with both; the second pair
+// of launches costs 8 us where it finds nothing to do (eight prompts of 256 to 2048: 198 and 219 us).
+bool may_mix(const nq_attention* a, int group) {
+    return group <= kSmallRows && 4 * int64_t(a->tokens) < int64_t(a->requests) * a->max_q;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -177,21 +233,35 @@ bool make_query_map(const AttnArgs& a, CUtensorMap* q) {
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int launch_attention_join(const AttnArgs& a, int slot_rows, int half_rows) {
-    const AttnWorkspace ws = attn_workspace(a.workspace, slot_rows, a.head_dim);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+namespace {
+cudaLaunchConfig_t join_config(const AttnArgs& a, int rows, int rows_per_block, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const bool few = slot_rows <= kSmallRows;
-    const int64_t rows = std::min<int64_t>(int64_t(a.tokens) * a.group, few ? kSmallRows : 2 * half_rows);
-    cfg.gridDim = dim3(kAttnGrid, unsigned(few ? rows : (rows + kJoinWarps - 1) / kJoinWarps));
+    rows = int(std::min<int64_t>(int64_t(a.tokens) * a.group, rows));
+    cfg.gridDim = dim3(kAttnGrid, unsigned((rows + rows_per_block - 1) / rows_per_block));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = a.stream;
-    cfg.attrs = &attr;
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = few ? launch_join<kJoinWarps>(cfg, a, ws, slot_rows, half_rows)
-                              : launch_join<1>(cfg, a, ws, slot_rows, half_rows);
+    return cfg;
+}
+}  // namespace
+
+int launch_join_few_rows(const AttnArgs& a, const AttnWorkspace& ws) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = join_config(a, kSmallRows, 1, &attr);
+    const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, join_few_rows_kernel<true>, a, ws)
+                                 : cudaLaunchKernelEx(&cfg, join_few_rows_kernel<false>, a, ws);
+    return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+}
+
+int launch_join_many_rows(const AttnArgs& a, const AttnWorkspace& ws) {
+    cudaLaunchAttribute attr;
+    const int half_rows = a.half_tokens * a.group;
+    const cudaLaunchConfig_t cfg = join_config(a, 2 * half_rows, kJoinWarps * kJoinRows, &attr);
+    const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, join_many_rows_kernel<true>, a, ws, half_rows)
+                                 : cudaLaunchKernelEx(&cfg, join_many_rows_kernel<false>, a, ws, half_rows);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
@@ -204,8 +274,9 @@ int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uin
     if (st != NQ_OK) return st;
     if (!bytes) return NQ_ERR_ARG;
     const int group = a->q_heads / pool->kv_heads;
-    *bytes = nq::few_rows(a, group) ? nq::attn_workspace(nullptr, nq::kSmallRows, pool->head_dim).total
-                                    : nq::chunk_workspace(a->tokens, group, a->requests, pool->head_dim);
+    // the large kernel's calls may be mixed; their size is the larger one in any case
+    *bytes = nq::attn_workspace(nullptr, nq::kSmallRows, pool->head_dim).total;
+    if (!nq::few_rows(a, group)) *bytes += nq::chunk_workspace(a->tokens, group, a->requests, pool->head_dim);
     return NQ_OK;
 }
 
@@ -267,9 +338,16 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
                   (a->q_heads == 1 || a->out_head_stride % 16 == 0);
     x.by_group = nq::FastDiv::by(uint32_t(x.group));
     x.half_tokens = 128 / x.group;
+    x.mixed = 0;
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
-    return nq::few_rows(a, x.group) ? nq::launch_attention_small(x) : nq::launch_attention_chunk(x);
+    if (nq::few_rows(a, x.group)) return nq::launch_attention_small(x);
+    if (nq::may_mix(a, x.group)) {
+        x.mixed = 1;
+        const int small = nq::launch_attention_small(x);
+        if (small != NQ_OK) return small;
+    }
+    return nq::launch_attention_chunk(x);
 }
 
 }  // extern "C"

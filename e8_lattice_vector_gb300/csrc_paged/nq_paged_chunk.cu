@@ -75,6 +75,7 @@ inline ChunkPlan chunk_plan(char* p, int64_t pairs, uint64_t* total) {
 }
 
 __device__ __forceinline__ int row_tiles_of(const AttnArgs& a, const Request& q) {
+    if (a.mixed && q.n * a.group <= kSmallRows) return 0;  // the small kernel's
     return (q.n + 2 * a.half_tokens - 1) / (2 * a.half_tokens);
 }
 
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int count = h ? w.count[1] : w.count[0];
             if (count == 0) continue;
             const int first = w.shared ? 0 : h * a.half_tokens, n_tokens = min(w.n - first, a.half_tokens);
-            const bool mine = row_token < n_tokens;
+            const bool mine = row_token < n_tokens, busy = __any_sync(0xffffffffu, mine);  // no rows: nothing to take exponentials of
             const int token = first + min(row_token, n_tokens - 1), head = w.head * a.group + row_head;
             const int lo = keys_from(a, w.pos + token), hi = keys_to(a, w.kv, w.pos + token);
             // keys [all_lo, all_hi) are seen by every row of the half
@@ -754,6 +755,11 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const int i = w.shared ? 2 * j + h : j;  // of the piece's tiles
                 const int key0 = w.key0 + i * kKeyTile;
                 wait(c.s_full[h], n_s & 1);
+                if (!busy) {
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(smem_ptr(&c.p_full[h]));
+                    continue;
+                }
                 const uint32_t live = *(volatile uint32_t*)&c.live[(tiles + i) % kLiveRing];
                 float s[kKeyTile];
                 float tops[4];  // four chains: one would be all latency
@@ -966,14 +972,15 @@ uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim) 
 int launch_attention_chunk(const AttnArgs& a) {
     CUtensorMap km, vm, qm;
     if (!make_pool_maps(a, &km, &vm) || !make_query_map(a, &qm)) return NQ_ERR_CUDA;
-    const AttnWorkspace ws = attn_workspace(a.workspace, kChunkRows, a.head_dim);
+    char* base = static_cast<char*>(a.workspace) + (a.mixed ? attn_workspace(nullptr, kSmallRows, a.head_dim).total : 0);
+    const AttnWorkspace ws = attn_workspace(base, kChunkRows, a.head_dim);
     uint64_t bytes = 0;
     const int64_t pairs = chunk_pairs(a.tokens, a.half_tokens, a.requests);
-    const ChunkPlan plan = chunk_plan(static_cast<char*>(a.workspace) + ws.total, pairs, &bytes);
+    const ChunkPlan plan = chunk_plan(base + ws.total, pairs, &bytes);
     attention_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a, plan, pairs);
     if (cudaGetLastError() != cudaSuccess) return NQ_ERR_CUDA;
     const int st = a.bf16 ? launch_chunk<true>(a, km, vm, qm, ws, plan) : launch_chunk<false>(a, km, vm, qm, ws, plan);
-    return st == NQ_OK ? launch_attention_join(a, kChunkRows, a.half_tokens * a.group) : st;
+    return st == NQ_OK ? launch_join_many_rows(a, ws) : st;
 }
 
 int chunk_gave_up(int* seen) {

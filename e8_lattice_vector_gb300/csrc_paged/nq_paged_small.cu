@@ -78,6 +78,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const Request& q) {
     Span s;
     s.row_tiles = (q.n * a.group + kSmallRows - 1) / kSmallRows;
+    if (a.mixed && s.row_tiles > 1) s.row_tiles = 0;  // the large kernel's
     const int lo = min(keys_from(a, q.kv - q.n), q.kv);
     s.first = lo / kKeyTile;
     s.count = max((q.kv + kKeyTile - 1) / kKeyTile - s.first, 1);
@@ -491,7 +492,7 @@ int launch_attention_small(const AttnArgs& a) {
     if (!make_pool_maps(a, &km, &vm)) return NQ_ERR_CUDA;
     const AttnWorkspace ws = attn_workspace(a.workspace, kSmallRows, a.head_dim);
     const int st = a.bf16 ? launch_small<true>(a, km, vm, ws) : launch_small<false>(a, km, vm, ws);
-    return st == NQ_OK ? launch_attention_join(a, kSmallRows, kSmallRows) : st;
+    return st == NQ_OK ? launch_join_few_rows(a, ws) : st;
 }
 
 int small_gave_up(int* seen) {
