@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_few_rows_kernel(const At
     join_store<BF16>(a, s, row, lane, acc, top, sum, lane == 0);
 }
 
-// Many rows with few pieces: a warp for four rows next to each other, whose loads are in flight together (one row a warp took
-// 14 us for 152 row tiles of 256 rows and two pieces, all of it latency).  Eight lanes share a row's maxima and sums.
-constexpr int kJoinRows = 4;
+// Many rows with few pieces: a warp for two rows next to each other, whose loads are in flight together (one row a warp took
+// 14 us for 152 row tiles of 256 rows and two pieces, all of it latency).  Sixteen lanes share a row's maxima and sums.
+constexpr int kJoinRows = 1, kJoinLanes = 32 / kJoinRows;
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     join_many_rows_kernel(const AttnArgs a, const AttnWorkspace ws, int half_rows) {
@@ -105,14 +105,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         row = min(row, s.n_rows - 1);
         return row >= half_rows ? 128 + row - half_rows : row;
     };
-    const int my_place = place(first + (lane >> 3));
+    const int my_place = place(first + lane / kJoinLanes);
     const float2 none = make_float2(-INFINITY, 0.0f);
     auto ml_at = [&](int i) { return i < pieces ? ws.ml[int64_t(piece_slot(b, i)) * kChunkRows + my_place] : none; };
-    const float2 ml = ml_at(lane & 7);
+    const float2 ml = ml_at(lane % kJoinLanes);
     float top = ml.x;
-    for (int i = (lane & 7) + 8; i < pieces; i += 8) top = fmaxf(top, ml_at(i).x);
+    for (int i = lane % kJoinLanes + kJoinLanes; i < pieces; i += kJoinLanes) top = fmaxf(top, ml_at(i).x);
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    for (int d = kJoinLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     float sum = 0.0f;
     float4 acc[kJoinRows];
     const float* o[kJoinRows];  // 8 columns of a half's 128 rows are stored together
@@ -122,17 +122,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         o[r] = ws.o + int64_t(p >> 7) * D * 128 + (lane >> 1) * 1024 + (p & 127) * 8 + 4 * (lane & 1);
     }
-    for (int i0 = 0; i0 < pieces; i0 += 8) {
-        const float2 x = i0 == 0 ? ml : ml_at(i0 + (lane & 7));
+    for (int i0 = 0; i0 < pieces; i0 += kJoinLanes) {
+        const float2 x = i0 == 0 ? ml : ml_at(i0 + lane % kJoinLanes);
         const float f = x.x == -INFINITY ? 0.0f : exp2_fast((x.x - top) * sc);
         sum += x.y * f;
-        const int n = min(pieces - i0, 8);
-#pragma unroll 2
+        const int n = min(pieces - i0, kJoinLanes);
+#pragma unroll 4
         for (int i = 0; i < n; ++i) {
             const int64_t off = int64_t(piece_slot(b, i0 + i)) * kChunkRows * D;
 #pragma unroll
             for (int r = 0; r < kJoinRows; ++r) {
-                const float fi = __shfl_sync(0xffffffffu, f, 8 * r + i);
+                const float fi = __shfl_sync(0xffffffffu, f, kJoinLanes * r + i);
                 if (4 * lane >= D) continue;
                 const float4 y = *reinterpret_cast<const float4*>(o[r] + off);
                 acc[r].x = fmaf(y.x, fi, acc[r].x);
@@ -143,11 +143,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         }
     }
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    for (int d = kJoinLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
 #pragma unroll
     for (int r = 0; r < kJoinRows; ++r) {
-        const float row_top = __shfl_sync(0xffffffffu, top, 8 * r), row_sum = __shfl_sync(0xffffffffu, sum, 8 * r);
-        if (first + r < s.n_rows) join_store<BF16>(a, s, first + r, lane, acc[r], row_top, row_sum, lane == 8 * r);
+        const float row_top = __shfl_sync(0xffffffffu, top, kJoinLanes * r), row_sum = __shfl_sync(0xffffffffu, sum, kJoinLanes * r);
+        if (first + r < s.n_rows) join_store<BF16>(a, s, first + r, lane, acc[r], row_top, row_sum, lane == kJoinLanes * r);
     }
 }
 

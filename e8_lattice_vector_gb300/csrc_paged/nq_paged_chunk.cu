@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll 1
                     for (int is_v = 0; is_v < 2; ++is_v, ++n, at.step()) {
                         if (n >= STAGES)
-                            go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.empty[at.stage]), at.phase ^ 1, &c.gave_up));
+                            go = __all_sync(0xffffffffu, mbar_wait<true>(smem_ptr(&c.empty[at.stage]), at.phase ^ 1, &c.gave_up));
                         if (!go) break;
                         const uint32_t full = smem_ptr(is_v ? &c.v_full[tile.stage] : &c.k_full[tile.stage]);
                         if (lane == 0) {
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             while (go && next_piece(piece_at, w, false)) {
                 for (int i = 0; go && i < w.take; ++i, tile.step()) {
                     at.step();  // past K
-                    go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.v_full[tile.stage]), tile.phase, &c.gave_up));
+                    go = __all_sync(0xffffffffu, mbar_wait<true>(smem_ptr(&c.v_full[tile.stage]), tile.phase, &c.gave_up));
                     const int key0 = w.key0 + i * kKeyTile;
                     const uint32_t live = *(volatile uint32_t*)&c.live[tile.stage];
                     if (key0 < w.lo || key0 + kKeyTile > w.hi || live != all) {
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             bool go = true;
             for (int n = 0; go; ++n) {
                 if (n >= kPieceRing)
-                    go = mbar_wait(smem_ptr(&c.piece_free[piece_at.stage]), piece_at.phase ^ 1, &c.gave_up);
+                    go = mbar_wait<true>(smem_ptr(&c.piece_free[piece_at.stage]), piece_at.phase ^ 1, &c.gave_up);
                 if (!go) break;
                 if (x.left <= 0) w.take = 0;
                 if (x.left > 0) {
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     if (w.count[h] == 0) break;
                     // As soon as the piece's last scores are there its Q is not read any more: the next one's loads run beside
                     // the last tile's exponentials, its product and the results.
-                    if (pieces[h] > 0) go = go && mbar_wait(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up);
+                    if (pieces[h] > 0) go = go && mbar_wait<true>(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up);
                     if (!go) break;
                     ++pieces[h];
                     const uint32_t full = smem_ptr(&c.q_full[h]);
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int count = h ? w.count[1] : w.count[0];
             if (count == 0) continue;
             const int first = w.shared ? 0 : h * a.half_tokens, n_tokens = min(w.n - first, a.half_tokens);
-            const bool mine = row_token < n_tokens, busy = __any_sync(0xffffffffu, mine);  // no rows: nothing to take exponentials of
+            const bool mine = row_token < n_tokens;
             const int token = first + min(row_token, n_tokens - 1), head = w.head * a.group + row_head;
             const int lo = keys_from(a, w.pos + token), hi = keys_to(a, w.kv, w.pos + token);
             // keys [all_lo, all_hi) are seen by every row of the half
@@ -755,35 +755,34 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const int i = w.shared ? 2 * j + h : j;  // of the piece's tiles
                 const int key0 = w.key0 + i * kKeyTile;
                 wait(c.s_full[h], n_s & 1);
-                if (!busy) {
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive(smem_ptr(&c.p_full[h]));
-                    continue;
-                }
                 const uint32_t live = *(volatile uint32_t*)&c.live[(tiles + i) % kLiveRing];
-                float s[kKeyTile];
-                float tops[4];  // four chains: one would be all latency
-#pragma unroll
-                for (int x0 = 0; x0 < kKeyTile; x0 += 64) {
-                    tm_load(s + x0, s_at + x0);
-                    tm_load(s + x0 + 32, s_at + x0 + 32);
-                }
-                tm_wait<kKeyTile>(s);
                 if (key0 < all_lo || key0 + kKeyTile > all_hi || live != all) {
+                    // Keys that the row does not see, in place.  This and the other rare parts are loops over 16 columns in tensor
+                    // memory: unrolled over registers they would push the common part out of the instruction caches.
                     const int from = lo - key0, to = hi - key0;
+#pragma unroll 1
+                    for (int x = 0; x < kKeyTile; x += 16) {
+                        const bool page = live >> (x >> a.page_shift) & 1u;
+                        const uint32_t see = page ? low_bits(to - x) & ~low_bits(from - x) : 0u;
+                        if (__all_sync(0xffffffffu, (see & 0xffffu) == 0xffffu)) continue;
+                        float y[16];
+                        tm_load16(y, s_at + x);
+                        tm_wait<16>(y);
 #pragma unroll
-                    for (int x0 = 0; x0 < kKeyTile; x0 += 32) {
-                        // a bit for each of 32 keys that this row sees
-                        uint32_t see = low_bits(to - x0) & ~low_bits(from - x0);
-                        const int shift = a.page_shift;
-                        if (!(live >> (x0 >> shift) & 1u)) see &= shift == 4 ? 0xffff0000u : 0u;
-                        if (shift == 4 && !(live >> ((x0 >> 4) + 1) & 1u)) see &= 0xffffu;
-                        if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            if (!(see & 1u << x)) s[x0 + x] = -INFINITY;
+                        for (int z = 0; z < 16; ++z)
+                            if (!(see & 1u << z)) y[z] = -INFINITY;
+                        tm_store16(s_at + x, reinterpret_cast<const uint32_t*>(y));
                     }
+                    tc_wait_st();
                 }
+                float s[kKeyTile];
+                auto load_scores = [&] {
+#pragma unroll
+                    for (int x = 0; x < kKeyTile; x += 32) tm_load(s + x, s_at + x);
+                    tm_wait<kKeyTile>(s);
+                };
+                load_scores();
+                float tops[4];  // four chains: one would be all latency
 #pragma unroll
                 for (int x = 0; x < 4; ++x) tops[x] = fmaxf(s[2 * x], s[2 * x + 1]);
 #pragma unroll
@@ -799,7 +798,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         const float f = moves && m != -INFINITY ? exp2_fast(__fmaf_rn(m - m_new, sc, rest_new - rest)) : 1.0f;
                         wait(c.o_full[h], (n_s - 1) & 1);  // the previous product has added to O
                         l *= f;
-#pragma unroll
+#pragma unroll 1
                         for (int x = 0; x < D; x += 16) {
                             float o[16];
                             tm_load16(o, o_at + x);
@@ -819,8 +818,17 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 }
                 if (__any_sync(0xffffffffu, far)) {  // a reference too large for one fp32 number: subtract first
                     const float by = far ? m : 0.0f;
+#pragma unroll 1
+                    for (int x = 0; x < kKeyTile; x += 16) {
+                        float y[16];
+                        tm_load16(y, s_at + x);
+                        tm_wait<16>(y);
 #pragma unroll
-                    for (int x = 0; x < kKeyTile; ++x) s[x] -= by;
+                        for (int z = 0; z < 16; ++z) y[z] -= by;
+                        tm_store16(s_at + x, reinterpret_cast<const uint32_t*>(y));
+                    }
+                    tc_wait_st();
+                    load_scores();
                 }
                 const float2 neg2 = make_float2(neg, neg), cc = make_float2(sc, sc);
                 float2 sums[4];
@@ -881,45 +889,48 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             }
             const int piece = (2 * blockIdx.x + w.slot) * 2 + h;  // a piece's half in the workspace
             uint16_t* out = static_cast<uint16_t*>(a.out) + int64_t(w.row + token) * a.out_token_stride + head * a.out_head_stride;
-            float o[D];
+#pragma unroll 1
+            for (int x0 = 0; x0 < D; x0 += 32) {
+                float o[32];
+                tm_load(o, o_at + x0);
+                tm_wait<32>(o);
 #pragma unroll
-            for (int x = 0; x < D; x += 32) tm_load(o + x, o_at + x);
-            tm_wait<D>(o);
+                for (int x = 0; x < 32; ++x) o[x] *= to_m;
+                if (both) {
+                    float o1[32];
+                    tm_load(o1, o_at + 128 + x0);
+                    tm_wait<32>(o1);
 #pragma unroll
-            for (int x = 0; x < D; ++x) o[x] *= to_m;
-            if (both) {
-#pragma unroll
-                for (int x0 = 0; x0 < D; x0 += 16) {
-                    float o1[16];
-                    tm_load16(o1, o_at + 128 + x0);
-                    tm_wait<16>(o1);
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) o[x0 + x] = __fmaf_rn(o1[x], to_other, o[x0 + x]);
+                    for (int x = 0; x < 32; ++x) o[x] = __fmaf_rn(o1[x], to_other, o[x]);
                 }
+                if (mine && whole) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 16) {
+                        uint32_t p[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) p[y] = pack2<BF16>(o[x + 2 * y], o[x + 2 * y + 1]);
+                        if (a.out_by_32) {
+                            store32(out + x0 + x, p);
+                        } else {
+                            *reinterpret_cast<uint4*>(out + x0 + x) = make_uint4(p[0], p[1], p[2], p[3]);
+                            *reinterpret_cast<uint4*>(out + x0 + x + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+                        }
+                    }
+                } else if (mine) {
+                    // 8 columns of the 128 rows together, so that a warp writes 1 KB in one piece
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8)
+                        store32(ws.o + (int64_t(piece) * D + x0 + x) * 128 + row * 8, reinterpret_cast<const uint32_t*>(o + x));
+                }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (both && lane == 0) mbar_arrive(smem_ptr(&c.merge_free));
             if (mine && whole) {
-#pragma unroll
-                for (int x = 0; x < D; x += 16) {
-                    uint32_t p[8];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) p[y] = pack2<BF16>(o[x + 2 * y], o[x + 2 * y + 1]);
-                    if (a.out_by_32) {
-                        store32(out + x, p);
-                    } else {
-                        *reinterpret_cast<uint4*>(out + x) = make_uint4(p[0], p[1], p[2], p[3]);
-                        *reinterpret_cast<uint4*>(out + x + 8) = make_uint4(p[4], p[5], p[6], p[7]);
-                    }
-                }
                 if (a.lse != nullptr)
                     a.lse[int64_t(w.row + token) * a.q_heads + head] = l > 0.0f ? m * a.scale + logf(l) : -INFINITY;
             } else if (mine) {
-                // 8 columns of the 128 rows together, so that a warp writes 1 KB in one piece
-#pragma unroll
-                for (int x = 0; x < D; x += 8)
-                    store32(ws.o + (int64_t(piece) * D + x) * 128 + row * 8, reinterpret_cast<const uint32_t*>(o + x));
                 ws.ml[piece * 128 + row] = make_float2(m, l);
             }
             __syncwarp();
