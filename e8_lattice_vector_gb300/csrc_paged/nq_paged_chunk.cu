@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll 1
                     for (int is_v = 0; is_v < 2; ++is_v, ++n, at.step()) {
                         if (n >= STAGES)
-                            go = __all_sync(0xffffffffu, mbar_wait<true>(smem_ptr(&c.empty[at.stage]), at.phase ^ 1, &c.gave_up));
+                            go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.empty[at.stage]), at.phase ^ 1, &c.gave_up));
                         if (!go) break;
                         const uint32_t full = smem_ptr(is_v ? &c.v_full[tile.stage] : &c.k_full[tile.stage]);
                         if (lane == 0) {
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             while (go && next_piece(piece_at, w, false)) {
                 for (int i = 0; go && i < w.take; ++i, tile.step()) {
                     at.step();  // past K
-                    go = __all_sync(0xffffffffu, mbar_wait<true>(smem_ptr(&c.v_full[tile.stage]), tile.phase, &c.gave_up));
+                    go = __all_sync(0xffffffffu, mbar_wait(smem_ptr(&c.v_full[tile.stage]), tile.phase, &c.gave_up));
                     const int key0 = w.key0 + i * kKeyTile;
                     const uint32_t live = *(volatile uint32_t*)&c.live[tile.stage];
                     if (key0 < w.lo || key0 + kKeyTile > w.hi || live != all) {
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             bool go = true;
             for (int n = 0; go; ++n) {
                 if (n >= kPieceRing)
-                    go = mbar_wait<true>(smem_ptr(&c.piece_free[piece_at.stage]), piece_at.phase ^ 1, &c.gave_up);
+                    go = mbar_wait(smem_ptr(&c.piece_free[piece_at.stage]), piece_at.phase ^ 1, &c.gave_up);
                 if (!go) break;
                 if (x.left <= 0) w.take = 0;
                 if (x.left > 0) {
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     if (w.count[h] == 0) break;
                     // As soon as the piece's last scores are there its Q is not read any more: the next one's loads run beside
                     // the last tile's exponentials, its product and the results.
-                    if (pieces[h] > 0) go = go && mbar_wait<true>(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up);
+                    if (pieces[h] > 0) go = go && mbar_wait(smem_ptr(&c.q_free[h]), (pieces[h] - 1) & 1, &c.gave_up);
                     if (!go) break;
                     ++pieces[h];
                     const uint32_t full = smem_ptr(&c.q_full[h]);

@@ -31,28 +31,17 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// PATIENT: suspended for longer at a time.  A waiting warp that comes back to look takes issue slots from the ones that
-// compute (loads and clearing, waiting so, cost the large kernel 5%); one whose wait the next product depends on wakes later
-// from a long suspension and should not use it.
-template <bool PATIENT>
+// Suspended for up to a millisecond at a time: a waiting warp that comes back to look takes issue slots from the ones that
+// compute (with the default limit the large kernel took 3 to 7% longer).
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    if constexpr (PATIENT)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ uint64_t global_ns() {
@@ -66,12 +55,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Waits for the phase of `parity` to end.  When it does not, or when another thread of the block has given up
 // (*gave_up), returns false at once; the caller goes on without its data, so that all barriers of the block are still passed.
-template <bool PATIENT = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-    if (mbar_try<PATIENT>(bar, parity)) return true;
+    if (mbar_try(bar, parity)) return true;
     uint64_t since = 0;
     for (int i = 0;; ++i) {
-        if (mbar_try<PATIENT>(bar, parity)) return true;
+        if (mbar_try(bar, parity)) return true;
         if ((i & 15) != 15) continue;
         if (*gave_up) return false;
         const uint64_t now = global_ns();
