@@ -596,3 +596,30 @@ def test_attention_many_pieces_in_every_block(nq, dtype, D, window, new):
     rng = np.random.default_rng(new)
     lens = [(int(c), int(n)) for c, n in zip(rng.integers(300, 2500, 60), rng.integers(1, new + 1, 60))]
     Step(lens, 16, 4, D, 32, dtype, seed=new).check(nq, window=window)
+
+
+@pytest.mark.parametrize("config,kw", [("tiny", {"steps": 3, "new": 1}), ("tiny", {"steps": 2, "new": 20, "page_size": 32}),
+                                       ("phi3mini", {"layers": 2, "tokens": 300, "q_heads": 32, "steps": 2, "new": 3})])
+def test_serving_from_a_compressed_cache(nq, config, kw):
+    """Compressed, decompressed, paged and attended to: the outputs differ from those over the original cache, by less than
+    the values do (three bits for keys and two for values leave about a quarter of a value's size as noise)."""
+    from e8_lattice_vector_gb300.serve import serve
+    from e8_lattice_vector_gb300.synth import CONFIGS
+
+    r = serve(CONFIGS[config], **kw)
+    assert 0.01 < r["attention_rel_error"] < 1.0 and 0.1 < r["compressed_share"] < 0.3
+    nq.paged_status()
+
+
+def test_paged_pools_hold_what_was_decompressed(nq):
+    """fill() puts every row of a decompressed cache where the table says."""
+    from e8_lattice_vector_gb300.serve import PagedCache
+
+    K, V = (torch.randn(2, 3, 2, 70, 64, device=DEV).half() for _ in range(2))
+    c = PagedCache(2, 3, 2, 64, 16, 80, torch.float16, torch.device(DEV, 0))
+    c.fill(K, V)
+    for pool, src in ((c.K, K), (c.V, V)):
+        for r in range(3):
+            for t in (0, 15, 16, 69):
+                page = int(c.table[r, t // 16])
+                assert torch.equal(pool[:, page, :, t % 16], src[:, r, :, t])
