@@ -99,15 +99,21 @@ __global__ void __launch_bounds__(kMapThreads)
         tile += (long long)((int(blockIdx.x) - int(tile % gridDim.x) + int(gridDim.x)) % int(gridDim.x));
         for (; tile * kMapThreads < end; tile += gridDim.x) {
             const long long i = tile * kMapThreads + threadIdx.x;
+            // the last request that starts at or before a row; the tile's first row's is every row's in a long prompt
+            const int n = min(kMapThreads, requests - r0);
+            auto request_of = [&](long long row, int lo) {
+                for (int hi = n; hi - lo > 1;) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_start[mid] <= row)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                return lo;
+            };
+            int lo = request_of(max(tile * kMapThreads, row0), 0);
             if (i < row0 || i >= end) continue;
-            int lo = 0, hi = min(kMapThreads, requests - r0);  // the last request that starts at or before row i
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_start[mid] <= i)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
+            if (lo + 1 < n && s_start[lo + 1] <= i) lo = request_of(i, lo);
             const long long pos = s_ctx[lo] + (i - s_start[lo]);
             const long long col = pos >> page_shift;
             const int off = int(pos) & (P - 1);
