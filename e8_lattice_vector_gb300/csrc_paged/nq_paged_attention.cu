@@ -87,68 +87,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_few_rows_kernel(const At
     join_store<BF16>(a, s, row, lane, acc, top, sum, lane == 0);
 }
 
-// Many rows with few pieces: a warp for two rows next to each other, whose loads are in flight together (one row a warp took
-// 14 us for 152 row tiles of 256 rows and two pieces, all of it latency).  Sixteen lanes share a row's maxima and sums.
-constexpr int kJoinRows = 1, kJoinLanes = 32 / kJoinRows;
+// Many rows with few pieces: a warp for a row.  (Two or four rows a warp, their loads in flight together, were 2 us faster for 152
+// row tiles of two pieces each and 3 to 6 us slower for 16 row tiles of ten.)  152 row tiles of 256 rows and two to three
+// pieces take 14 us, 4.5 TB/s, nearly all of it out of the L2.
 template <bool BF16>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     join_many_rows_kernel(const AttnArgs a, const AttnWorkspace ws, int half_rows) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
     pdl_wait();
     const AttnSplit s = ws.split[b];
-    const int first = (int(blockIdx.y) * kJoinWarps + warp) * kJoinRows;
-    if (s.last_block < 0 || first >= s.n_rows) return;
+    const int row = int(blockIdx.y) * kJoinWarps + warp;
+    if (s.last_block < 0 || row >= s.n_rows) return;
     const int pieces = s.last_block - b + 1, D = a.head_dim;
     const float sc = a.scale * kLog2e;
-    // a row's place among the 256 of a slot: the halves' rows begin at 0 and 128
-    auto place = [&](int row) {
-        row = min(row, s.n_rows - 1);
-        return row >= half_rows ? 128 + row - half_rows : row;
-    };
-    const int my_place = place(first + lane / kJoinLanes);
+    const int place = row >= half_rows ? 128 + row - half_rows : row;  // among the 256 of a slot: the halves begin at 0 and 128
     const float2 none = make_float2(-INFINITY, 0.0f);
-    auto ml_at = [&](int i) { return i < pieces ? ws.ml[int64_t(piece_slot(b, i)) * kChunkRows + my_place] : none; };
-    const float2 ml = ml_at(lane % kJoinLanes);
+    auto ml_at = [&](int i) { return i < pieces ? ws.ml[int64_t(piece_slot(b, i)) * kChunkRows + place] : none; };
+    const float2 ml = ml_at(lane);
     float top = ml.x;
-    for (int i = lane % kJoinLanes + kJoinLanes; i < pieces; i += kJoinLanes) top = fmaxf(top, ml_at(i).x);
+    for (int i = lane + 32; i < pieces; i += 32) top = fmaxf(top, ml_at(i).x);
 #pragma unroll
-    for (int d = kJoinLanes / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    // 8 columns of a half's 128 rows are stored together
+    const float* o = ws.o + int64_t(place >> 7) * D * 128 + (lane >> 1) * 1024 + (place & 127) * 8 + 4 * (lane & 1);
     float sum = 0.0f;
-    float4 acc[kJoinRows];
-    const float* o[kJoinRows];  // 8 columns of a half's 128 rows are stored together
-#pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) {
-        const int p = place(first + r);
-        acc[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        o[r] = ws.o + int64_t(p >> 7) * D * 128 + (lane >> 1) * 1024 + (p & 127) * 8 + 4 * (lane & 1);
-    }
-    for (int i0 = 0; i0 < pieces; i0 += kJoinLanes) {
-        const float2 x = i0 == 0 ? ml : ml_at(i0 + lane % kJoinLanes);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+        const float2 x = i0 == 0 ? ml : ml_at(i0 + lane);
         const float f = x.x == -INFINITY ? 0.0f : exp2_fast((x.x - top) * sc);
         sum += x.y * f;
-        const int n = min(pieces - i0, kJoinLanes);
+        const int n = min(pieces - i0, 32);
 #pragma unroll 4
         for (int i = 0; i < n; ++i) {
-            const int64_t off = int64_t(piece_slot(b, i0 + i)) * kChunkRows * D;
-#pragma unroll
-            for (int r = 0; r < kJoinRows; ++r) {
-                const float fi = __shfl_sync(0xffffffffu, f, kJoinLanes * r + i);
-                if (4 * lane >= D) continue;
-                const float4 y = *reinterpret_cast<const float4*>(o[r] + off);
-                acc[r].x = fmaf(y.x, fi, acc[r].x);
-                acc[r].y = fmaf(y.y, fi, acc[r].y);
-                acc[r].z = fmaf(y.z, fi, acc[r].z);
-                acc[r].w = fmaf(y.w, fi, acc[r].w);
-            }
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (4 * lane >= D) continue;
+            const float4 y = *reinterpret_cast<const float4*>(o + int64_t(piece_slot(b, i0 + i)) * kChunkRows * D);
+            acc.x = fmaf(y.x, fi, acc.x);
+            acc.y = fmaf(y.y, fi, acc.y);
+            acc.z = fmaf(y.z, fi, acc.z);
+            acc.w = fmaf(y.w, fi, acc.w);
         }
     }
 #pragma unroll
-    for (int d = kJoinLanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-#pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) {
-        const float row_top = __shfl_sync(0xffffffffu, top, kJoinLanes * r), row_sum = __shfl_sync(0xffffffffu, sum, kJoinLanes * r);
-        if (first + r < s.n_rows) join_store<BF16>(a, s, first + r, lane, acc[r], row_top, row_sum, lane == kJoinLanes * r);
-    }
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    join_store<BF16>(a, s, row, lane, acc, top, sum, lane == 0);
 }
 
 int check_attention(const nq_attention* a, const nq_pool* pool) {
@@ -259,7 +241,7 @@ int launch_join_few_rows(const AttnArgs& a, const AttnWorkspace& ws) {
 int launch_join_many_rows(const AttnArgs& a, const AttnWorkspace& ws) {
     cudaLaunchAttribute attr;
     const int half_rows = a.half_tokens * a.group;
-    const cudaLaunchConfig_t cfg = join_config(a, 2 * half_rows, kJoinWarps * kJoinRows, &attr);
+    const cudaLaunchConfig_t cfg = join_config(a, 2 * half_rows, kJoinWarps, &attr);
     const cudaError_t e = a.bf16 ? cudaLaunchKernelEx(&cfg, join_many_rows_kernel<true>, a, ws, half_rows)
                                  : cudaLaunchKernelEx(&cfg, join_many_rows_kernel<false>, a, ws, half_rows);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;

@@ -15,6 +15,16 @@
 //
 // Shares: the row tiles' key tiles, in order, in equal parts over 152 blocks; a launch of one block finds where each part
 // begins.  Row tiles that end up in several blocks are joined by a second launch.
+//
+// Measured (32 query heads on 8 KV heads, head_dim 128, 2000 tokens over 30000 cached): fp16 676 us, 1504 TFLOP/s, 81% of the
+// measured cuBLAS rate; bf16 920 us, 1104 TFLOP/s.  What bounds it is the chain of one half: its exponentials (about 1200 of 3000
+// cycles a tile), its two products (1024, 1536 in bf16) and the hand-overs between them, with the tensor cores busy 68% (bf16: 73%)
+// of the time under the profiler.  Taking the exponentials before the maximum is known, or starting the second product with
+// half of P, shortened the chain and took as long or longer.
+//
+// In bf16 P is the sum of two bf16 (hi + lo), each with its own product: one bf16 has 2^-8 of p as its rounding error, as much as
+// the output's own, and fp16 tensors, whose P has 2^-11, show that the second product costs 36% of the time.  It is the
+// price of an output that is off by its own rounding and nothing else.
 #include "nq_paged_device.cuh"
 
 namespace nq {
@@ -22,7 +32,7 @@ namespace {
 
 __device__ int g_gave_up;  // set when a wait was given up
 
-constexpr int kThreadsChunk = 384;  // two warpgroups for the halves; load, product and two spare warps
+constexpr int kThreadsChunk = 384;  // two warpgroups for the halves; loads, products, clearing, pieces and Q
 constexpr int kPlanThreads = 1024;
 constexpr float kSlack = 8.0f;  // in powers of two
 constexpr float kExactRef = 1048576.0f;  // references up to 2^20: off by 2^-5 from m sc at most
@@ -125,8 +135,7 @@ __device__ __forceinline__ long long plan_scan(long long x, long long* total) {
 // pairs that the arrays hold, all there are unless row starts decrease.
 //
 // The order is request, KV head, row tile: the row tiles that read the same keys come one after the other, in a block and in
-// its neighbours, and find them in the L2 (row tiles outside heads, eight prompts of 2048 with 32 KV heads of 96 read 727 MB
-// from memory instead of HEAD_MAJOR_MB).
+// its neighbours, and find them in the L2 (with row tiles outside heads 2000 tokens over 30000 cached took 691 us, now 676).
 __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const AttnArgs a, const ChunkPlan plan, long long room) {
     __shared__ int s_pair[kPlanThreads];
     pdl_trigger();
