@@ -31,7 +31,7 @@ inline int check_pool(const nq_pool* p) {
     if (p->dtype != NQ_F16 && p->dtype != NQ_BF16) return NQ_ERR_UNSUPPORTED;
     if (p->head_dim != 64 && p->head_dim != 96 && p->head_dim != 128) return NQ_ERR_UNSUPPORTED;
     if (!paged_page_size_ok(p->page_size)) return NQ_ERR_UNSUPPORTED;
-    if (p->pages < 1 || p->kv_heads < 1) return NQ_ERR_ARG;
+    if (p->pages < 1 || p->kv_heads < 1 || p->kv_heads > 65536) return NQ_ERR_ARG;
     if (!paged_stride_ok(p->page_stride, p->pages, p->head_dim) ||
         !paged_stride_ok(p->head_stride, p->kv_heads, p->head_dim) ||
         !paged_stride_ok(p->slot_stride, p->page_size, p->head_dim))

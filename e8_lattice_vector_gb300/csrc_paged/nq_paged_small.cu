@@ -115,10 +115,10 @@ struct Walk {
         tile += n;
         if (tile < s.count) return;  // left == 0
         tile = 0;
+        if (++row_tile < s.row_tiles) return;  // the same keys once more, out of the L2
+        row_tile = 0;
         if (++head < kv_heads) return;
         head = 0;
-        if (++row_tile < s.row_tiles) return;
-        row_tile = 0;
         if (left <= 0) return;
         do {
             if (++r >= a.requests) {  // not reached while the lengths stay as they were summed
@@ -189,11 +189,11 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             if (at < n) break;
             at -= n;
         }
-        const long long per_tile = (long long)s.count * a.kv_heads;
+        const long long per_head = (long long)s.count * s.row_tiles;
         c.request = r;
-        c.row_tile = int(at / per_tile);
-        at %= per_tile;
-        c.head = int(at / s.count);
+        c.head = int(at / per_head);
+        at %= per_head;
+        c.row_tile = int(at / s.count);
         c.tile = int(at % s.count);
         c.pos = pos;
         c.end = end;

@@ -296,7 +296,7 @@ enum { NQ_F16 = 0, NQ_BF16 = 1 };
  * [pages][page_size][kv_heads][head_dim] are both such layouts, and so are
  * slices of a larger pool.
  *  dtype: NQ_F16 or NQ_BF16.  head_dim: 64, 96 or 128.  page_size: 16, 32, 64,
- *  128 or 256.  pages >= 1, kv_heads >= 1.  Strides: multiples of 8 elements,
+ *  128 or 256.  pages >= 1, 1 <= kv_heads <= 65536.  Strides: multiples of 8 elements,
  *  >= head_dim and < 2^39 (the stride of an extent of one is not looked at).
  *  Buffers are 16-byte aligned. */
 typedef struct {
@@ -333,7 +333,7 @@ int nq_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int32_t reques
 
 /* Write the step's K and V rows into the pools.  Row (t, h) of k sits at
  * t * k_token_stride + h * k_head_stride elements (v likewise; strides
- * multiples of 8, so the codec's head-major output goes in as it is) and goes to slot
+ * multiples of 8, zero to repeat a row, so the codec's head-major output goes in as it is) and goes to slot
  * slots[t] (device int64[tokens]) of its head; a slot outside [0, pages *
  * page_size) writes nothing.  Two rows with the same slot leave one of the two
  * values in each element.  The source must not overlap the pools. */
@@ -348,7 +348,8 @@ int nq_paged_append(const void* k, int64_t k_token_stride, int64_t k_head_stride
  *  (results do not depend on it).  causal: 0 or 1.  window: 0 = none, else the
  *  number of most recent keys a token sees, its own included.  scale > 0, finite.
  *  q / out element (t, head, d): t * token_stride + head * head_stride + d, strides
- *  multiples of 8 elements. */
+ *  multiples of 8 elements and >= head_dim (a stride of zero is for the append's sources alone).
+ *  tokens * q_heads and table_cols * page_size stay below 2^31 - 2^16. */
 typedef struct {
     int32_t tokens, q_heads, requests, table_cols, max_q, causal, window;
     float scale;

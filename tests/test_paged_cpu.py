@@ -34,7 +34,7 @@ def _attn(nq, **kw):
     return nq.Attention(**f)
 
 
-BAD_POOLS = [(dict(dtype=2), UNSUPPORTED), (dict(head_dim=80), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED),
+BAD_POOLS = [(dict(kv_heads=65537), ARG), (dict(dtype=2), UNSUPPORTED), (dict(head_dim=80), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED),
              (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED), (dict(page_size=512), UNSUPPORTED),
              (dict(pages=0), ARG), (dict(kv_heads=0), ARG), (dict(page_stride=100), ARG), (dict(slot_stride=132), ARG),
              (dict(slot_stride=64), ARG), (dict(head_stride=0), ARG), (dict(head_stride=-128), ARG),
@@ -98,7 +98,8 @@ def test_attention_refusals(nq):
     for kw in (dict(tokens=-1), dict(requests=-1), dict(table_cols=-1), dict(max_q=-1), dict(window=-1),
                dict(causal=2), dict(causal=-1), dict(q_heads=0), dict(q_heads=12), dict(q_heads=-8), dict(scale=0.0),
                dict(scale=-1.0), dict(scale=inf), dict(scale=nan), dict(table_cols=1 << 27, table_stride=1 << 27),
-               dict(table_stride=4), dict(q_token_stride=4), dict(q_head_stride=-8), dict(out_token_stride=12),
+               dict(table_stride=4), dict(q_token_stride=4), dict(q_head_stride=0), dict(out_token_stride=64),
+               dict(tokens=1 << 26),  dict(q_head_stride=-8), dict(out_token_stride=12),
                dict(out_head_stride=1 << 39)):
         args = list(good)
         args[0] = ctypes.byref(_attn(nq, **kw))

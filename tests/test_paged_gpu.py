@@ -623,3 +623,37 @@ def test_paged_pools_hold_what_was_decompressed(nq):
             for t in (0, 15, 16, 69):
                 page = int(c.table[r, t // 16])
                 assert torch.equal(pool[:, page, :, t % 16], src[:, r, :, t])
+
+
+def test_append_repeated_rows(nq):
+    """One K and V row for every head (a head stride of zero)."""
+    Kp, Vp = (torch.zeros(2, 4, 16, 64, dtype=torch.float16, device=DEV) for _ in range(2))
+    K = torch.randn(5, 1, 64, device=DEV).half().expand(5, 4, 64)
+    nq.paged_append(K, K, Kp, Vp, torch.arange(5, device=DEV) + 14)
+    assert torch.equal(Kp[0, :, 14], K[0]) and torch.equal(Kp[1, :, :3].transpose(0, 1), K[2:]) and torch.equal(Kp, Vp)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(100, 1), (128, 1), (130, 1), (520, 2)])
+@pytest.mark.parametrize("new", [1, 9])
+def test_attention_heads_around_a_half(nq, heads, kv_heads, new):
+    """Query heads on one KV head that nearly fill, fill and pass the 128 rows of a half."""
+    Step([(300, new), (0, new), (17, 1)], heads, kv_heads, 64, 16, torch.float16, seed=heads).check(nq)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_table_without_columns(nq, new):
+    s = Step([(0, new), (20, new)], 4, 2, 64, 16, torch.float16, cols=0)
+    out, lse = nq.paged_attention(s.Q, s.Kp, s.Vp, s.table, s.q_start, s.kv_lens, max_q=new,
+                                  lse=torch.zeros(s.tokens, 4, device=DEV))
+    assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_mostly_single_tokens(nq, dtype):
+    """Batches that are shared between the kernels, and batches of drafts of which some need a second tile."""
+    rng = np.random.default_rng(3)
+    lens = [(int(c), 1) for c in rng.integers(0, 3000, 30)] + [(1000, 200), (50, 3), (0, 0), (777, 16)]
+    Step(lens, 8, 2, 128, 16, dtype, seed=5).check(nq)
+    Step(lens, 8, 2, 64, 64, dtype, seed=6).check(nq, window=500)
+    drafts = [(int(c), int(n)) for c, n in zip(rng.integers(0, 2000, 25), rng.integers(1, 5, 25))] + [(600, 8)]
+    Step(drafts, 16, 4, 128, 32, dtype, seed=7).check(nq)
