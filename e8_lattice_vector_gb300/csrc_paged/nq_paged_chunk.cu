@@ -786,8 +786,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                         const uint32_t see = page ? low_bits(to - x) & ~low_bits(from - x) : 0u;
                         if (__all_sync(0xffffffffu, (see & 0xffffu) == 0xffffu)) continue;
                         float y[16];
-                        tm_load16(y, s_at + x);
-                        tm_wait<16>(y);
+                        if (__any_sync(0xffffffffu, (see & 0xffffu) != 0u)) {
+                            tm_load16(y, s_at + x);
+                            tm_wait<16>(y);
+                        }
 #pragma unroll
                         for (int z = 0; z < 16; ++z)
                             if (!(see & 1u << z)) y[z] = -INFINITY;
