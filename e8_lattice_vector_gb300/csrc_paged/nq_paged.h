@@ -73,7 +73,7 @@ struct AttnArgs {
     int64_t page_stride, head_stride, slot_stride;
     int tokens, q_heads, kv_heads, group, requests, table_cols, page_shift, pages, head_dim, causal, window;
     int bf16;
-    int mixed;      // both kernels are launched: the small one takes the requests of at most kSmallRows rows, the large one the others
+    int mixed;      // both kernels are launched: the small one takes requests of at most kSmallRows rows, the large one others
     int out_by_32;  // rows of out start on 32-byte boundaries
     FastDiv by_group;
     int half_tokens;  // tokens whose rows fit one half of the large kernel's row tile (0: a group of more than 128 heads)

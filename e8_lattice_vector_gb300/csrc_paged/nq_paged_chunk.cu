@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     const long long begin = shares.begin(b);
     ChunkStart start{0, 0, 0, 0, begin, shares.begin(b + 1), units, cost};
     if (begin < units) {
-        auto last_at = [&](long long lo, long long hi, long long heads, long long at) {  // the last pair that begins at or before it
+        // the last pair that begins at or before `at`
+        auto last_at = [&](long long lo, long long hi, long long heads, long long at) {
             while (hi - lo > 1) {
                 const long long mid = (lo + hi) >> 1;
                 if (plan.unit_sum[mid] * heads <= at)
@@ -194,7 +195,8 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
             }
             return lo;
         };
-        const long long some = last_at(0, pairs, a.kv_heads, begin);  // a pair of the request: those before it count for all heads
+        // a pair of the request (the requests before it count for all heads)
+        const long long some = last_at(0, pairs, a.kv_heads, begin);
         const long long p0 = some - plan.pair_row_tile[some];
         start.request = plan.pair_request[some];
         const long long p1 = min(p0 + row_tiles_of(a, load_request(a, start.request)), pairs), from = plan.unit_sum[p0];
@@ -597,7 +599,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll 1
                         for (int h = w.shared ? i & 1 : 0; go && h < (w.shared ? (i & 1) + 1 : 2); ++h) {
                             const int count = h ? w.count[1] : w.count[0];
-                            const int of_v = w.shared ? i >> 1 : i, of_k = w.shared ? (i + 2) >> 1 : i + 1;  // of the half's tiles
+                            // of the half's tiles
+                            const int of_v = w.shared ? i >> 1 : i, of_k = w.shared ? (i + 2) >> 1 : i + 1;
                             const uint32_t p = tmem + h * 128;
                             if (i >= 0 && of_v < count) {  // O_h += P_h V
                                 await(c.p_full[h], h ? p_phase[1] : p_phase[0]);
@@ -672,8 +675,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                             const int r = r0 + (lane >> 4), half = (lane >> 3) & 1;
                             const bool seen = key0 + r >= w.lo && key0 + r < w.hi && (live >> (r >> a.page_shift) & 1u);
                             if (!seen && half < HALVES)
-                                *reinterpret_cast<uint4*>(ring + at.stage * C::TILE + half * kHalfBytes + r * 128 + (lane & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(ring + at.stage * C::TILE + half * kHalfBytes + r * 128 +
+                                                          (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         proxy_fence();
                         __syncwarp();
@@ -910,7 +913,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 to_other *= inv;
             }
             const int piece = (2 * blockIdx.x + w.slot) * 2 + h;  // a piece's half in the workspace
-            uint16_t* out = static_cast<uint16_t*>(a.out) + int64_t(w.row + token) * a.out_token_stride + head * a.out_head_stride;
+            uint16_t* out =
+                static_cast<uint16_t*>(a.out) + int64_t(w.row + token) * a.out_token_stride + head * a.out_head_stride;
 #pragma unroll 1
             for (int x0 = 0; x0 < D; x0 += 32) {
                 float o[32];
@@ -981,7 +985,8 @@ int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm
     cfg.stream = a.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_chunk_kernel<D, BF16>, a, km, vm, qm, ws, plan) == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_chunk_kernel<D, BF16>, a, km, vm, qm, ws, plan);
+    return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
 template <bool BF16>
