@@ -137,6 +137,9 @@ class _Fake:
     def data_ptr(self):
         return self._ptr
 
+    def get_device(self):
+        return self.device.index
+
 
 H16, I32, I64 = torch.float16, torch.int32, torch.int64
 
