@@ -82,7 +82,7 @@ struct AttnArgs {
 };
 
 // Both kernels run one block per multiprocessor of a GB300, each with an equal share of the step's (row tile, key
-// tile) pairs, in the order request, row tile, KV head, key tile.  A row tile whose keys end up in several
+// tile) pairs, in the order request, KV head, row tile, key tile.  A row tile whose keys end up in several
 // blocks leaves partial results in the workspace: per block two slots (0: its first piece, which an earlier
 // block began; 1: its last, which a later block ends), joined by a second launch.
 constexpr int kAttnGrid = 152;

@@ -1,5 +1,6 @@
 // nq_paged_small.cu -- attention of a few rows per request over the paged cache (single tokens and short drafts:
-// at most 16 rows for each KV head, rows being tokens times the query heads that share it).
+// 16 rows for each KV head, rows being tokens times the query heads that share it; the few requests of a step that
+// have up to twice as many get a second row tile, which reads their keys again).
 //
 // The time is that of reading K and V once: 2 * 2 * head_dim bytes a key against 4 * rows * head_dim operations, 16
 // operations a byte at most.  So the design is about bytes in flight: one block per multiprocessor with a ring of
@@ -73,8 +74,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Tiles of one row tile of a request: the same for each of its row tiles (there is one, unless the caller's
-// bound on rows was too low), at least one so that rows without keys are written too.
+// Tiles of one row tile of a request: the same for each of its row tiles (several for the longer drafts and for groups
+// of more heads than a row tile has rows), at least one so that rows without keys are written too.
 struct Span {
     int first, count;  // key tiles
     int row_tiles;
