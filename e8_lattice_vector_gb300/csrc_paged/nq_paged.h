@@ -100,8 +100,13 @@ struct AttnWorkspace {
     uint64_t total;
 };
 
+// The arrays begin on the first 256-byte boundary at or after `base`: pieces are stored 32 bytes at a time, and a caller's
+// scratch need only be 16-byte aligned.  `total` counts from `base` and has room for the bytes that are skipped.
+constexpr uintptr_t kWorkspaceAlign = 256;
+
 inline AttnWorkspace attn_workspace(void* base, int rows, int head_dim) {
     char* p = static_cast<char*>(base);
+    p += (kWorkspaceAlign - reinterpret_cast<uintptr_t>(p) % kWorkspaceAlign) % kWorkspaceAlign;
     AttnWorkspace w;
     uint64_t off = 0;
     w.split = reinterpret_cast<AttnSplit*>(p);
@@ -110,7 +115,7 @@ inline AttnWorkspace attn_workspace(void* base, int rows, int head_dim) {
     off += (uint64_t(kAttnGrid) * 2 * rows * sizeof(float2) + 255) / 256 * 256;
     w.o = reinterpret_cast<float*>(p + off);
     off += uint64_t(kAttnGrid) * 2 * rows * head_dim * sizeof(float);
-    w.total = off;
+    w.total = off + kWorkspaceAlign - 16;
     return w;
 }
 
