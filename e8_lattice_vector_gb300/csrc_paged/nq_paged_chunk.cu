@@ -25,7 +25,7 @@
 // In bf16 P is the sum of two bf16 (hi + lo), each with its own product: one bf16 has 2^-8 of p as its rounding error, as much as
 // the output's own, and fp16 tensors, whose P has 2^-11, show that the second product costs 36% of the time.  It is the
 // price of an output that is off by its own rounding and nothing else.
-#include "nq_paged_device.cuh"
+#include "nq_paged_walk.cuh"
 
 namespace nq {
 namespace {
@@ -46,67 +46,6 @@ struct Chunk {
     static constexpr int SMEM = 1024 + Q + STAGES * TILE;
 };
 constexpr int kLiveRing = 8;  // tiles whose page masks are kept; the loads are at most six tiles ahead of a half
-
-// A row tile costs about this many key tiles on top of its own: its Q, the first scores, the results.  Shares are equal in
-// key tiles plus these, or the block whose share is many short row tiles (the beginning of a prompt) would be the last
-// to end.  Not counted when a share has few tiles: there a block's idle time is worth more than an even cost.
-constexpr int kRowTileCost = 3, kCostFrom = 16;
-
-// Where a block's share begins: `unit` counts the row tile's cost, then its key tiles.
-struct ChunkStart {
-    int request, row_tile, head, unit;
-    long long begin, end, total;
-    int cost;
-};
-
-struct ChunkPlan {
-    ChunkStart* start;     // [kAttnGrid]
-    long long* unit_sum;   // [pairs + 1]: units of the (request, row tile) pairs before, for one KV head
-    int* pair_request;     // [pairs]
-    int* pair_row_tile;    // [pairs]
-};
-
-inline int64_t chunk_pairs(int64_t tokens, int half_tokens, int requests) { return tokens / (2 * half_tokens) + requests; }
-
-inline ChunkPlan chunk_plan(char* p, int64_t pairs, uint64_t* total) {
-    ChunkPlan c;
-    uint64_t off = 0;
-    auto take = [&](uint64_t bytes) {
-        char* at = p + off;
-        off += (bytes + 255) / 256 * 256;
-        return at;
-    };
-    c.start = reinterpret_cast<ChunkStart*>(take(kAttnGrid * sizeof(ChunkStart)));
-    c.unit_sum = reinterpret_cast<long long*>(take(uint64_t(pairs + 1) * sizeof(long long)));
-    c.pair_request = reinterpret_cast<int*>(take(uint64_t(pairs) * sizeof(int)));
-    c.pair_row_tile = reinterpret_cast<int*>(take(uint64_t(pairs) * sizeof(int)));
-    *total = off;
-    return c;
-}
-
-__device__ __forceinline__ int row_tiles_of(const AttnArgs& a, const Request& q) {
-    if (a.mixed && q.n * a.group <= kSmallRows) return 0;  // the small kernel's
-    return (q.n + 2 * a.half_tokens - 1) / (2 * a.half_tokens);
-}
-
-// The tokens and keys of one row tile.
-struct RowTile {
-    int token0, n, lo, hi;  // n tokens; keys [lo, hi) are seen by some of them
-    int first, count;       // key tiles, at least one so that rows without keys are written too
-    bool shared;            // one half's tokens, for both halves
-};
-__device__ __forceinline__ RowTile row_tile_of(const AttnArgs& a, const Request& q, int row_tile) {
-    RowTile t;
-    t.token0 = row_tile * 2 * a.half_tokens;
-    t.n = min(q.n - t.token0, 2 * a.half_tokens);
-    t.shared = t.n <= a.half_tokens;
-    const int p0 = q.kv - q.n + t.token0;
-    t.lo = keys_from(a, p0);
-    t.hi = keys_to(a, q.kv, p0 + t.n - 1);
-    t.first = min(t.lo, t.hi) / kKeyTile;
-    t.count = max((t.hi + kKeyTile - 1) / kKeyTile - t.first, 1);
-    return t;
-}
 
 // Block-wide inclusive sum; *total the sum over all threads.
 __device__ __forceinline__ long long plan_scan(long long x, long long* total) {
@@ -131,8 +70,24 @@ __device__ __forceinline__ long long plan_scan(long long x, long long* total) {
     return x + (warp > 0 ? before : 0);
 }
 
-// One block: the running sum of key tiles over the (request, row tile) pairs, then the beginning of every share.  `room`:
-// pairs that the arrays hold, all there are unless row starts decrease.
+// The largest of the values (none negative) of the threads before; *total over all threads.
+__device__ __forceinline__ int plan_top(int x, int* total) {
+    __shared__ int warps[kPlanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) x = max(x, __shfl_up_sync(0xffffffffu, x, d));  // lanes below d get their own
+    int before = __shfl_up_sync(0xffffffffu, x, 1);
+    if (lane == 0) before = 0;
+    __syncthreads();
+    if (lane == 31) warps[warp] = x;
+    __syncthreads();
+    const int w = warps[lane];
+    *total = __reduce_max_sync(0xffffffffu, w);
+    return max(before, __reduce_max_sync(0xffffffffu, lane < warp ? w : 0));
+}
+
+// One block: the requests' rows, the running sum of key tiles over the (request, row tile) pairs, then the beginning of every
+// share.  `room`: pairs that the arrays hold, all there are.
 //
 // The order is request, KV head, row tile: the row tiles that read the same keys come one after the other, in a block and in
 // its neighbours, and find them in the L2 (with row tiles outside heads 2000 tokens over 30000 cached took 691 us, now 676).
@@ -140,9 +95,16 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     __shared__ int s_pair[kPlanThreads];
     pdl_trigger();
     long long pairs = 0, tiles = 0;
+    int top = 0;
     for (int r0 = 0; r0 < a.requests; r0 += kPlanThreads) {
         const int r = r0 + threadIdx.x;
-        const int n = r < a.requests ? row_tiles_of(a, load_request(a, r)) : 0;
+        Request q{0, 0, 0};
+        if (r < a.requests) q = load_request(a, r);
+        int chunk_top;
+        const RowRange rows = row_range(a, q, max(plan_top(rows_end(q), &chunk_top), top));
+        top = max(top, chunk_top);
+        if (r < a.requests) plan.rows[r] = rows;
+        const int n = row_tiles_of(a, Request{rows.begin, rows.n, 0});
         long long chunk_pairs, chunk_tiles;
         const int upto = int(plan_scan(n, &chunk_pairs));
         __syncthreads();  // s_pair of the previous chunk is read
@@ -162,7 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
                         hi = mid;
                 }
                 const int row_tile = p - s_pair[lo];
-                mine = row_tile_of(a, load_request(a, r0 + lo), row_tile).count;
+                mine = row_tile_of(a, planned_request(a, plan, r0 + lo), row_tile).count;
                 plan.pair_request[pairs + p] = r0 + lo;
                 plan.pair_row_tile[pairs + p] = row_tile;
             }
@@ -178,35 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const Attn
     if (threadIdx.x == 0) plan.unit_sum[pairs] = tiles + cost * pairs;
     __syncthreads();
     const int b = threadIdx.x;
-    if (b >= kAttnGrid) return;
-    const long long units = (tiles + cost * pairs) * a.kv_heads;
-    const Shares shares(units);
-    const long long begin = shares.begin(b);
-    ChunkStart start{0, 0, 0, 0, begin, shares.begin(b + 1), units, cost};
-    if (begin < units) {
-        // the last pair that begins at or before `at`
-        auto last_at = [&](long long lo, long long hi, long long heads, long long at) {
-            while (hi - lo > 1) {
-                const long long mid = (lo + hi) >> 1;
-                if (plan.unit_sum[mid] * heads <= at)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            return lo;
-        };
-        // a pair of the request (the requests before it count for all heads)
-        const long long some = last_at(0, pairs, a.kv_heads, begin);
-        const long long p0 = some - plan.pair_row_tile[some];
-        start.request = plan.pair_request[some];
-        const long long p1 = min(p0 + row_tiles_of(a, load_request(a, start.request)), pairs), from = plan.unit_sum[p0];
-        const long long of_head = plan.unit_sum[p1] - from, at = begin - from * a.kv_heads;
-        start.head = int(at / of_head);
-        const long long rest = at - start.head * of_head + from, p = last_at(p0, p1, 1, rest);
-        start.row_tile = int(p - p0);
-        start.unit = int(rest - plan.unit_sum[p]);
-    }
-    plan.start[b] = start;
+    if (b < kAttnGrid) plan.start[b] = chunk_start(a, plan, pairs, (tiles + cost * pairs) * a.kv_heads, cost, b);
 }
 
 // ------------------------------------------------------------------- tcgen05
@@ -388,67 +322,6 @@ struct ChunkControl {
     float m[128], l[128];  // a shared row tile's second half, for the first
 };
 constexpr int kPieceReaders = 11;  // eight softmax warps, loads, products, clearing
-
-// Walks the pieces of a block's share.
-struct ChunkWalk {
-    int r, row_tile, head, unit, cost;
-    long long left;  // units
-    Request q;
-    int row_tiles;
-    RowTile t;
-    int tile, take;  // the piece: key tiles [tile, tile + take) of the row tile; take > 0 while left > 0
-
-    __device__ __forceinline__ void begin(const AttnArgs& a, const ChunkStart& s) {
-        r = s.request;
-        row_tile = s.row_tile;
-        head = s.head;
-        unit = s.unit;
-        cost = s.cost;
-        left = s.end - s.begin;
-        if (left > 0) {
-            q = load_request(a, r);
-            row_tiles = row_tiles_of(a, q);
-            t = row_tile_of(a, q, row_tile);
-            if (!piece()) next(a);
-        }
-    }
-    __device__ __forceinline__ bool piece() {
-        const int end = int(min((long long)(t.count + cost), unit + left));
-        tile = max(unit - cost, 0);
-        take = end - cost - tile;
-        return take > 0;
-    }
-    // Half h's key tiles of the piece (at least one unless shared: its results are written in any case).
-    __device__ __forceinline__ int tiles_of(const AttnArgs& a, int h) const {
-        if (t.shared) return (take + 1 - h) >> 1;
-        if (h == 1) return take;
-        const int hi = keys_to(a, q.kv, q.kv - q.n + t.token0 + a.half_tokens - 1);
-        return min(max((hi + kKeyTile - 1) / kKeyTile - t.first - tile, 1), take);
-    }
-    __device__ __forceinline__ void next(const AttnArgs& a) {
-        do {
-            const int n = int(min((long long)(t.count + cost - unit), left));
-            left -= n;
-            if (left <= 0) return;
-            unit = 0;
-            if (++row_tile >= row_tiles) {
-                row_tile = 0;
-                if (++head >= a.kv_heads) {
-                    head = 0;
-                    do {
-                        if (++r >= a.requests) {  // not reached while the lengths stay as they were summed
-                            left = 0;
-                            return;
-                        }
-                        q = load_request(a, r);
-                        row_tiles = row_tiles_of(a, q);
-                    } while (row_tiles == 0);
-                }
-            }
-            t = row_tile_of(a, q, row_tile);
-        } while (!piece());
-    }
-};
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreadsChunk, 1)
@@ -689,7 +562,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // -------- the pieces, their Q, and the row tile that this block begins and does not end
             const ChunkStart start = plan.start[blockIdx.x];
             ChunkWalk x;
-            x.begin(a, start);
+            x.begin(a, plan, start);
             AttnSplit split{0, 0, 0, 0, -1};
             uint32_t pieces[2] = {0, 0};
             bool go = true;
@@ -699,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (!go) break;
                 if (x.left <= 0) w.take = 0;
                 if (x.left > 0) {
-                    const bool whole = x.tile == 0 && x.take == x.t.count;
+                    const bool whole = x.whole();
                     w.take = x.take;
                     w.count[0] = x.tiles_of(a, 0);
                     w.count[1] = x.tiles_of(a, 1);
@@ -715,14 +588,13 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     w.request = x.r;
                     w.slot = whole ? -1 : x.tile > 0 ? 0 : 1;
                     if (!whole && x.tile == 0)  // the last piece
-                        split = AttnSplit{w.row, 0, w.n * a.group, x.head,
-                                          share_holding(start.total, start.end - 1 + (x.t.count - x.take))};
+                        split = AttnSplit{w.row, 0, w.n * a.group, x.head, x.last_block(start)};
                 }
                 c.piece[piece_at.stage] = w;
                 mbar_arrive(smem_ptr(&c.piece_full[piece_at.stage]));
                 piece_at.step();
                 if (x.left <= 0) break;
-                x.next(a);  // before the wait for room for Q
+                x.next(a, plan);  // before the wait for room for Q
                 for (int h = 0; h < 2; ++h) {
                     if (w.count[h] == 0) break;
                     // As soon as the piece's last scores are there its Q is not read any more: the next one's loads run beside
@@ -1003,7 +875,7 @@ int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm
 
 uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim) {
     uint64_t bytes = 0;
-    chunk_plan(nullptr, chunk_pairs(tokens, 128 / group, requests), &bytes);
+    chunk_plan(nullptr, chunk_pairs(tokens, 128 / group, requests), requests, &bytes);
     return attn_workspace(nullptr, kChunkRows, head_dim).total + bytes;
 }
 
@@ -1014,7 +886,7 @@ int launch_attention_chunk(const AttnArgs& a) {
     const AttnWorkspace ws = attn_workspace(base, kChunkRows, a.head_dim);
     uint64_t bytes = 0;
     const int64_t pairs = chunk_pairs(a.tokens, a.half_tokens, a.requests);
-    const ChunkPlan plan = chunk_plan(base + ws.total, pairs, &bytes);
+    const ChunkPlan plan = chunk_plan(base + ws.total, pairs, a.requests, &bytes);
     attention_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a, plan, pairs);
     if (cudaGetLastError() != cudaSuccess) return NQ_ERR_CUDA;
     const int st = a.bf16 ? launch_chunk<true>(a, km, vm, qm, ws, plan) : launch_chunk<false>(a, km, vm, qm, ws, plan);

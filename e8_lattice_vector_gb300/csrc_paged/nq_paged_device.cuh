@@ -128,19 +128,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Shares {
     long long total, each;
     uint32_t parts, more;  // total = each * parts + more
-    __device__ __forceinline__ explicit Shares(long long t) : total(t) {
+    __host__ __device__ __forceinline__ explicit Shares(long long t) : total(t) {
         parts = uint32_t(min(max(t, 1LL), (long long)kAttnGrid));
         each = t / parts;
         more = uint32_t(t - each * parts);
     }
-    __device__ __forceinline__ long long begin(uint32_t b) const {
+    __host__ __device__ __forceinline__ long long begin(uint32_t b) const {
         return b >= parts ? total : each * b + more * b / parts;
     }
 };
-// The block whose share holds tile `at` (< total): the last b with total b / parts < at + 1.
-__device__ __forceinline__ int share_holding(long long total, long long at) {
+// The block whose share holds tile `at` (< total): the last b with total b / parts < at + 1.  Never past the grid, whatever
+// `at` is: the join takes the workspace's slots from it.
+__host__ __device__ __forceinline__ int share_holding(long long total, long long at) {
     const long long parts = min(total, (long long)kAttnGrid);
-    return int(((at + 1) * parts - 1) / total);
+    return int(min(((at + 1) * parts - 1) / total, (long long)kAttnGrid - 1));
 }
 
 // ------------------------------------------------------------------- lengths
@@ -150,18 +151,23 @@ struct Request {
     int begin, n, kv;
 };
 
-__device__ __forceinline__ Request load_request(const AttnArgs& a, int r) {
+__host__ __device__ __forceinline__ int load_kv(const AttnArgs& a, int r) {
+    return int(min(int64_t(max(a.kv_lens[r], 0)), int64_t(a.table_cols) << a.page_shift));
+}
+__host__ __device__ __forceinline__ Request load_request(const AttnArgs& a, int r) {
     Request q;
     q.begin = min(max(a.q_start[r], 0), a.tokens);
     q.n = max(min(max(a.q_start[r + 1], 0), a.tokens) - q.begin, 0);
-    q.kv = int(min(int64_t(max(a.kv_lens[r], 0)), int64_t(a.table_cols) << a.page_shift));
+    q.kv = load_kv(a, r);
     return q;
 }
 
 // First key that a row at position p sees, and the end of its keys.
-__device__ __forceinline__ int keys_from(const AttnArgs& a, int p) {
+__host__ __device__ __forceinline__ int keys_from(const AttnArgs& a, int p) {
     return a.window > 0 ? int(max(int64_t(p) - a.window + 1, int64_t(0))) : 0;
 }
-__device__ __forceinline__ int keys_to(const AttnArgs& a, int kv, int p) { return a.causal ? max(min(kv, p + 1), 0) : kv; }
+__host__ __device__ __forceinline__ int keys_to(const AttnArgs& a, int kv, int p) {
+    return a.causal ? max(min(kv, p + 1), 0) : kv;
+}
 
 }  // namespace nq

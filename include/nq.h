@@ -370,8 +370,9 @@ typedef struct {
  *              aligned; nothing in it has to start at zero and nothing is kept in it
  * Rows of no request are left as they are.  q_start is clamped to [0,
  * tokens], kv_lens to [0, table_cols * page_size]; a table entry outside [0,
- * pages) hides its keys.  q_start must not decrease (a request whose end is
- * before its start has no rows; rows of two requests hold one of the results).
+ * pages) hides its keys.  q_start must not decrease.  Where it does, a request
+ * whose end is before its start has no rows, and rows before the end of an earlier request's
+ * hold results of requests that claim them, or are left as they are.
  * Keys and values that some row of the request sees must be finite; what no
  * row of it may see (slots past its length, pages outside its table) may hold anything.
  * The result does not depend on the run: no atomics, partial sums are added in a fixed order. */

@@ -3,6 +3,7 @@ import ctypes
 import os
 import subprocess
 
+import numpy as np
 import pytest
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,3 +35,90 @@ def test_workspace_is_aligned_for_any_caller(host, rows, head_dim, base):
     assert split % 32 == 0 and ml % 32 == 0 and o % 32 == 0
     assert base <= split and split + grid * split_bytes <= ml and ml + grid * 2 * rows * 8 <= o
     assert o + grid * 2 * rows * head_dim * 4 <= base + total
+
+
+def walk(host, q_start, kv_lens, tokens, group, kv_heads, P=16, cols=1000, causal=1, window=0, mixed=0):
+    R, room = len(kv_lens), 1 << 18
+    pieces, last = np.zeros((room, 8), np.int32), np.zeros(152, np.int32)
+    starts, lens = np.array(q_start, np.int32), np.array(kv_lens, np.int32)
+    planned, space = ctypes.c_longlong(), ctypes.c_longlong()
+    host.chunk_pieces.restype = ctypes.c_longlong
+    p = lambda x: x.ctypes.data_as(ctypes.c_void_p)
+    n = host.chunk_pieces(tokens, group, kv_heads, R, cols, P.bit_length() - 1, causal, window, mixed, p(starts), p(lens),
+                          p(pieces), ctypes.c_longlong(room), p(last), ctypes.byref(planned), ctypes.byref(space))
+    assert n >= 0
+    return pieces[:n].tolist(), last.tolist(), planned.value, space.value
+
+
+def check_walk(host, q_start, kv_lens, tokens, group, kv_heads, mixed=0, **kw):
+    """Every row tile's key tiles are taken once, in order; a row tile that several blocks share is begun by one that names its
+    last block, and the parts in between are the first pieces of their blocks; no row lies outside q or in two requests."""
+    pieces, last, planned, space = walk(host, q_start, kv_lens, tokens, group, kv_heads, mixed=mixed, **kw)
+    assert planned <= space, "%d pairs, room for %d" % (planned, space)
+    parts, owner = {}, np.full(tokens + 1, -1)
+    seen_first = set()
+    for b, row, n, head, r, tile, take, count in pieces:
+        assert 0 <= row and n > 0 and row + n <= tokens and 0 <= head < kv_heads and take > 0
+        if tile > 0:  # slot 0 of the block's two
+            assert b not in seen_first
+        seen_first.add(b)
+        mine = owner[row:row + n]
+        assert ((mine == -1) | (mine == r)).all(), "rows of two requests"
+        mine[:] = r
+        parts.setdefault((r, row, head), []).append((b, tile, take, count))
+    begun = [-1] * 152
+    for (r, row, head), p in parts.items():
+        at = 0
+        for i, (b, tile, take, count) in enumerate(p):
+            assert tile == at and b == p[0][0] + i and count == p[0][3]
+            at += take
+        assert at == p[0][3]
+        if len(p) > 1:
+            assert begun[p[0][0]] == -1
+            begun[p[0][0]] = p[-1][0]
+    assert begun == last
+    return owner
+
+
+@pytest.mark.parametrize("q_start,lens", [([0, 4000, 0, 4000], [4000, 4000, 4000]), ([0, 3999, 0, 4000, 0], [9000] * 4),
+                                          ([0, 4000] * 40, [5000] * 79), ([4000, 0, 4000], [4000, 4000]),
+                                          ([0, 4000, 3000, 3500, 1, 4000, 4000], [6000] * 6),
+                                          ([2 ** 31 - 1, -5, 77, 77, 4000], [100, 200, 300, 5000])])
+@pytest.mark.parametrize("group", [1, 3, 4, 48])
+@pytest.mark.parametrize("mixed", [0, 1])
+def test_row_starts_that_decrease_stay_in_the_plan(host, q_start, lens, group, mixed):
+    owner = check_walk(host, q_start, lens, 4000, group, 8 if group < 48 else 1, mixed=mixed)
+    top = 0
+    for r in range(len(lens)):  # a request has its rows past the end of all earlier ones
+        taken = np.flatnonzero(owner == r)
+        begin, end = (min(max(q, 0), 4000) for q in q_start[r:r + 2])
+        if mixed and max(end - begin, 0) * group <= 16:
+            assert taken.size == 0
+        else:
+            assert taken.tolist() == list(range(max(begin, top), end))
+        if end > begin:
+            top = max(top, end)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_shares_and_walk(host, seed):
+    """Random batches: starts in order, and starts at random."""
+    rng = np.random.default_rng(seed)
+    R = int(rng.integers(1, 60))
+    lens = rng.integers(0, 200 if seed % 3 else 3, R) * (rng.random(R) < 0.8)
+    ctx = rng.integers(0, 5000, R)
+    group, kv_heads = int(rng.choice([1, 2, 3, 4, 7, 8, 50, 128])), int(rng.choice([1, 2, 8]))
+    kw = dict(mixed=int(rng.integers(0, 2)), causal=int(rng.integers(0, 2)), window=int(rng.choice([0, 0, 1, 300])))
+    q_start = np.concatenate([[0], np.cumsum(lens)])
+    T = int(q_start[-1])
+    owner = check_walk(host, q_start, (ctx + lens).tolist(), T, group, kv_heads, **kw)
+    for r in range(R):
+        if lens[r] and not (kw["mixed"] and lens[r] * group <= 16):
+            assert (owner[q_start[r]:q_start[r + 1]] == r).all()
+    wild = rng.integers(-10, T + 10, R + 1)
+    check_walk(host, wild, (ctx + lens).tolist(), T, group, kv_heads, **kw)
+
+
+def test_no_share_lies_past_the_grid(host):
+    for total, at in ((1, 5), (152, 152), (1000, 1000), (1000, 10 ** 6), (10 ** 9, 10 ** 9 + 7)):
+        assert 0 <= host.share_holding(ctypes.c_longlong(total), ctypes.c_longlong(at)) < 152
