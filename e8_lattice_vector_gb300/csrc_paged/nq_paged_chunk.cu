@@ -6,8 +6,8 @@
 //   P = exp2((S - m) c)          by a warpgroup, a thread per row: no exchange between threads
 //   O = O f + P V                P from tensor memory, where it takes the place of S
 // m is a reference that follows the running maximum only when that has grown by more than 2^8 in P (kSlack): O is
-// rescaled on those few tiles, and on the others the tensor cores add to it undisturbed.  P stays below 2^8, and
-// its sum below 2^39 for any length.
+// rescaled on those few tiles, and on the others the tensor cores add to it undisturbed.  P stays below 2^8 (times 2^7 in
+// fp16, see kLift), and its sum below 2^46 for any length.
 //
 // The two halves alternate on the tensor cores: while one half's exponentials are taken, the other half's products run.  A
 // row tile with rows for one half only is given to both, each taking every other key tile; the two sums meet
@@ -253,10 +253,17 @@ __device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t* u) {
         : "memory");
 }
 
-// m sc - the reference taken for it (exact).
+// The reference is taken as fp32's nearest to LIFT - m sc; this is m sc + that number - LIFT, to the last bits of m sc (the sum's
+// rounding error by Knuth's two-sum).
+template <bool BF16>
 __device__ __forceinline__ float beyond_reference(float m, float sc) {
     const float scaled = m * sc;
-    return fabsf(scaled) > kExactRef ? 0.0f : __fmaf_rn(m, sc, -scaled);
+    if (fabsf(scaled) > kExactRef) return 0.0f;
+    const float rest = __fmaf_rn(m, sc, -scaled);
+    if constexpr (BF16) return rest;
+    constexpr float lift = kLift<BF16, 7>;
+    const float neg = lift - scaled, b = neg - lift;
+    return rest - ((lift - (neg - b)) + (-scaled - b));
 }
 
 // 32 bytes to a 32-byte boundary.
@@ -622,6 +629,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t s_at = tmem + h * 128 + lanes, o_at = tmem + 256 + h * 128 + lanes;
         const float sc = a.scale * kLog2e;
+        constexpr float lift = kLift<BF16, 7>;
         auto wait = [&](uint64_t& bar, uint32_t parity) {
             mbar_wait(smem_ptr(&bar), parity, &c.gave_up);
             __syncwarp();
@@ -642,8 +650,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int all_lo = keys_from(a, w.pos + first + n_tokens - 1), all_hi = keys_to(a, w.kv, w.pos + first);
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
-            // p = 2^(s sc + neg).  The reference is the fp32 number nearest to m sc, and rest = m sc - reference (exact); a
-            // huge one (far) would leave no digits for the difference, there s - m is taken first and the reference is m sc.
+            // p = 2^(s sc + neg), lifted in fp16.  neg is the fp32 number nearest to lift - m sc, and rest what it leaves of that; a
+            // huge m sc (far) would leave no digits for the difference, there s - m is taken first and neg is the lift.
             float m = -INFINITY, l = 0.0f, neg = 0.0f, rest = 0.0f;
             bool far = false;
             for (int j = 0; j < count; ++j, ++n_s) {
@@ -690,7 +698,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 if (__any_sync(0xffffffffu, moves)) {
                     const float m_new = moves ? top : m, scaled = m_new * sc;
                     const bool huge = fabsf(scaled) > kExactRef;
-                    const float rest_new = beyond_reference(m_new, sc);
+                    const float rest_new = beyond_reference<BF16>(m_new, sc);
                     if (__any_sync(0xffffffffu, moves && m != -INFINITY)) {
                         const float f = moves && m != -INFINITY ? exp2_fast(__fmaf_rn(m - m_new, sc, rest_new - rest)) : 1.0f;
                         wait(c.o_full[h], (n_s - 1) & 1);  // the previous product has added to O
@@ -709,7 +717,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     if (moves) {  // O and l are zero as long as m is -infinity
                         m = m_new;
                         rest = rest_new;
-                        neg = huge ? 0.0f : -scaled;
+                        neg = huge ? lift : lift - scaled;
                         far = huge;
                     }
                 }
@@ -756,7 +764,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 
             // ------------------------------------------------------- results
             wait(c.o_full[h], (n_s - 1) & 1);
-            float to_m = exp2_fast(-rest);  // from the reference to m
+            float to_m = exp2_fast(-rest) * (1.0f / kLifted<BF16, 7>);  // from the reference to m
             l *= to_m;
             const bool both = w.shared && w.take > 1, whole = w.slot < 0;
             float to_other = 0.0f;  // the other half's part in the result
@@ -776,7 +784,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 const float f1 = m1 == -INFINITY ? 0.0f : exp2_fast((m1 - top) * sc);
                 l = l * f0 + c.l[row] * f1;
                 to_m *= f0;
-                to_other = exp2_fast(-beyond_reference(m1, sc)) * f1;
+                to_other = exp2_fast(-beyond_reference<BF16>(m1, sc)) * (1.0f / kLifted<BF16, 7>) * f1;
                 m = top;
             }
             if (whole) {

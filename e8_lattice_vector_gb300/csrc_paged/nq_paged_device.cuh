@@ -121,6 +121,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// exp(s - m) goes to the tensor cores in 16 bits.  fp16 loses digits below 2^-14 and everything below 2^-25, and a long context
+// has that many small weights that their sum counts.  So there they go in 2^LIFT times as large, up to 2^15: 14 in the small
+// kernel, whose largest is 1, and 7 in the large one, whose largest is 2^8 (weights below 2^-39 and 2^-32 are lost, 2^-15 of a result over
+// 131072 keys at most).  bf16 has fp32's range and needs none.
+template <bool BF16, int LIFT>
+constexpr float kLift = BF16 ? 0.0f : float(LIFT);
+template <bool BF16, int LIFT>
+constexpr float kLifted = BF16 ? 1.0f : float(1 << LIFT);
+
 // -------------------------------------------------------------------- shares
 
 // `total` tiles over the first min(total, kAttnGrid) blocks, sizes differing by one: block b's begin at

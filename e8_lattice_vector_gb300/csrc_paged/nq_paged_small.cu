@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
 
     // -------------------------------------------------------------- compute
     const float sc = a.scale * kLog2e;
+    constexpr float lifted = kLifted<BF16, 14>;
     const int rq = lane >> 2, cq = lane & 3;  // this lane's rows rq, rq + 8 and its column pair
     if (threadIdx.x == 0) ws.split[blockIdx.x].last_block = -1;
     int n = 0;
@@ -349,8 +350,9 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
                         }
                     }
                 }
-                // p in 16 bits: fp16's rounding error (2^-11 of p) is below what out's own rounding costs, bf16's
-                // (2^-8) is not, so there p goes in as the sum of two bf16 (2^-17); its second product hides behind the loads
+                // p in 16 bits, lifted in fp16 (o is 2^14 times too large until it is joined): fp16's rounding error (2^-11 of p)
+                // is what out's own rounding costs at most, bf16's (2^-8) would show beside it in a mean of many, so there p
+                // goes in as the sum of two bf16 (2^-17); its second product hides behind the loads
                 uint32_t pf[4], pl[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
                         // subtracted before it is scaled: exact for the largest scores too
                         const float p0 = exp2_fast((s[j][2 * e] - mm) * sc), p1 = exp2_fast((s[j][2 * e + 1] - mm) * sc);
                         l[e] += p0 + p1;
-                        pf[2 * j + e] = pack2<BF16>(p0, p1);
+                        pf[2 * j + e] = pack2<BF16>(p0 * lifted, p1 * lifted);
                         if constexpr (BF16)
                             pl[2 * j + e] = pack2<true>(p0 - bf16_low(pf[2 * j + e]), p1 - bf16_high(pf[2 * j + e]));
                     }
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             float top = c.m[0][rq + 8 * e];
 #pragma unroll
             for (int v = 1; v < kWarps; ++v) top = fmaxf(top, c.m[v][rq + 8 * e]);
-            const float f = m[e] == -INFINITY ? 0.0f : exp2_fast((m[e] - top) * sc);
+            const float f = m[e] == -INFINITY ? 0.0f : exp2_fast((m[e] - top) * sc) * (1.0f / lifted);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 o[j][2 * e] *= f;

@@ -49,3 +49,76 @@ def test_attention_row_starts_that_decrease(nq, T, max_q):
             ok |= out == 77
         assert bool(ok.all())
     nq.paged_status()
+
+
+def check_weights(nq, s, scale, new, copies=1):
+    """One request's causal rows (all of `copies` requests over the same pages) against 64 bits, by a bound in which the weights have their own roundoff.  With u the type's
+    unit roundoff (2^-11 fp16, 2^-8 bf16) and w the weights' (2^-11; 2^-17 in bf16, where they are the sum of two):
+      |out - exact| <= u |exact| + 2^-25 + A (w + 2 S + 2 (n + 8) e) (1 + u) + 2^-32 sum |v| / l
+    S, A, l, n and e as in test_paged_gpu; the last term, fp16's alone, is a weight below fp16's normal range: off by 2^-25 when
+    the largest is 2^7 at least."""
+    half = s.dtype == torch.float16
+    u, w = (2.0 ** -11, 2.0 ** -11) if half else (2.0 ** -8, 2.0 ** -17)
+    G, D, L = s.heads // s.kv_heads, s.D, s.k[0].shape[0]
+    lse = torch.empty(copies * new, s.heads, device=DEV)
+    starts = torch.arange(copies + 1, dtype=torch.int32, device=DEV) * new
+    out, _ = nq.paged_attention(s.Q.repeat(copies, 1, 1), s.Kp, s.Vp, s.table.repeat(copies, 1), starts,
+                                s.kv_lens.repeat(copies), max_q=new, scale=scale, lse=lse)
+    for i in range(1, copies):
+        assert torch.equal(out[i * new:(i + 1) * new], out[:new]) and torch.equal(lse[i * new:(i + 1) * new], lse[:new])
+    out, lse = out[:new], lse[:new]
+    hidden = torch.arange(L, device=DEV)[None] > torch.arange(L - new, L, device=DEV)[:, None]
+    for h in range(s.heads):
+        q, k, v = s.Q[:, h].double(), s.k[0][:, h // G].double(), s.v[0][:, h // G].double()
+        x = (q @ k.T * scale).masked_fill(hidden, -float("inf"))
+        p = torch.exp(x - x.amax(-1, keepdim=True))
+        l = p.sum(-1, keepdim=True)
+        exact, A = p @ v / l, p @ v.abs() / l
+        S = (D + 4) * E32 * scale * (q.abs() @ k.abs().T).masked_fill(hidden, 0.0).amax(-1, keepdim=True)
+        tol = u * exact.abs() + 2.0 ** -25 + A * (w + 2 * S + 2 * (L + 8) * E32) * (1 + u)
+        if half:
+            tol += 2.0 ** -32 * (~hidden).double() @ v.abs() / l
+        err = (out[:, h].double() - exact).abs()
+        assert bool((err <= tol).all()), "out: worst error / tolerance %.3g" % float((err / tol).max())
+        z = torch.logsumexp(x, -1)
+        err, tol = (lse[:, h].double() - z).abs(), S.squeeze(-1) + (L + 8) * E32 + 4 * E32 * z.abs()
+        assert bool((err <= tol).all()), "lse: worst error / tolerance %.3g" % float((err / tol).max())
+
+
+def put_keys(s, k, v):
+    """New keys and values for the single request of a step."""
+    s.k[0], s.v[0] = k.to(s.dtype), v.to(s.dtype)
+    for c in range(-(-len(k) // s.P)):
+        n = min(s.P, len(k) - c * s.P)
+        page = int(s.table[0, c])
+        s.Kp[page, :, :n] = s.k[0][c * s.P:c * s.P + n].transpose(0, 1)
+        s.Vp[page, :, :n] = s.v[0][c * s.P:c * s.P + n].transpose(0, 1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("place", [0, 70000, 131000])
+@pytest.mark.parametrize("gap", [5.5, 10.0, 14.0, 17.0, 17.5, 20.0])
+def test_attention_one_key_far_above_a_long_context(nq, dtype, new, place, gap):
+    """One key that takes most of the weight, and very many that share a small part of it, which their values make the whole
+    result: no weight may be lost, nor all of them rounded one way.  As many requests as the grid has blocks, each of which
+    then has a whole context and one running maximum for it (the small kernel: one for each of its warps)."""
+    L = 131072
+    s = Step([(L - new, new)], 4, 1, 64, 256, dtype, seed=3)
+    s.Q.fill_(1.0)
+    k, v = torch.zeros(L, 1, 64, device=DEV), torch.rand(L, 1, 64, device=DEV) + 0.5
+    k[place], v[place] = gap / 64, 0.0
+    put_keys(s, k, v)
+    check_weights(nq, s, 1.0, new, copies=152)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_weights_have_their_bits(nq, dtype, new, D):
+    """Few keys of equal size, whose weights are not powers of two, and values of the largest magnitude: the weights' own
+    roundoff, and no overflow in the sums."""
+    for L, big in ((new + 2, 1.0), (3000, 1.0), (3000, 60000.0)):
+        s = Step([(L - new, new)], 4, 2, D, 16, dtype, seed=L)
+        put_keys(s, torch.randn(L, 2, D, device=DEV) * 0.4, (torch.rand(L, 2, D, device=DEV) + 0.05) * big)
+        check_weights(nq, s, D ** -0.5, new)
