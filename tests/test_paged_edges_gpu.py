@@ -122,3 +122,24 @@ def test_attention_weights_have_their_bits(nq, dtype, new, D):
         s = Step([(L - new, new)], 4, 2, D, 16, dtype, seed=L)
         put_keys(s, torch.randn(L, 2, D, device=DEV) * 0.4, (torch.rand(L, 2, D, device=DEV) + 0.05) * big)
         check_weights(nq, s, D ** -0.5, new)
+
+
+def test_waits_are_limited_and_end_soon_after_another(nq, tmp_path):
+    """A barrier that nothing completes: a wait gives up after its limit and says so, and when another thread has given up it
+    returns within 0.1 ms."""
+    import ctypes
+    import os
+    import subprocess
+
+    from e8_lattice_vector_gb300 import build as nqbuild
+
+    here = os.path.dirname(os.path.abspath(__file__))
+    so = str(tmp_path / "paged_waits.so")
+    subprocess.run([nqbuild._nvcc()] + nqbuild.NVCC_FLAGS + ["-shared", os.path.join(here, "paged_waits.cu"), "-o", so], check=True)
+    call, result = ctypes.CDLL(so).wait_for_nothing_once, torch.zeros(3, dtype=torch.int64, device=DEV)
+    assert call(0, 1, ctypes.c_void_p(result.data_ptr())) == 0
+    passed, flag, ns = result.tolist()
+    assert passed == 0 and flag == 1 and 1.9e9 < ns < 3e9
+    assert call(1, 20, ctypes.c_void_p(result.data_ptr())) == 0
+    passed, flag, ns = result.tolist()
+    assert passed == 0 and flag == 1 and ns < 20 * 1e5, "20 waits after another was given up took %.1f ms" % (ns * 1e-6)
