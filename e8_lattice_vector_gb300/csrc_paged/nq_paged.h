@@ -5,6 +5,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "../../include/nq.h"
 
@@ -136,9 +139,28 @@ uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim);
 int launch_join_few_rows(const AttnArgs& a, const AttnWorkspace& ws);
 int launch_join_many_rows(const AttnArgs& a, const AttnWorkspace& ws);
 
-// Whether a kernel gave up a wait since the last call.
-int small_gave_up(int* seen);
-int chunk_gave_up(int* seen);
+// Copies of the counts of blocks that gave up a wait, in stream order.
+int read_small_gave_up(uint64_t* blocks, cudaStream_t stream);
+int read_chunk_gave_up(uint64_t* blocks, cudaStream_t stream);
+
+// What has been reported of these counts, per device.  The counts on the device only grow, so that one that grows while it is
+// read, by a kernel on another stream, is reported by the next call.
+class GiveUps {
+public:
+    // Whether either count is past what has been reported; it is reported then.  A copy older than another thread's says nothing.
+    bool grew(int device, uint64_t small, uint64_t chunk) {
+        std::lock_guard<std::mutex> lock(mu_);
+        auto& seen = seen_[device];
+        const bool s = small > seen.first, c = chunk > seen.second;
+        if (s) seen.first = small;
+        if (c) seen.second = chunk;
+        return s || c;
+    }
+
+private:
+    std::mutex mu_;
+    std::map<int, std::pair<uint64_t, uint64_t>> seen_;
+};
 
 // Allow `kernel` `smem` bytes of dynamic shared memory on the current device (once per device); false on a CUDA error.
 bool ensure_smem(const void* kernel, int smem);

@@ -267,10 +267,13 @@ int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uin
 }
 
 int nq_paged_status(void* stream) {
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return NQ_ERR_CUDA;
-    int small = 0, chunk = 0;
-    if (nq::small_gave_up(&small) != NQ_OK || nq::chunk_gave_up(&chunk) != NQ_OK) return NQ_ERR_CUDA;
-    return small || chunk ? NQ_ERR_CUDA : NQ_OK;
+    static nq::GiveUps reported;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint64_t small = 0, chunk = 0;
+    int device = 0;
+    const bool read = nq::read_small_gave_up(&small, s) == NQ_OK && nq::read_chunk_gave_up(&chunk, s) == NQ_OK;
+    if (cudaStreamSynchronize(s) != cudaSuccess || !read || cudaGetDevice(&device) != cudaSuccess) return NQ_ERR_CUDA;
+    return reported.grew(device, small, chunk) ? NQ_ERR_CUDA : NQ_OK;
 }
 
 int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool, const void* k_pages,

@@ -30,7 +30,7 @@
 namespace nq {
 namespace {
 
-__device__ int g_gave_up;  // set when a wait was given up
+__device__ unsigned long long g_gave_up;  // blocks that gave up a wait, ever
 
 constexpr int kThreadsChunk = 384;  // two warpgroups for the halves; loads, products, clearing, pieces and Q
 constexpr int kPlanThreads = 1024;
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     }
     __syncwarp();
     __syncthreads();
-    if (threadIdx.x == 0 && *(volatile int*)&c.gave_up) atomicExch(&g_gave_up, 1);
+    if (threadIdx.x == 0 && *(volatile int*)&c.gave_up) atomicAdd(&g_gave_up, 1ull);
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -901,12 +901,10 @@ int launch_attention_chunk(const AttnArgs& a) {
     return st == NQ_OK ? launch_join_many_rows(a, ws) : st;
 }
 
-int chunk_gave_up(int* seen) {
-    const int zero = 0;
-    if (cudaMemcpyFromSymbol(seen, g_gave_up, sizeof(int)) != cudaSuccess ||
-        cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(int)) != cudaSuccess)
-        return NQ_ERR_CUDA;
-    return NQ_OK;
+int read_chunk_gave_up(uint64_t* blocks, cudaStream_t stream) {
+    return cudaMemcpyFromSymbolAsync(blocks, g_gave_up, sizeof(uint64_t), 0, cudaMemcpyDeviceToHost, stream) == cudaSuccess
+               ? NQ_OK
+               : NQ_ERR_CUDA;
 }
 
 }  // namespace nq

@@ -18,7 +18,7 @@
 namespace nq {
 namespace {
 
-__device__ int g_gave_up;  // set when a wait was given up
+__device__ unsigned long long g_gave_up;  // blocks that gave up a wait, ever
 
 constexpr int kWarps = 8;
 constexpr int kConsumers = kWarps * 32;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             int late = 0;
             for (int i = max(n - S::STAGES, 0); i < n; ++i)
                 mbar_wait(smem_ptr(&c.full[i % S::STAGES]), (i / S::STAGES) & 1, &late);
-            if (late || *(volatile int*)&c.gave_up) atomicExch(&g_gave_up, 1);
+            if (late || *(volatile int*)&c.gave_up) atomicAdd(&g_gave_up, 1ull);
         }
         return;
     }
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
         named_barrier<1, kConsumers>();  // the join buffer and the sums are read
         w.next(a, a.kv_heads);
     }
-    if (threadIdx.x == 0 && *(volatile int*)&c.gave_up) atomicExch(&g_gave_up, 1);
+    if (threadIdx.x == 0 && *(volatile int*)&c.gave_up) atomicAdd(&g_gave_up, 1ull);
 }
 
 }  // namespace
@@ -502,12 +502,10 @@ int launch_attention_small(const AttnArgs& a) {
     return st == NQ_OK ? launch_join_few_rows(a, ws) : st;
 }
 
-int small_gave_up(int* seen) {
-    const int zero = 0;
-    if (cudaMemcpyFromSymbol(seen, g_gave_up, sizeof(int)) != cudaSuccess ||
-        cudaMemcpyToSymbol(g_gave_up, &zero, sizeof(int)) != cudaSuccess)
-        return NQ_ERR_CUDA;
-    return NQ_OK;
+int read_small_gave_up(uint64_t* blocks, cudaStream_t stream) {
+    return cudaMemcpyFromSymbolAsync(blocks, g_gave_up, sizeof(uint64_t), 0, cudaMemcpyDeviceToHost, stream) == cudaSuccess
+               ? NQ_OK
+               : NQ_ERR_CUDA;
 }
 
 }  // namespace nq

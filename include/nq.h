@@ -383,8 +383,9 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
                        void* stream);
 
 /* Waits for `stream`, then returns NQ_ERR_CUDA if it failed or if an attention
- * kernel on the current device gave up waiting for its loads since the last call of this
- * function (its outputs are then void), else NQ_OK.  A wait is given up after about two
+ * kernel on the current device gave up waiting for its loads since that was last
+ * reported (its outputs are then void), else NQ_OK.  Any thread may call it, while kernels run on other streams
+ * too: a report covers what `stream` has done and what of the others is done, and none is lost.  A wait is given up after about two
  * seconds, and every later one of its block within 0.1 ms, except that for the block's own copies
  * at its end: two seconds again. */
 int nq_paged_status(void* stream);

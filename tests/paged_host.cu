@@ -79,3 +79,9 @@ extern "C" long long chunk_pieces(int tokens, int group, int kv_heads, int reque
 }
 
 extern "C" int share_holding(long long total, long long at) { return nq::share_holding(total, at); }
+
+// One GiveUps through a sequence of reads (device, small, chunk); grew[i]: what the i-th says.
+extern "C" void give_ups(const uint64_t* reads, int n, int* grew) {
+    nq::GiveUps g;
+    for (int i = 0; i < n; ++i) grew[i] = g.grew(int(reads[3 * i]), reads[3 * i + 1], reads[3 * i + 2]);
+}

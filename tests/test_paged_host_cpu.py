@@ -122,3 +122,15 @@ def test_shares_and_walk(host, seed):
 def test_no_share_lies_past_the_grid(host):
     for total, at in ((1, 5), (152, 152), (1000, 1000), (1000, 10 ** 6), (10 ** 9, 10 ** 9 + 7)):
         assert 0 <= host.share_holding(ctypes.c_longlong(total), ctypes.c_longlong(at)) < 152
+
+
+def test_every_wait_that_was_given_up_is_reported(host):
+    """Counts that only grow: each growth is reported once, also one that comes between another read and its report, for
+    either kernel and each device by itself, of any size."""
+    reads = [(0, 0, 0, 0), (0, 2, 0, 1), (0, 2, 0, 0), (0, 3, 0, 1), (0, 3, 5, 1), (0, 3, 5, 0),
+             (0, 2, 5, 0),  # copied before the last but one report, compared after it
+             (1, 0, 0, 0), (1, 1, 0, 1), (0, 3, 6, 1), (0, 2 ** 31 - 1, 6, 1), (0, 2 ** 32 - 1, 6, 1), (0, 2 ** 40, 6, 1), (0, 2 ** 40, 6, 0)]
+    flat = np.array([r[:3] for r in reads], np.uint64)
+    grew = np.zeros(len(reads), np.int32)
+    host.give_ups(flat.ctypes.data_as(ctypes.c_void_p), len(reads), grew.ctypes.data_as(ctypes.c_void_p))
+    assert grew.tolist() == [r[3] for r in reads]
