@@ -274,5 +274,7 @@ def _check_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q, 
 def paged_status(device=None):
     """Waits for the device's current stream; raises NQError when it failed or when an attention kernel gave up
     waiting for its loads (outputs since the last paged_status are then void)."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    _launch(dev.index, _lib.lib().nq_paged_status)
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError("paged_status needs a CUDA device, got %s" % dev)
+    _launch(torch.cuda.current_device() if dev.index is None else dev.index, _lib.lib().nq_paged_status)
