@@ -72,7 +72,22 @@ def _launch(index, fn, *args):
         _lib.check(fn.__name__, st)
 
 
+_I32_MAX = 2 ** 31 - 1
+
+
+def _bound(n):
+    """A number that only bounds others, for a 32-bit argument (ctypes would keep its low 32 bits): past them, the largest; below
+    zero, one that is refused."""
+    return max(min(operator.index(n), _I32_MAX), -1)
+
+
+def _check_size(n, name):
+    if not 0 <= n <= _I32_MAX:
+        raise ValueError("%s is %d; the kernels count in 32 bits" % (name, n))
+
+
 def _check_vec(x, name, dtype, device, n):
+    _check_size(n, "the length of %s" % name)
     if not (x.is_cuda and x.dtype == dtype and x.dim() == 1 and x.is_contiguous()):
         raise ValueError("%s must be a contiguous 1-D %s CUDA tensor" % (name, str(dtype)[6:]))
     if x.shape[0] != n:
@@ -82,11 +97,13 @@ def _check_vec(x, name, dtype, device, n):
 
 
 def _check_table(table, requests, device):
+    """Also that its columns fit 32 bits; its rows are `requests`, a length that was checked."""
     if not (table.is_cuda and table.dtype == torch.int32 and table.dim() == 2 and
             (table.stride(1) == 1 or table.shape[1] <= 1 or table.shape[0] == 0)):
         raise ValueError("block_table must be a 2-D int32 CUDA tensor with contiguous rows")
     if table.shape[0] != requests:
         raise ValueError("block_table has %d rows; there are %d requests" % (table.shape[0], requests))
+    _check_size(table.shape[1], "the width of block_table")
     if table.device != device:
         raise ValueError("block_table is on %s; the call runs on %s" % (table.device, device))
 
@@ -124,6 +141,8 @@ def _pool(K_pages, V_pages):
     if V_pages is not None and (V_pages.dtype != K_pages.dtype or V_pages.shape != K_pages.shape or
                                 V_pages.device != K_pages.device or V_pages.stride() != K_pages.stride()):
         raise ValueError("V_pages must have K_pages' type, shape, strides and device")
+    for n in K_pages.shape:
+        _check_size(n, "a size of K_pages")
     return _lib.Pool(_DTYPES[K_pages.dtype], *K_pages.shape, 0, *K_pages.stride()[:3])
 
 
@@ -134,12 +153,12 @@ def page_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, out
     the sum are padding).  Returns a PageMap: q_start [requests + 1], kv_lens [requests], slots [tokens] (int64:
     page * page_size + offset, -1 for padding and for tokens without a page), positions [tokens] (-1 for padding) and
     counts [4]: new tokens, pages taken, pages the free list lacked, requests longer than their table row."""
-    key = ("map", tokens, *_meta(ctx_lens), *_meta(new_lens), *_meta(free_pages), *_meta(block_table))
+    key = ("map", page_size, tokens, *_meta(ctx_lens), *_meta(new_lens), *_meta(free_pages), *_meta(block_table))
     if out is not None:
         key += (*_meta(out.q_start), *_meta(out.kv_lens), *_meta(out.slots), *_meta(out.positions), *_meta(out.counts))
     kept = _KEPT.get(key)
     if kept is None:
-        kept = _keep(key, _check_map(ctx_lens, new_lens, free_pages, block_table, tokens, out))
+        kept = _keep(key, _check_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, out))
     index, fn, n, n_free, cols, stride = kept
     if out is None:
         out = PageMap.empty(n, tokens, ctx_lens.device)
@@ -149,8 +168,11 @@ def page_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, out
     return out
 
 
-def _check_map(ctx_lens, new_lens, free_pages, block_table, tokens, out):
+def _check_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, out):
     dev, n, i32 = ctx_lens.device, ctx_lens.numel(), torch.int32
+    if page_size > 0:  # others are the library's to refuse
+        _check_size(page_size, "page_size")
+    _check_size(tokens, "tokens")
     _check_vec(ctx_lens, "ctx_lens", i32, dev, n)
     _check_vec(new_lens, "new_lens", i32, dev, n)
     _check_vec(free_pages, "free_pages", i32, dev, free_pages.numel())
@@ -206,6 +228,8 @@ def _attention(Q, out, K_pages, V_pages, block_table, requests, max_q, scale, ca
 def paged_attention_workspace(Q, K_pages, block_table, max_q=None):
     """A scratch tensor for paged_attention calls with these shapes (None when they need none).  Reuse it across
     calls on one stream."""
+    if max_q is not None:
+        max_q = _bound(max_q)
     return workspace(_attention(Q, Q, K_pages, None, block_table, block_table.shape[0], max_q, None, 1, 0)[2], Q.device)
 
 
@@ -219,10 +243,10 @@ def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=No
     the row's own position.  window > 0: only the last `window` of those.  A row that sees nothing is 0.
     Returns out (as Q); with lse (float32 [tokens, q_heads], filled with the log of the sum of exponentials) (out,
     lse).  ws: scratch from paged_attention_workspace, allocated here when not given."""
-    if max_q is not None and type(max_q) is not int:
-        max_q = operator.index(max_q)
-    if type(window) is not int:
-        window = operator.index(window)
+    if max_q is not None and (type(max_q) is not int or not 0 <= max_q <= _I32_MAX):
+        max_q = _bound(max_q)
+    if type(window) is not int or not 0 <= window <= _I32_MAX:
+        window = _bound(window)
     if scale is not None and type(scale) is not float:
         scale = float(scale)
     causal = 1 if causal else 0
@@ -254,6 +278,7 @@ def _check_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q, 
     if Q.dim() != 3:
         raise ValueError("Q must be [tokens, q_heads, head_dim], got %s" % (tuple(Q.shape),))
     tokens, heads = Q.shape[0], Q.shape[1]
+    _check_size(tokens, "the length of Q")
     if heads == 0 or heads % pool.kv_heads:
         raise ValueError("%d query heads cannot share %d KV heads" % (heads, pool.kv_heads))
     shape = (tokens, heads, pool.head_dim)

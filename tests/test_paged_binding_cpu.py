@@ -24,3 +24,46 @@ def test_status_of_any_device(paged):
     with pytest.raises(ValueError, match="CUDA device"):
         paged.paged_status("cpu")
     assert not paged.calls
+
+
+def test_numbers_past_32_bits_do_not_wrap(paged, monkeypatch):
+    """The library's counts are 32-bit: a bound or a window past them means the largest, a size past them is refused."""
+    from test_paged_cpu import H16, I32, I64, _Fake
+
+    pool, q, lens = _Fake((10, 8, 16, 128), H16), _Fake((4, 32, 128), H16), _Fake((3,), I32)
+    table, starts, ws = _Fake((3, 7), I32), _Fake((4,), I32), _Fake((1 << 30,), torch.uint8)
+
+    def attention(**kw):
+        paged.paged_attention(q, pool, pool, kw.pop("table", table), starts, lens, out=q, ws=ws, **kw)
+        return paged.calls.pop()[2][0]._obj
+
+    assert attention(window=5).window == 5 and attention().window == 0
+    for n in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 70):
+        assert attention(window=n).window == 2 ** 31 - 1
+        assert attention(max_q=n).max_q == 2 ** 31 - 1
+    rows, sizes = _Fake((40, 32, 128), H16), []
+    monkeypatch.setattr(paged, "workspace", lambda need, device: sizes.append(need))
+    for n in (1, 2 ** 31 - 1, 2 ** 32 + 1):
+        paged.paged_attention_workspace(rows, pool, table, max_q=n)
+    assert sizes[0] < sizes[1] == sizes[2]
+    for n in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 5):
+        with pytest.raises(RuntimeError):
+            attention(window=n)
+        with pytest.raises(RuntimeError):
+            attention(max_q=n)
+    with pytest.raises(ValueError, match="block_table"):
+        attention(table=_Fake((3, 2 ** 32 + 7), I32))
+    vec = lambda n, t=I32: _Fake((n,), t)
+    out = lambda tokens: paged.PageMap(vec(4), vec(3), vec(tokens, I64), vec(tokens), vec(4))
+    paged.page_map(lens, lens, vec(9), table, 16, 4, out=out(4))
+    assert paged.calls.pop()[2][8:10] == (16, 4)
+    for name, args in (("page_size", (vec(9), table, 2 ** 32 + 16, 4, out(4))),
+                       ("tokens", (vec(9), table, 16, 2 ** 32 + 4, out(2 ** 32 + 4))),
+                       ("free_pages", (vec(2 ** 32 + 9), table, 16, 4, out(4))),
+                       ("block_table", (vec(9), _Fake((3, 2 ** 32 + 7), I32), 16, 4, out(4)))):
+        with pytest.raises(ValueError, match=name):
+            paged.page_map(lens, lens, *args[:-1], out=args[-1])
+    big = 2 ** 32 + 4
+    with pytest.raises(ValueError, match="slots"):
+        paged.paged_append(_Fake((big, 8, 128), H16), _Fake((big, 8, 128), H16), pool, pool, vec(big, I64))
+    assert not paged.calls
