@@ -13,6 +13,7 @@ current torch CUDA stream.
 """
 import ctypes
 import operator
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -47,13 +48,14 @@ class PageMap:
 # A step makes several of these calls per layer, and the GPU is done with a small one in ten microseconds.  So the checks of
 # types, shapes, strides and devices run once for each combination of them, and what they yield is kept under that combination
 # (never under a tensor or its address); a later call looks it up, checks its pointers and launches.
-_KEPT = {}
+_KEPT, _KEPT_LOCK = {}, threading.Lock()
 
 
 def _keep(key, checked):
-    if len(_KEPT) >= 1024:
-        _KEPT.clear()
-    _KEPT[key] = checked
+    with _KEPT_LOCK:
+        while len(_KEPT) >= 1024:
+            del _KEPT[next(iter(_KEPT))]  # the oldest
+        _KEPT[key] = checked
     return checked
 
 
@@ -153,13 +155,18 @@ def page_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, out
     the sum are padding).  Returns a PageMap: q_start [requests + 1], kv_lens [requests], slots [tokens] (int64:
     page * page_size + offset, -1 for padding and for tokens without a page), positions [tokens] (-1 for padding) and
     counts [4]: new tokens, pages taken, pages the free list lacked, requests longer than their table row."""
-    key = ("map", page_size, tokens, *_meta(ctx_lens), *_meta(new_lens), *_meta(free_pages), *_meta(block_table))
+    # the free list's length changes from step to step, and is checked here
+    n_free = free_pages.numel()
+    if n_free > _I32_MAX:
+        _check_size(n_free, "the length of free_pages")
+    key = ("map", page_size, tokens, *_meta(ctx_lens), *_meta(new_lens), *_meta(block_table), free_pages.dtype,
+           free_pages.dim(), free_pages.is_contiguous(), free_pages.get_device())
     if out is not None:
         key += (*_meta(out.q_start), *_meta(out.kv_lens), *_meta(out.slots), *_meta(out.positions), *_meta(out.counts))
     kept = _KEPT.get(key)
     if kept is None:
         kept = _keep(key, _check_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, out))
-    index, fn, n, n_free, cols, stride = kept
+    index, fn, n, cols, stride = kept
     if out is None:
         out = PageMap.empty(n, tokens, ctx_lens.device)
     _launch(index, fn, ctx_lens.data_ptr(), new_lens.data_ptr(), n, free_pages.data_ptr(), n_free, block_table.data_ptr(),
@@ -183,7 +190,7 @@ def _check_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, o
         _check_vec(out.slots, "out.slots", torch.int64, dev, tokens)
         _check_vec(out.positions, "out.positions", i32, dev, tokens)
         _check_vec(out.counts, "out.counts", i32, dev, 4)
-    return dev.index, _lib.lib().nq_page_map, n, free_pages.numel(), block_table.shape[1], block_table.stride(0)
+    return dev.index, _lib.lib().nq_page_map, n, block_table.shape[1], block_table.stride(0)
 
 
 def paged_append(K, V, K_pages, V_pages, slots):

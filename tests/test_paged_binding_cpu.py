@@ -67,3 +67,36 @@ def test_numbers_past_32_bits_do_not_wrap(paged, monkeypatch):
     with pytest.raises(ValueError, match="slots"):
         paged.paged_append(_Fake((big, 8, 128), H16), _Fake((big, 8, 128), H16), pool, pool, vec(big, I64))
     assert not paged.calls
+
+
+def test_checks_run_once_for_a_free_list_of_any_length(paged, monkeypatch):
+    """A free list gets shorter with almost every step: its length is no part of what the checks are kept under."""
+    from test_paged_cpu import I32, I64, _Fake
+
+    vec = lambda n, t=I32, **kw: _Fake((n,), t, **kw)
+    lens, table, runs, check = vec(3), _Fake((3, 7), I32), [], paged._check_map
+    out = paged.PageMap(vec(4), vec(3), vec(4, I64), vec(4), vec(4))
+    monkeypatch.setattr(paged, "_check_map", lambda *a: runs.append(1) or check(*a))
+    for n in (1, 900, 0, 37, 1000):
+        paged.page_map(lens, lens, vec(n), table, 16, 4, out=out)
+        assert paged.calls.pop()[2][4] == n
+    assert len(runs) == 1
+    # a single entry is contiguous whatever its stride, two are not
+    one, two = vec(1, strides=(2,)), vec(2, strides=(2,))
+    one._dense = True
+    paged.page_map(lens, lens, one, table, 16, 4, out=out)
+    with pytest.raises(ValueError, match="free_pages must be"):
+        paged.page_map(lens, lens, two, table, 16, 4, out=out)
+    with pytest.raises(ValueError, match="free_pages"):
+        paged.page_map(lens, lens, vec(2 ** 31), table, 16, 4, out=out)
+
+
+def test_new_shapes_do_not_drop_all_that_is_kept(paged):
+    """Steps whose token counts vary: the checks of one shape make room for one other, not for all."""
+    from test_paged_cpu import H16, I64, _Fake
+
+    pool = _Fake((10, 8, 16, 128), H16)
+    for n in range(1, 1300):
+        kv = _Fake((n, 8, 128), H16)
+        paged.paged_append(kv, kv, pool, pool, _Fake((n,), I64))
+        assert len(paged._KEPT) == min(n, 1024)
