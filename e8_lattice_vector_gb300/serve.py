@@ -33,9 +33,10 @@ class PagedCache:
 
     def extend(self, new):
         """Map a step that brings new[r] tokens for request r; returns its PageMap."""
-        dev = self.table.device
-        ctx = torch.tensor(self.lengths, dtype=torch.int32, device=dev)
-        m = page_map(ctx, torch.tensor(new, dtype=torch.int32, device=dev), self.free, self.table, self.page_size, sum(new))
+        dev, lens = self.table.device, torch.tensor([self.lengths, new], dtype=torch.int32)
+        # from pinned memory, so that the copy does not wait for the work before it
+        ctx, fresh = (lens.pin_memory() if dev.type == "cuda" else lens).to(dev, non_blocking=True)
+        m = page_map(ctx, fresh, self.free, self.table, self.page_size, sum(new))
         taken = sum(-(-(c + n) // self.page_size) - -(-c // self.page_size) for c, n in zip(self.lengths, new))
         self.free = self.free[taken:]
         self.lengths = [c + n for c, n in zip(self.lengths, new)]

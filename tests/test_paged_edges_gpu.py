@@ -143,3 +143,28 @@ def test_waits_are_limited_and_end_soon_after_another(nq, tmp_path):
     assert call(1, 20, ctypes.c_void_p(result.data_ptr())) == 0
     passed, flag, ns = result.tolist()
     assert passed == 0 and flag == 1 and ns < 20 * 1e5, "20 waits after another was given up took %.1f ms" % (ns * 1e-6)
+
+
+def test_serving_steps_do_not_wait_for_the_gpu(nq):
+    """A step is enqueued while the GPU is still busy with what came before it: its lengths are copied without waiting."""
+    import time
+
+    from e8_lattice_vector_gb300.serve import PagedCache
+
+    c = PagedCache(2, 3, 2, 64, 16, 200, torch.float16, torch.device(DEV, 0))
+    q, k, v = (torch.randn(2, 3, h, 64, device=DEV).half() for h in (8, 2, 2))
+    c.fill(*(torch.randn(2, 3, 2, 70, 64, device=DEV).half() for _ in range(2)))
+    for _ in range(3):
+        c.step(q, k, v, [1, 1, 1])
+    torch.cuda.synchronize()
+    busy = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    busy[0].record()
+    torch.cuda._sleep(400_000_000)  # about 0.2 s
+    busy[1].record()
+    at = time.perf_counter()
+    for _ in range(3):
+        c.step(q, k, v, [1, 1, 1])
+    took = time.perf_counter() - at
+    assert not busy[1].query(), "the steps waited for the work before them (%.3f s)" % took
+    torch.cuda.synchronize()
+    assert took < 0.5e-3 * busy[0].elapsed_time(busy[1])
