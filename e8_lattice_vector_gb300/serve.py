@@ -33,6 +33,11 @@ class PagedCache:
 
     def extend(self, new):
         """Map a step that brings new[r] tokens for request r; returns its PageMap."""
+        if len(new) != len(self.lengths) or any(n < 0 for n in new):
+            raise ValueError("a step brings a number of tokens for each of %d requests, got %s" % (len(self.lengths), new))
+        for c, n in zip(self.lengths, new):
+            if c + n > self.columns * self.page_size:
+                raise ValueError("%d tokens do not fit %d pages of %d" % (c + n, self.columns, self.page_size))
         dev, lens = self.table.device, torch.tensor([self.lengths, new], dtype=torch.int32)
         # from pinned memory, so that the copy does not wait for the work before it
         ctx, fresh = (lens.pin_memory() if dev.type == "cuda" else lens).to(dev, non_blocking=True)

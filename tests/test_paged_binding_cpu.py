@@ -100,3 +100,23 @@ def test_new_shapes_do_not_drop_all_that_is_kept(paged):
         kv = _Fake((n, 8, 128), H16)
         paged.paged_append(kv, kv, pool, pool, _Fake((n,), I64))
         assert len(paged._KEPT) == min(n, 1024)
+
+
+def test_a_paged_cache_refuses_what_does_not_fit(monkeypatch):
+    """More tokens than a request's table row holds would have nowhere to go: said before anything changes."""
+    from e8_lattice_vector_gb300 import serve
+
+    maps = []
+    monkeypatch.setattr(serve, "page_map", lambda *a: maps.append(a))
+    c = serve.PagedCache(1, 2, 1, 64, 16, 40, torch.float16, torch.device("cpu"))  # three pages each
+    c.extend([40, 1])
+    assert c.lengths == [40, 1] and c.free.numel() == 6 - 4 and len(maps) == 1
+    for new in ([9, 0], [0, 48], [-1, 1], [1], [1, 1, 1]):
+        with pytest.raises(ValueError):
+            c.extend(new)
+        assert c.lengths == [40, 1] and c.free.numel() == 2 and len(maps) == 1
+    c.extend([8, 47])  # to the end of the pages
+    assert c.lengths == [48, 48] and c.free.numel() == 0
+    ctx, new, free, table, page, tokens = maps[-1]
+    assert ctx.tolist() == [40, 1] and new.tolist() == [8, 47] and ctx.dtype == new.dtype == torch.int32
+    assert free.numel() == 2 and (page, tokens) == (16, 55)
