@@ -14,7 +14,7 @@ import json
 import torch
 
 from .codec import RopeTable, compress_kv, decompress_kv
-from .paged import page_map, paged_append, paged_attention, paged_attention_workspace
+from .paged import page_map, paged_append, paged_attention, paged_attention_workspace, paged_status
 from .synth import CONFIGS, make_cache
 
 
@@ -102,6 +102,7 @@ def serve(cfg, steps=4, new=1, q_heads=None, page_size=16, layers=None, tokens=N
         ms.append(events[0].elapsed_time(events[1]))
         diff += float((coded.double() - exact.double()).square().sum())
         norm += float(exact.double().square().sum())
+    paged_status(device)  # the report is void when a kernel gave up a wait
     return {"config": cfg.name, "layers": L, "requests": B, "cached_tokens": T, "new_tokens": new, "steps": steps,
             "q_heads": heads, "kv_heads": H, "head_dim": D, "page_size": page_size,
             "bits": [params.key_bits, params.value_bits], "compressed_share": buf.numel() / (2 * 2 * K.numel()),

@@ -168,3 +168,17 @@ def test_serving_steps_do_not_wait_for_the_gpu(nq):
     assert not busy[1].query(), "the steps waited for the work before them (%.3f s)" % took
     torch.cuda.synchronize()
     assert took < 0.5e-3 * busy[0].elapsed_time(busy[1])
+
+
+def test_the_serving_report_asks_whether_it_holds(nq, monkeypatch):
+    """No report is made of outputs that are void."""
+    from e8_lattice_vector_gb300 import _lib, serve
+    from e8_lattice_vector_gb300.synth import CONFIGS
+
+    def gave_up(device):
+        raise _lib.NQError("nq_paged_status", 4)
+
+    serve.serve(CONFIGS["tiny"], steps=1)
+    monkeypatch.setattr(serve, "paged_status", gave_up, raising=False)
+    with pytest.raises(_lib.NQError):
+        serve.serve(CONFIGS["tiny"], steps=1)
