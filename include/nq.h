@@ -361,8 +361,9 @@ typedef struct {
  * is a page of the pool, j <= p (causal) and j > p - window (window > 0):
  *   s_j = scale * q . k_j,  m = max s_j,  l = sum exp(s_j - m),
  *   out = sum exp(s_j - m) v_j / l,  lse = m + ln(l)
- * Scores, maxima, sums and accumulators are 32-bit; exp(s - m) is rounded to
- * the pool's type for its product with v, and out once at the end.  A row that
+ * Scores, maxima, sums and accumulators are 32-bit.  For its product with v, exp(s - m) is rounded to
+ * fp16 in an fp16 pool (a power of two larger, so that 2^-39 to 2^-32 of the largest is the least that
+ * counts), and to the sum of two bf16 in a bf16 pool (2^-17 of it).  out is rounded once at the end.  A row that
  * sees no key gets out = 0 and lse = -infinity.
  *   q, out   device, the pool's type; must not overlap
  *   lse      device float [tokens][q_heads], or NULL
@@ -373,7 +374,8 @@ typedef struct {
  * pages) hides its keys.  q_start must not decrease.  Where it does, a request
  * whose end is before its start has no rows, and rows before the end of an earlier request's
  * hold results of requests that claim them, or are left as they are.
- * Keys and values that some row of the request sees must be finite; what no
+ * Keys and values that some row of the request sees must be finite, and 2^8 times the sum of exp(s - m) |v|
+ * within fp32's range (fp16 values are, and bf16 values below 2^88 for any length); what no
  * row of it may see (slots past its length, pages outside its table) may hold anything.
  * The result does not depend on the run: no atomics, partial sums are added in a fixed order. */
 int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uint64_t* bytes);

@@ -182,3 +182,15 @@ def test_the_serving_report_asks_whether_it_holds(nq, monkeypatch):
     monkeypatch.setattr(serve, "paged_status", gave_up, raising=False)
     with pytest.raises(_lib.NQError):
         serve.serve(CONFIGS["tiny"], steps=1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_attention_weights_where_values_cancel(nq, dtype, new, D):
+    """Values of both signs over few keys: where they cancel, the output's own rounding is small and the weights' shows.  (In
+    bf16 the weights' first part alone passes the bound five to twenty times over.)"""
+    for L in (new + 2, new + 20):
+        s = Step([(L - new, new)], 4, 2, D, 16, dtype, seed=L)
+        put_keys(s, torch.randn(L, 2, D, device=DEV) * 0.4, torch.randn(L, 2, D, device=DEV))
+        check_weights(nq, s, D ** -0.5, new)
