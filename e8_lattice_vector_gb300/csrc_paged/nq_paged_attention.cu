@@ -152,21 +152,28 @@ int check_attention(const nq_attention* a, const nq_pool* pool) {
     return NQ_OK;
 }
 
-// The small kernel's calls: a request's rows for one KV head fit its tile, or some need a second one and most do not (32
-// requests of 1 to 5 tokens and 4 rows a token over a window of 4096, head_dim 64, bf16: 64 us, the large kernel 76; with 5 tokens
-// each it is 93 against 77), or a token's rows do not fit a half of the large kernel's row tile.
-bool few_rows(const nq_attention* a, int group) {
-    const int64_t longest = int64_t(std::min(a->max_q, a->tokens)) * group;
-    return longest <= kSmallRows || group > 128 ||
-           (longest <= 2 * kSmallRows && 4 * int64_t(a->tokens) * group <= 3 * kSmallRows * int64_t(a->requests));
-}
-
 // Whether most requests have far fewer rows than the longest: then the small kernel takes those that fit its tile and the
-// large kernel the others.  The large kernel alone spends tiles of 128 rows on single tokens: a chunk of 512 tokens and 31
-// single tokens over 8000 cached (32 heads on 8, head_dim 128, bf16) took it 249 us, and 221 us with both; the second pair
-// of launches costs 8 us where it finds nothing to do (eight prompts of 256 to 2048: 198 and 219 us).
+// large kernel the others.  The large kernel alone spends tiles of 128 rows on single tokens.  What both take, over what the large
+// one alone takes (32 heads on 8): 512 tokens beside 31 single tokens over 8000 cached 0.66 to 0.97 (head_dim 64 and 128, fp16 and
+// bf16; 252 against 301 us at 128 in bf16), over 2000 cached 0.83 to 1.14, 128 tokens beside 7 over 2000 1.08 to 1.30, and where the
+// small kernel finds nothing to do 1.05 to 1.11 (its two launches: 4 to 5 us).  The contexts, which decide, are not known here; a
+// long one gains more than a short one loses.
 bool may_mix(const nq_attention* a, int group) {
     return group <= kSmallRows && 4 * int64_t(a->tokens) < int64_t(a->requests) * a->max_q;
+}
+
+// The small kernel's calls: a request's rows for one KV head fit its tile, or some need a second one and most do not, or a
+// token's rows do not fit a half of the large kernel's row tile.  "Most do not": rows of three quarters of a tile on average, when
+// rows are short enough that reading keys twice costs less than the large kernel's tiles of 128 rows, else calls that would be mixed.
+// Drafts of 1 to 8 tokens for 32 requests over 2000 and 8000 cached and windows of 4096 (32 heads on 8, fp16 and bf16; what
+// the small kernel takes, over the large one or the mixed call): head_dim 64 0.64 to 1.05, 96 0.76 to 1.09, 128 0.78 to 1.01 where the
+// call would be mixed, and 0.98 to 1.18 where not.
+bool few_rows(const nq_attention* a, int group, int head_dim) {
+    const int64_t longest = int64_t(std::min(a->max_q, a->tokens)) * group;
+    if (longest <= kSmallRows || group > 128) return true;
+    if (longest > 2 * kSmallRows) return false;
+    return may_mix(a, group) ||
+           (head_dim <= 96 && 4 * int64_t(a->tokens) * group <= 3 * kSmallRows * int64_t(a->requests));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -262,7 +269,7 @@ int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uin
     const int group = a->q_heads / pool->kv_heads;
     // the large kernel's calls may be mixed; their size is the larger one in any case
     *bytes = nq::attn_workspace(nullptr, nq::kSmallRows, pool->head_dim).total;
-    if (!nq::few_rows(a, group)) *bytes += nq::chunk_workspace(a->tokens, group, a->requests, pool->head_dim);
+    if (!nq::few_rows(a, group, pool->head_dim)) *bytes += nq::chunk_workspace(a->tokens, group, a->requests, pool->head_dim);
     return NQ_OK;
 }
 
@@ -330,7 +337,7 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
     x.mixed = 0;
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
-    if (nq::few_rows(a, x.group)) return nq::launch_attention_small(x);
+    if (nq::few_rows(a, x.group, x.head_dim)) return nq::launch_attention_small(x);
     if (nq::may_mix(a, x.group)) {
         x.mixed = 1;
         const int small = nq::launch_attention_small(x);

@@ -120,3 +120,17 @@ def test_a_paged_cache_refuses_what_does_not_fit(monkeypatch):
     ctx, new, free, table, page, tokens = maps[-1]
     assert ctx.tolist() == [40, 1] and new.tolist() == [8, 47] and ctx.dtype == new.dtype == torch.int32
     assert free.numel() == 2 and (page, tokens) == (16, 55)
+
+
+@pytest.mark.parametrize("dim,tokens,max_q,small", [(64, 95, 5, True), (96, 95, 5, True), (128, 95, 5, False), (128, 39, 8, True),
+                                                    (128, 88, 8, False), (64, 97, 5, False), (64, 32, 1, True),
+                                                    (128, 128, 4, True), (64, 39, 9, False)])
+def test_which_kernel_takes_drafts(paged, dim, tokens, max_q, small):
+    """32 requests, four query heads on a KV head: the large kernel's calls need scratch for its plan."""
+    from test_paged_cpu import H16, I32, _Fake
+
+    pool, table = _Fake((10, 8, 16, dim), H16), _Fake((32, 7), I32)
+    q = _Fake((tokens, 32, dim), H16)
+    need = paged._attention(q, q, pool, None, table, 32, max_q, None, 1, 0)[2]
+    least = paged._attention(q, q, pool, None, table, 32, 1, None, 1, 0)[2]
+    assert (need == least) == small
