@@ -9,8 +9,9 @@ extern "C" void workspace_places(uint64_t base, int rows, int head_dim, uint64_t
     places[3] = w.total;
 }
 
-// The large kernel's plan, its sums formed one after the other, and every block's walk through it.  Each piece is eight
-// numbers: block, row of q, tokens, KV head, request, first key tile of the piece, key tiles of the piece, of the row tile.
+// The large kernel's plan, its sums formed one after the other, and every block's walk through it.  Each piece is eleven
+// numbers: block, row of q, tokens, KV head, request, first key tile of the piece, key tiles of the piece, of the row tile, whether
+// the halves share its rows, and each half's key tiles.
 // `last_block`: per block, of the row tile that it begins and does not end, or -1.  Returns the pieces, -1 when there are
 // more than `room`; *planned the pairs, *space their room.
 #include <vector>
@@ -69,7 +70,8 @@ extern "C" long long chunk_pieces(int tokens, int group, int kv_heads, int reque
         last_block[b] = -1;
         for (; x.left > 0; x.next(a, plan)) {
             if (n == room) return -1;
-            const int piece[8] = {b, x.q.begin + x.t.token0, x.t.n, x.head, x.r, x.tile, x.take, x.t.count};
+            const int piece[11] = {b,      x.q.begin + x.t.token0, x.t.n,      x.head,           x.r,             x.tile,
+                                   x.take, x.t.count,              x.t.shared, x.tiles_of(a, 0), x.tiles_of(a, 1)};
             for (int v : piece) *pieces++ = v;
             ++n;
             if (x.tile == 0 && !x.whole()) last_block[b] = x.last_block(start);

@@ -39,7 +39,7 @@ def test_workspace_is_aligned_for_any_caller(host, rows, head_dim, base):
 
 def walk(host, q_start, kv_lens, tokens, group, kv_heads, P=16, cols=1000, causal=1, window=0, mixed=0):
     R, room = len(kv_lens), 1 << 18
-    pieces, last = np.zeros((room, 8), np.int32), np.zeros(152, np.int32)
+    pieces, last = np.zeros((room, 11), np.int32), np.zeros(152, np.int32)
     starts, lens = np.array(q_start, np.int32), np.array(kv_lens, np.int32)
     planned, space = ctypes.c_longlong(), ctypes.c_longlong()
     host.chunk_pieces.restype = ctypes.c_longlong
@@ -57,7 +57,8 @@ def check_walk(host, q_start, kv_lens, tokens, group, kv_heads, mixed=0, **kw):
     assert planned <= space, "%d pairs, room for %d" % (planned, space)
     parts, owner = {}, np.full(tokens + 1, -1)
     seen_first = set()
-    for b, row, n, head, r, tile, take, count in pieces:
+    for b, row, n, head, r, tile, take, count, shared, first, second in pieces:
+        assert (first + second == take) if shared else (second == take and 1 <= first <= take)
         assert 0 <= row and n > 0 and row + n <= tokens and 0 <= head < kv_heads and take > 0
         if tile > 0:  # slot 0 of the block's two
             assert b not in seen_first
@@ -134,3 +135,37 @@ def test_every_wait_that_was_given_up_is_reported(host):
     grew = np.zeros(len(reads), np.int32)
     host.give_ups(flat.ctypes.data_as(ctypes.c_void_p), len(reads), grew.ctypes.data_as(ctypes.c_void_p))
     assert grew.tolist() == [r[3] for r in reads]
+
+
+def test_barriers_with_the_pieces_of_real_batches(host):
+    """The model of the large kernel's barriers, run with the pieces that the kernel's own walk gives its blocks."""
+    from test_paged_protocol_cpu import simulate
+
+    rng = np.random.default_rng(1)
+    lens = rng.integers(1, 260, 12)
+    kv = (lens + rng.integers(0, 900, 12) * (rng.random(12) < 0.7)).tolist()
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    for group, kv_heads, window in ((4, 8, 0), (1, 2, 300), (3, 8, 0)):
+        blocks = {}
+        for p in walk(host, starts, kv, int(starts[-1]), group, kv_heads, window=window)[0]:
+            b, take, shared, count = p[0], p[6], bool(p[8]), p[9:11]
+            mine = blocks.setdefault(b, [])
+            mine.append({"id": len(mine), "take": take, "shared": shared, "count": count})
+        for b in list(blocks)[::7]:
+            for stages in (5, 12):
+                simulate(b, stages, blocks[b])
+
+
+def test_the_model_has_the_kernels_numbers():
+    """Ring lengths and arrival counts, from the kernel's source."""
+    import re
+
+    import test_paged_protocol_cpu as model
+
+    folder = os.path.join(os.path.dirname(HERE), "e8_lattice_vector_gb300", "csrc_paged")
+    source = open(os.path.join(folder, "nq_paged_chunk.cu")).read()
+    number = lambda name: int(re.search(r"constexpr int %s = (\d+);" % name, source).group(1))
+    assert (number("kLiveRing"), number("kPieceRing"), number("kPieceReaders")) == (model.TILE_RING, model.PIECE_RING, model.READERS)
+    counts = dict(re.findall(r"mbar_init\(smem_ptr\(&c\.(\w+)(?:\[i\])?\), (\w+)\);", source))
+    one = dict.fromkeys(("empty", "k_full", "v_full", "clean", "q_full", "q_free", "s_full", "o_full", "piece_full", "drained"), "1")
+    assert counts == dict(one, p_full="4", merge_full="4", merge_free="4", piece_free="kPieceReaders")
