@@ -16,14 +16,15 @@
 // Shares: the row tiles' key tiles, in order, in equal parts over 152 blocks; a launch of one block finds where each part
 // begins.  Row tiles that end up in several blocks are joined by a second launch.
 //
-// Measured (32 query heads on 8 KV heads, head_dim 128, 2000 tokens over 30000 cached): fp16 676 us, 1504 TFLOP/s, 81% of the
-// measured cuBLAS rate; bf16 920 us, 1104 TFLOP/s.  What bounds it is the chain of one half: its exponentials (about 1200 of 3000
+// Measured (32 query heads on 8 KV heads, head_dim 128, 2000 tokens over 30000 cached, median of graph replays): fp16 706 us, 1438
+// TFLOP/s, 77% of the measured cuBLAS rate (the best replay 664; 736 to 768 in long streams of calls, under the power cap); bf16
+// 972 us, 1045 TFLOP/s (the best 922).  What bounds it is the chain of one half: its exponentials (about 1200 of 3000
 // cycles a tile), its two products (1024, 1536 in bf16) and the hand-overs between them, with the tensor cores busy 68% (bf16: 73%)
 // of the time under the profiler.  Taking the exponentials before the maximum is known, or starting the second product with
 // half of P, shortened the chain and took as long or longer.
 //
 // In bf16 P is the sum of two bf16 (hi + lo), each with its own product: one bf16 has 2^-8 of p as its rounding error, as much as
-// the output's own, and fp16 tensors, whose P has 2^-11, show that the second product costs 36% of the time.  It is the
+// the output's own, and fp16 tensors, whose P has 2^-11, show that the second product costs 38% of the time.  It is the
 // price of an output that is off by its own rounding and nothing else.
 #include "nq_paged_walk.cuh"
 
@@ -90,7 +91,7 @@ __device__ __forceinline__ int plan_top(int x, int* total) {
 // share.  `room`: pairs that the arrays hold, all there are.
 //
 // The order is request, KV head, row tile: the row tiles that read the same keys come one after the other, in a block and in
-// its neighbours, and find them in the L2 (with row tiles outside heads 2000 tokens over 30000 cached took 691 us, now 676).
+// its neighbours, and find them in the L2 (with row tiles outside heads 2000 tokens over 30000 cached took 2% longer).
 __global__ void __launch_bounds__(kPlanThreads) attention_plan_kernel(const AttnArgs a, const ChunkPlan plan, long long room) {
     __shared__ int s_pair[kPlanThreads];
     pdl_trigger();

@@ -10,8 +10,8 @@
 // (mma m16n8k16); the eight are joined through shared memory when a row tile ends.  tcgen05 has no shape this small that
 // would help: the tensor pipe is busy 17% of the time as it is.
 //
-// Measured: 64 requests over 16384 (32 query heads on 8 KV heads, head_dim 128, fp16, pages of 16) 611 us, 7.0 TB/s of K and V,
-// above the measured copy rate; one request over 131072 (40 on 8, bf16) 88 us, 6.1 TB/s; one over 1501 11 us, of which
+// Measured: 64 requests over 16384 (32 query heads on 8 KV heads, head_dim 128, fp16, pages of 16) 619 us, 6.9 TB/s of K and V,
+// above the measured copy rate; one request over 131072 (40 on 8, bf16) 88 us, 6.1 TB/s; one over 1501 10.3 us, of which
 // the launches, the first loads and the joining launch are all but one.  Bound by memory, and by about 12 us at both ends.
 #include "nq_paged_device.cuh"
 

@@ -247,7 +247,8 @@ def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=No
     Q [tokens, q_heads, head_dim] of the pool's type, strided; request r's rows are q_start[r] .. q_start[r + 1], and
     its row i stands at position kv_lens[r] - n + i of n.  max_q: a bound on a request's rows, which picks the
     kernel (default: all rows; results do not depend on it).  scale: head_dim ** -0.5 by default.  causal: keys up to
-    the row's own position.  window > 0: only the last `window` of those.  A row that sees nothing is 0.
+    the row's own position.  window > 0: only the last `window` of those.  A row that sees nothing is 0; rows of no
+    request (a padded step's) are not written.
     Returns out (as Q); with lse (float32 [tokens, q_heads], filled with the log of the sum of exponentials) (out,
     lse).  ws: scratch from paged_attention_workspace, allocated here when not given."""
     if max_q is not None and (type(max_q) is not int or not 0 <= max_q <= _I32_MAX):
