@@ -361,10 +361,11 @@ typedef struct {
  * is a page of the pool, j <= p (causal) and j > p - window (window > 0):
  *   s_j = scale * q . k_j,  m = max s_j,  l = sum exp(s_j - m),
  *   out = sum exp(s_j - m) v_j / l,  lse = m + ln(l)
- * Scores, maxima, sums and accumulators are 32-bit.  For its product with v, exp(s - m) is rounded to
- * fp16 in an fp16 pool (a power of two larger, so that 2^-39 to 2^-32 of the largest is the least that
- * counts), and to the sum of two bf16 in a bf16 pool (2^-17 of it).  out is rounded once at the end.  A row that
- * sees no key gets out = 0 and lse = -infinity.
+ * Scores, maxima, sums and accumulators are 32-bit.  For its product with v,
+ * exp(s - m) is rounded to fp16 in an fp16 pool (a power of two larger, so that
+ * 2^-39 to 2^-32 of the largest is the least that counts), and to the sum of two
+ * bf16 in a bf16 pool (2^-17 of it).  out is rounded once at the end.  A row
+ * that sees no key gets out = 0 and lse = -infinity.
  *   q, out   device, the pool's type; must not overlap
  *   lse      device float [tokens][q_heads], or NULL
  *   workspace  device scratch of nq_paged_attention_workspace() bytes, 16-byte
@@ -372,11 +373,12 @@ typedef struct {
  * Rows of no request are left as they are.  q_start is clamped to [0,
  * tokens], kv_lens to [0, table_cols * page_size]; a table entry outside [0,
  * pages) hides its keys.  q_start must not decrease.  Where it does, a request
- * whose end is before its start has no rows, and rows before the end of an earlier request's
- * hold results of requests that claim them, or are left as they are.
- * Keys and values that some row of the request sees must be finite, and 2^8 times the sum of exp(s - m) |v|
- * within fp32's range (fp16 values are, and bf16 values below 2^88 for any length); what no
- * row of it may see (slots past its length, pages outside its table) may hold anything.
+ * whose end is before its start has no rows, and rows before the end of an
+ * earlier request's hold results of requests that claim them, or are left.
+ * Keys and values that some row of the request sees must be finite, and 2^8
+ * times the sum of exp(s - m) |v| within fp32's range (fp16 values are, and bf16
+ * values below 2^88 for any length); what no row of it may see (slots past its
+ * length, pages outside its table) may hold anything.
  * The result does not depend on the run: no atomics, partial sums are added in a fixed order. */
 int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uint64_t* bytes);
 int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool, const void* k_pages,
@@ -385,11 +387,12 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
                        void* stream);
 
 /* Waits for `stream`, then returns NQ_ERR_CUDA if it failed or if an attention
- * kernel on the current device gave up waiting for its loads since that was last
- * reported (its outputs are then void), else NQ_OK.  Any thread may call it, while kernels run on other streams
- * too: a report covers what `stream` has done and what of the others is done, and none is lost.  A wait is given up after about two
- * seconds, and every later one of its block within 0.1 ms, except that for the block's own copies
- * at its end: two seconds again. */
+ * kernel on the current device gave up waiting for its loads since that was
+ * last reported (its outputs are then void), else NQ_OK.  Any thread may call
+ * it, also while kernels run on other streams: what they give up later is left
+ * for a later call.  A wait is given up after about two seconds, and every later
+ * one of its block within 0.1 ms, except that for the block's own copies at its
+ * end: two seconds again. */
 int nq_paged_status(void* stream);
 
 /* Static description of a status code. */

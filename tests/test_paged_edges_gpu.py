@@ -1,5 +1,4 @@
 """The paged operators at the edges of what callers may pass, against the same 64-bit reference as test_paged_gpu."""
-import numpy as np
 import pytest
 import torch
 
