@@ -79,6 +79,9 @@ struct AttnArgs {
     int mixed;      // both kernels are launched: the small one takes requests of at most kSmallRows rows, the large one others
     int out_by_32;  // rows of out start on 32-byte boundaries
     FastDiv by_group;
+    const unsigned long long* ancestors;  // drafted trees: [tokens][tree_words], or NULL
+    const int32_t* positions;
+    int tree_words;
     int half_tokens;  // tokens whose rows fit one half of the large kernel's row tile (0: a group of more than 128 heads)
     float scale;
     cudaStream_t stream;
@@ -134,6 +137,7 @@ bool make_query_map(const AttnArgs& a, CUtensorMap* q);
 
 int launch_attention_small(const AttnArgs& a);
 int launch_attention_chunk(const AttnArgs& a);
+int launch_attention_tree(const AttnArgs& a);
 uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim);
 // Join the pieces of split row tiles, launched after the small or the large kernel as its dependent.
 int launch_join_few_rows(const AttnArgs& a, const AttnWorkspace& ws);

@@ -260,6 +260,79 @@ int launch_join_many_rows(const AttnArgs& a, const AttnWorkspace& ws) {
 
 }  // namespace nq
 
+namespace nq {
+namespace {
+
+int attention(const nq_attention* a, const int64_t* ancestors, const int32_t* positions, int words, const void* q,
+              const nq_pool* pool, const void* k_pages, const void* v_pages, const int32_t* block_table,
+              const int32_t* q_start, const int32_t* kv_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+              void* stream) {
+    uint64_t need = 0;
+    const int st = nq_paged_attention_workspace(a, pool, &need);
+    if (st != NQ_OK) return st;
+    if (a->tokens == 0 || a->requests == 0) return NQ_OK;
+    if (!q || !k_pages || !v_pages || !q_start || !kv_lens || !out) return NQ_ERR_ARG;
+    if (a->table_cols > 0 && !block_table) return NQ_ERR_ARG;
+    if (need > 0 && !workspace) return NQ_ERR_ARG;
+    for (const void* p : {q, k_pages, v_pages, static_cast<const void*>(out), static_cast<const void*>(workspace)})
+        if (!paged_aligned(p, 16)) return NQ_ERR_ARG;
+    for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(q_start),
+                          static_cast<const void*>(kv_lens), static_cast<const void*>(lse)})
+        if (!paged_aligned(p, 4)) return NQ_ERR_ARG;
+    if (workspace_bytes < need) return NQ_ERR_SIZE;
+    AttnArgs x;
+    x.q = q;
+    x.out = out;
+    x.lse = lse;
+    x.table = block_table;
+    x.q_start = q_start;
+    x.kv_lens = kv_lens;
+    x.k_pages = k_pages;
+    x.v_pages = v_pages;
+    x.workspace = workspace;
+    x.table_stride = a->table_stride;
+    x.q_token_stride = a->q_token_stride;
+    x.q_head_stride = a->q_head_stride;
+    x.out_token_stride = a->out_token_stride;
+    x.out_head_stride = a->out_head_stride;
+    x.page_stride = pool->page_stride;
+    x.head_stride = pool->head_stride;
+    x.slot_stride = pool->slot_stride;
+    x.tokens = a->tokens;
+    x.q_heads = a->q_heads;
+    x.kv_heads = pool->kv_heads;
+    x.group = a->q_heads / pool->kv_heads;
+    x.requests = a->requests;
+    x.table_cols = a->table_cols;
+    x.page_shift = paged_page_shift(pool->page_size);
+    x.pages = pool->pages;
+    x.head_dim = pool->head_dim;
+    x.causal = a->causal;
+    x.window = a->window;
+    x.bf16 = pool->dtype == NQ_BF16;
+    x.out_by_32 = paged_aligned(out, 32) && (a->tokens == 1 || a->out_token_stride % 16 == 0) &&
+                  (a->q_heads == 1 || a->out_head_stride % 16 == 0);
+    x.by_group = FastDiv::by(uint32_t(x.group));
+    x.half_tokens = 128 / x.group;
+    x.mixed = 0;
+    x.ancestors = reinterpret_cast<const unsigned long long*>(ancestors);
+    x.positions = positions;
+    x.tree_words = words;
+    x.scale = a->scale;
+    x.stream = static_cast<cudaStream_t>(stream);
+    if (ancestors) return launch_attention_tree(x);
+    if (few_rows(a, x.group, x.head_dim)) return launch_attention_small(x);
+    if (may_mix(a, x.group)) {
+        x.mixed = 1;
+        const int small = launch_attention_small(x);
+        if (small != NQ_OK) return small;
+    }
+    return launch_attention_chunk(x);
+}
+
+}  // namespace
+}  // namespace nq
+
 extern "C" {
 
 int nq_paged_attention_workspace(const nq_attention* a, const nq_pool* pool, uint64_t* bytes) {
@@ -287,63 +360,19 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
                        const void* v_pages, const int32_t* block_table, const int32_t* q_start,
                        const int32_t* kv_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
                        void* stream) {
-    uint64_t need = 0;
-    const int st = nq_paged_attention_workspace(a, pool, &need);
-    if (st != NQ_OK) return st;
-    if (a->tokens == 0 || a->requests == 0) return NQ_OK;
-    if (!q || !k_pages || !v_pages || !q_start || !kv_lens || !out) return NQ_ERR_ARG;
-    if (a->table_cols > 0 && !block_table) return NQ_ERR_ARG;
-    if (need > 0 && !workspace) return NQ_ERR_ARG;
-    for (const void* p : {q, k_pages, v_pages, static_cast<const void*>(out), static_cast<const void*>(workspace)})
-        if (!nq::paged_aligned(p, 16)) return NQ_ERR_ARG;
-    for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(q_start),
-                          static_cast<const void*>(kv_lens), static_cast<const void*>(lse)})
-        if (!nq::paged_aligned(p, 4)) return NQ_ERR_ARG;
-    if (workspace_bytes < need) return NQ_ERR_SIZE;
-    nq::AttnArgs x;
-    x.q = q;
-    x.out = out;
-    x.lse = lse;
-    x.table = block_table;
-    x.q_start = q_start;
-    x.kv_lens = kv_lens;
-    x.k_pages = k_pages;
-    x.v_pages = v_pages;
-    x.workspace = workspace;
-    x.table_stride = a->table_stride;
-    x.q_token_stride = a->q_token_stride;
-    x.q_head_stride = a->q_head_stride;
-    x.out_token_stride = a->out_token_stride;
-    x.out_head_stride = a->out_head_stride;
-    x.page_stride = pool->page_stride;
-    x.head_stride = pool->head_stride;
-    x.slot_stride = pool->slot_stride;
-    x.tokens = a->tokens;
-    x.q_heads = a->q_heads;
-    x.kv_heads = pool->kv_heads;
-    x.group = a->q_heads / pool->kv_heads;
-    x.requests = a->requests;
-    x.table_cols = a->table_cols;
-    x.page_shift = nq::paged_page_shift(pool->page_size);
-    x.pages = pool->pages;
-    x.head_dim = pool->head_dim;
-    x.causal = a->causal;
-    x.window = a->window;
-    x.bf16 = pool->dtype == NQ_BF16;
-    x.out_by_32 = nq::paged_aligned(out, 32) && (a->tokens == 1 || a->out_token_stride % 16 == 0) &&
-                  (a->q_heads == 1 || a->out_head_stride % 16 == 0);
-    x.by_group = nq::FastDiv::by(uint32_t(x.group));
-    x.half_tokens = 128 / x.group;
-    x.mixed = 0;
-    x.scale = a->scale;
-    x.stream = static_cast<cudaStream_t>(stream);
-    if (nq::few_rows(a, x.group, x.head_dim)) return nq::launch_attention_small(x);
-    if (nq::may_mix(a, x.group)) {
-        x.mixed = 1;
-        const int small = nq::launch_attention_small(x);
-        if (small != NQ_OK) return small;
-    }
-    return nq::launch_attention_chunk(x);
+    return nq::attention(a, nullptr, nullptr, 0, q, pool, k_pages, v_pages, block_table, q_start, kv_lens, out, lse, workspace,
+                         workspace_bytes, stream);
+}
+
+int nq_paged_tree_attention(const nq_attention* a, const int64_t* ancestors, const int32_t* positions, int32_t words,
+                            const void* q, const nq_pool* pool, const void* k_pages, const void* v_pages,
+                            const int32_t* block_table, const int32_t* q_start, const int32_t* kv_lens, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    if (!a || words < 1 || words > NQ_TREE_WORDS || a->causal != 1) return NQ_ERR_ARG;
+    if (a->tokens > 0 && a->requests > 0 && (!ancestors || !positions)) return NQ_ERR_ARG;
+    if (!nq::paged_aligned(ancestors, 8) || !nq::paged_aligned(positions, 4)) return NQ_ERR_ARG;
+    return nq::attention(a, ancestors, positions, words, q, pool, k_pages, v_pages, block_table, q_start, kv_lens, out, lse,
+                         workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

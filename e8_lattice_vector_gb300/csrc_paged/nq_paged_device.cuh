@@ -180,4 +180,17 @@ __host__ __device__ __forceinline__ int keys_to(const AttnArgs& a, int kv, int p
     return a.causal ? max(min(kv, p + 1), 0) : kv;
 }
 
+// ------------------------------------------------------------- drafted trees
+
+// First key that drafted token i of a request, at row t, may see: its position comes from memory, and a node of a tree stands
+// somewhere between its root's place and its own in the row order.  The window is for cached keys, the drafted ones have bits.
+__device__ __forceinline__ int tree_keys_from(const AttnArgs& a, const Request& q, int t, int i) {
+    const int ctx = q.kv - q.n;
+    return min(keys_from(a, min(max(a.positions[t], ctx), ctx + i)), max(ctx, 0));
+}
+// Whether row t sees the request's drafted token j >= 0.
+__device__ __forceinline__ bool tree_sees(const AttnArgs& a, int t, int j) {
+    return j >> 6 < a.tree_words && (a.ancestors[int64_t(t) * a.tree_words + (j >> 6)] >> (j & 63) & 1);
+}
+
 }  // namespace nq

@@ -21,7 +21,8 @@ import torch
 from . import _lib
 from .codec import _on, ctypes_ref, workspace
 
-__all__ = ["PageMap", "page_map", "paged_append", "paged_attention", "paged_attention_workspace", "paged_status"]
+__all__ = ["PageMap", "page_map", "page_release", "paged_append", "paged_attention", "paged_attention_workspace",
+           "paged_compact", "paged_status"]
 
 _DTYPES = {torch.float16: _lib.NQ_F16, torch.bfloat16: _lib.NQ_BF16}
 
@@ -241,7 +242,7 @@ def paged_attention_workspace(Q, K_pages, block_table, max_q=None):
 
 
 def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=None, scale=None, causal=True,
-                    window=0, out=None, lse=None, ws=None):
+                    window=0, out=None, lse=None, ws=None, tree=None):
     """Attention of the step's tokens over the paged cache, their own keys included (append first).
 
     Q [tokens, q_heads, head_dim] of the pool's type, strided; request r's rows are q_start[r] .. q_start[r + 1], and
@@ -249,6 +250,8 @@ def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=No
     kernel (default: all rows; results do not depend on it).  scale: head_dim ** -0.5 by default.  causal: keys up to
     the row's own position.  window > 0: only the last `window` of those.  A row that sees nothing is 0; rows of no
     request (a padded step's) are not written.
+    tree: the DraftTree of a step whose rows are drafted trees: a row sees the request's cached tokens (the last `window` before
+    its position) and, of the drafted ones, those that its bits name up to itself.
     Returns out (as Q); with lse (float32 [tokens, q_heads], filled with the log of the sum of exponentials) (out,
     lse).  ws: scratch from paged_attention_workspace, allocated here when not given."""
     if max_q is not None and (type(max_q) is not int or not 0 <= max_q <= _I32_MAX):
@@ -260,10 +263,12 @@ def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=No
     causal = 1 if causal else 0
     key = ("attention", max_q, scale, causal, window, *_meta(Q), *_meta(K_pages), *_meta(V_pages), *_meta(block_table),
            *_meta(q_start), *_meta(kv_lens), None if out is None else _meta(out), None if lse is None else _meta(lse))
+    if tree is not None:
+        key += (*_meta(tree.ancestors), *_meta(tree.positions))
     kept = _KEPT.get(key)
     if kept is None:
         kept = _keep(key, _check_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q, scale, causal, window,
-                                           out, lse))
+                                           out, lse, tree))
     index, fn, pool, a, need = kept
     if out is None:
         out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
@@ -276,12 +281,14 @@ def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=No
         raise ValueError("ws must be a contiguous uint8 CUDA tensor on the call's device")
     elif ws.numel() < need:
         raise ValueError("ws has %d bytes; the call needs %d" % (ws.numel(), need))
-    _launch(index, fn, a, q, pool, k, v, block_table.data_ptr(), q_start.data_ptr(), kv_lens.data_ptr(), o,
+    what = (a,) if tree is None else (a, tree.ancestors.data_ptr(), tree.positions.data_ptr(), tree.ancestors.shape[1])
+    _launch(index, fn, *what, q, pool, k, v, block_table.data_ptr(), q_start.data_ptr(), kv_lens.data_ptr(), o,
             None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out if lse is None else (out, lse)
 
 
-def _check_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q, scale, causal, window, out, lse):
+def _check_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q, scale, causal, window, out, lse,
+                     tree=None):
     pool, dev, dtype = _pool(K_pages, V_pages), K_pages.device, K_pages.dtype
     if Q.dim() != 3:
         raise ValueError("Q must be [tokens, q_heads, head_dim], got %s" % (tuple(Q.shape),))
@@ -300,8 +307,104 @@ def _check_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q, 
     if lse is not None and not (lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (tokens, heads) and
                                 lse.device == dev):
         raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads] on the call's device")
+    fn = _lib.lib().nq_paged_attention
+    if tree is not None:
+        check_tree(tree, tokens, dev)
+        if not causal:
+            raise ValueError("a drafted tree is causal: every token sees its ancestors")
+        fn = _lib.lib().nq_paged_tree_attention
     pool, a, need = _attention(Q, out, K_pages, V_pages, block_table, n, max_q, scale, causal, window)
-    return dev.index, _lib.lib().nq_paged_attention, ctypes_ref(pool), ctypes_ref(a), need
+    return dev.index, fn, ctypes_ref(pool), ctypes_ref(a), need
+
+
+def check_tree(tree, tokens, device, name="tree"):
+    """A DraftTree's tensors, whose width the caller may read afterwards."""
+    bits = tree.ancestors
+    if not (bits.is_cuda and bits.dtype == torch.int64 and bits.dim() == 2 and bits.is_contiguous()):
+        raise ValueError("%s.ancestors must be a contiguous 2-D int64 CUDA tensor [tokens, words]" % name)
+    if bits.shape[0] != tokens or not 1 <= bits.shape[1] <= _lib.NQ_TREE_WORDS:
+        raise ValueError("%s.ancestors has shape %s; the call needs %d rows of 1 to %d words"
+                         % (name, tuple(bits.shape), tokens, _lib.NQ_TREE_WORDS))
+    if bits.device != device:
+        raise ValueError("%s.ancestors is on %s; the call runs on %s" % (name, bits.device, device))
+    _check_vec(tree.positions, name + ".positions", torch.int32, device, tokens)
+
+
+def paged_compact(K_pages, V_pages, block_table, q_start, kv_lens, path):
+    """Move the accepted rows of a step's drafted tokens to the front of their requests' rows, in all layers at once.
+
+    Pools as elsewhere, or [layers, pages, kv_heads, page_size, head_dim].  q_start and kv_lens are the step's; path
+    (int32 [tokens], from verify_drafts) holds at a request's rows the accepted ones in order: its k-th entry's K and V become
+    row k's, up to the first entry that does not increase (-1 behind the last).  Returns the pools."""
+    key = ("compact", *_meta(K_pages), *_meta(V_pages), *_meta(block_table), *_meta(q_start), *_meta(kv_lens), *_meta(path))
+    kept = _KEPT.get(key)
+    if kept is None:
+        kept = _keep(key, _check_compact(K_pages, V_pages, block_table, q_start, kv_lens, path))
+    index, fn, pool, layers, layer_stride, stride, cols, requests, tokens = kept
+    k, v = K_pages.data_ptr(), V_pages.data_ptr()
+    if (k | v) & 15:
+        _check_starts(K_pages=K_pages, V_pages=V_pages)
+    _launch(index, fn, pool, layers, layer_stride, k, v, block_table.data_ptr(), stride, cols, q_start.data_ptr(),
+            kv_lens.data_ptr(), requests, path.data_ptr(), tokens)
+    return K_pages, V_pages
+
+
+def _check_compact(K_pages, V_pages, block_table, q_start, kv_lens, path):
+    layers = layer_stride = 0
+    if K_pages.dim() == 5:
+        layers, layer_stride = K_pages.shape[0], K_pages.stride(0)
+        _check_size(layers, "the layers of K_pages")
+        if V_pages.dim() != 5 or V_pages.shape[0] != layers or V_pages.stride(0) != layer_stride:
+            raise ValueError("V_pages must have K_pages' type, shape, strides and device")
+        if layers == 0:
+            raise ValueError("K_pages has no layers")
+        if layers > 1 and layer_stride % 8:
+            raise ValueError("K_pages has stride %d along axis 0; the kernels need multiples of 8" % layer_stride)
+        pool = _pool(K_pages[0], V_pages[0])
+    else:
+        pool = _pool(K_pages, V_pages)
+    dev, n = K_pages.device, kv_lens.numel()
+    _check_vec(path, "path", torch.int32, dev, path.numel())
+    _check_vec(kv_lens, "kv_lens", torch.int32, dev, n)
+    _check_vec(q_start, "q_start", torch.int32, dev, n + 1)
+    _check_table(block_table, n, dev)
+    return (dev.index, _lib.lib().nq_paged_compact, ctypes_ref(pool), max(layers, 1), layer_stride, block_table.stride(0),
+            block_table.shape[1], n, path.shape[0])
+
+
+def page_release(block_table, kv_lens, keep_lens, page_size, free_pages, top, out=None):
+    """Give back the pages past the tokens that requests keep (device int32 [requests] each: tokens with pages, tokens to keep).
+
+    free_pages (int32, updated in place) is the whole free list, a stack whose free part begins at `top`: free_pages[top:] is what
+    page_map is given.  The k-th released page, requests and columns in order, goes to free_pages[top - 1 - k].
+    Returns counts [2]: pages released (top is lower by as many), those that found no room.  The table stays as it is."""
+    n_free = free_pages.numel()
+    if not 0 <= top <= n_free or n_free > _I32_MAX:
+        raise ValueError("top is %d; free_pages has %d entries" % (top, n_free))
+    key = ("release", page_size, *_meta(block_table), *_meta(kv_lens), *_meta(keep_lens), free_pages.dtype, free_pages.dim(),
+           free_pages.is_contiguous(), free_pages.get_device(), None if out is None else _meta(out))
+    kept = _KEPT.get(key)
+    if kept is None:
+        kept = _keep(key, _check_release(block_table, kv_lens, keep_lens, page_size, free_pages, out))
+    index, fn, n, cols, stride = kept
+    if out is None:
+        out = torch.empty(2, dtype=torch.int32, device=kv_lens.device)
+    _launch(index, fn, block_table.data_ptr(), stride, cols, kv_lens.data_ptr(), keep_lens.data_ptr(), n, page_size,
+            free_pages.data_ptr(), operator.index(top), out.data_ptr())
+    return out
+
+
+def _check_release(block_table, kv_lens, keep_lens, page_size, free_pages, out):
+    dev, n, i32 = kv_lens.device, kv_lens.numel(), torch.int32
+    if page_size > 0:  # others are the library's to refuse
+        _check_size(page_size, "page_size")
+    _check_vec(kv_lens, "kv_lens", i32, dev, n)
+    _check_vec(keep_lens, "keep_lens", i32, dev, n)
+    _check_vec(free_pages, "free_pages", i32, dev, free_pages.numel())
+    _check_table(block_table, n, dev)
+    if out is not None:
+        _check_vec(out, "out", i32, dev, 2)
+    return dev.index, _lib.lib().nq_page_release, n, block_table.shape[1], block_table.stride(0)
 
 
 def paged_status(device=None):

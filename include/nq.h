@@ -287,7 +287,7 @@ int nq_e8_nearest(const float* u, float* out, int64_t n_blocks, int strict, int 
  * (each call says how): no table, length or slot makes a call read or write
  * outside the buffers that its host arguments describe. */
 
-enum { NQ_F16 = 0, NQ_BF16 = 1 };
+enum { NQ_F16 = 0, NQ_BF16 = 1, NQ_F32 = 2 };
 
 /* A page pool, the same for K and for V (two buffers of one layout): element
  * (page, head, slot, d) sits at page * page_stride + head * head_stride +
@@ -385,6 +385,100 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
                        const void* v_pages, const int32_t* block_table, const int32_t* q_start,
                        const int32_t* kv_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
                        void* stream);
+
+/* Drafted trees.  A step may bring a tree of drafted tokens for each request
+ * instead of tokens in a row: the request's rows q_start[r] .. q_start[r + 1]
+ * are the tree's nodes, every node after its parent.  They are appended like any
+ * other tokens, node i at the place of token c + i with c = kv_lens[r] - n.  Such
+ * a step is nq_page_map and nq_draft_tree once, nq_paged_append and
+ * nq_paged_tree_attention per layer, then nq_verify_drafts,
+ * nq_paged_compact for all layers at once, and nq_page_release. */
+
+/* Words of 64 bits that a node's ancestors may take: requests of up to 4096 drafted tokens. */
+#define NQ_TREE_WORDS 64
+
+/* The map of a step's trees.
+ *   parents    device int32[tokens]: the parent's number in its request; -1 (and
+ *              any number that is not below the node's own) = none, the node
+ *              follows the cached tokens
+ *   ancestors  device int64[tokens][words]: bit j & 63 of word j >> 6 says that the
+ *              row's node is j or descends from j; with window > 0, that j is also
+ *              fewer than `window` levels above it.  Bits past the words are left out
+ *   positions  device int32[tokens]: c + the number of the node's ancestors
+ * 1 <= words <= NQ_TREE_WORDS.  q_start is clamped to [0, tokens].  Rows of no
+ * request are left as they are. */
+int nq_draft_tree(const int32_t* parents, int32_t tokens, const int32_t* q_start, const int32_t* kv_lens,
+                  int32_t requests, int32_t window, int32_t words, int64_t* ancestors, int32_t* positions,
+                  void* stream);
+
+/* nq_paged_attention of drafted trees.  Row i of n sees, of the keys that the
+ * table shows, key j < c when window = 0 or j > positions - window (positions
+ * are clamped to [c, c + i]), and key c + j, j <= i, when the row's bit j is
+ * set.  ancestors and positions as nq_draft_tree leaves them; bits past row i's
+ * own and past the words are not set.  causal has to be 1.  Keys and values of
+ * all drafted rows must be finite; all else, the workspace too, is as there. */
+int nq_paged_tree_attention(const nq_attention* a, const int64_t* ancestors, const int32_t* positions, int32_t words,
+                            const void* q, const nq_pool* pool, const void* k_pages, const void* v_pages,
+                            const int32_t* block_table, const int32_t* q_start, const int32_t* kv_lens, void* out,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Which drafted tokens the model's probabilities accept, and the token that follows them.
+ * Node 0 of a request is a token that is certain already (the last step's);
+ * the others are drafts that follow their parents.
+ *   probs        device [tokens][vocab] of dtype (NQ_F32, NQ_F16, NQ_BF16), rows
+ *                probs_stride elements apart: row i is what the model says of the
+ *                token after node i
+ *   draft_probs  the same from the draft, whose row i the children of node i were
+ *                drawn from, independently; NULL when the drafts were not drawn (the
+ *                most likely tokens, say)
+ *   drafts       device int32[tokens]: the nodes' tokens; one outside [0, vocab) is no draft
+ *   parents      as in nq_draft_tree
+ *   uniform      device float[tokens], in [0, 1): a draft's own number at its row,
+ *                the number of the token that follows at the request's first row
+ * The walk begins at cur = 0 with w = p_cur, S = 1 and takes the drafts i = 1, 2, ...
+ * whose parent is cur, x the draft's token and q = q_cur (without draft_probs q is 1 at x
+ * and 0 elsewhere): when uniform[i] * S * q(x) < w(x), i is accepted and the
+ * walk goes on from cur = i with w = p_cur, S = 1.  When not, w becomes max(w - S q, 0)
+ * (without draft_probs: w with w(x) = 0), and S the sum of w (S - w(x)).  The token that
+ * follows is the lowest x whose running sum of w is above uniform[0] times the sum of w; where
+ * no w is left, of p_cur.  So each token of the result is one of the model's own.
+ *   accepted    device int32[requests]: accepted nodes, node 0 among them; 0 without rows
+ *   path        device int32[tokens]: at the request's rows the accepted nodes in order, then -1
+ *   tokens_out  device int32[tokens]: at the request's rows the tokens of the accepted
+ *               nodes but the first, then the one that follows, then -1: as many as accepted
+ * Probabilities are >= 0; NaN and negative ones count as 0.  Sums over the
+ * vocabulary, S and the comparisons carry at least 44 bits.  When all p_cur are 0 the token that
+ * follows is -1.  q_start is clamped to [0, tokens]; rows of no request are
+ * left as they are.  Outputs must not overlap inputs.
+ * The result does not depend on the run. */
+int nq_verify_drafts(const void* probs, int64_t probs_stride, const void* draft_probs, int64_t draft_stride,
+                     int32_t dtype, int32_t vocab, const int32_t* drafts, const int32_t* parents,
+                     const float* uniform, int32_t tokens, const int32_t* q_start, int32_t requests,
+                     int32_t* accepted, int32_t* path, int32_t* tokens_out, void* stream);
+
+/* Move the accepted rows of drafted tokens to the front, in all layers.
+ * For k = 0, 1, ...: the K and V row of request r's token c + path[k] (path at
+ * the request's rows, device int32[tokens]) is copied to token c + k, while path[k] is
+ * above path[k - 1] (path[0] >= 0) and below n; the first entry that is not ends the
+ * request's moves.  Tokens without a page of the pool are passed over.  Pools:
+ * `layers` of them, layer_stride elements apart (a multiple of 8).  q_start and kv_lens are those of
+ * the step, clamped as in nq_paged_attention.  Requests must not share pages. */
+int nq_paged_compact(const nq_pool* pool, int32_t layers, int64_t layer_stride, void* k_pages, void* v_pages,
+                     const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* q_start,
+                     const int32_t* kv_lens, int32_t requests, const int32_t* path, int32_t tokens, void* stream);
+
+/* Give back the pages past the tokens that requests keep.
+ * Request r's columns from ceil(keep_lens[r] / page_size) to ceil(kv_lens[r] /
+ * page_size) (both device int32[requests], at least 0; columns past table_cols do not count) are
+ * released, requests in order, columns in order: the k-th goes to free_pages[top - 1 - k].
+ * The free list is a stack: free_pages[top ...] is what nq_page_map is given, and top is
+ * lower by counts[0] afterwards.
+ *   counts  device int32[2]: columns released; those among them for which
+ *           there was no room (k >= top), which go nowhere
+ * Entries are copied, not checked; the table is left as it is. */
+int nq_page_release(const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
+                    const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top,
+                    int32_t* counts, void* stream);
 
 /* Waits for `stream`, then returns NQ_ERR_CUDA if it failed or if an attention
  * kernel on the current device gave up waiting for its loads since that was
