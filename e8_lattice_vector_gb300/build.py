@@ -19,7 +19,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["nq_api.cu", "nq_compress.cu", "nq_compress_delta.cu", "nq_decompress.cu", "nq_decompress_delta.cu", "nq_roundtrip.cu", "nq_stats.cu", "nq_layers.cu", "nq_noalloc.cu"]
 # the paged-cache operators, in a folder of their own: the codec's traffic record names a hash of csrc
 PAGED_SOURCES = ["nq_page_map.cu", "nq_paged_append.cu", "nq_paged_attention.cu", "nq_paged_small.cu",
-                 "nq_paged_chunk.cu", "nq_paged_tree.cu", "nq_draft_tree.cu", "nq_verify_drafts.cu", "nq_paged_compact.cu",
+                 "nq_paged_chunk.cu", "nq_draft_tree.cu", "nq_verify_drafts.cu", "nq_paged_compact.cu",
                  "nq_page_release.cu"]
 
 

@@ -137,7 +137,6 @@ bool make_query_map(const AttnArgs& a, CUtensorMap* q);
 
 int launch_attention_small(const AttnArgs& a);
 int launch_attention_chunk(const AttnArgs& a);
-int launch_attention_tree(const AttnArgs& a);
 uint64_t chunk_workspace(int64_t tokens, int group, int requests, int head_dim);
 // Join the pieces of split row tiles, launched after the small or the large kernel as its dependent.
 int launch_join_few_rows(const AttnArgs& a, const AttnWorkspace& ws);

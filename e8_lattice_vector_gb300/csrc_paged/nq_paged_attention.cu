@@ -320,7 +320,6 @@ int attention(const nq_attention* a, const int64_t* ancestors, const int32_t* po
     x.tree_words = words;
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
-    if (ancestors) return launch_attention_tree(x);
     if (few_rows(a, x.group, x.head_dim)) return launch_attention_small(x);
     if (may_mix(a, x.group)) {
         x.mixed = 1;

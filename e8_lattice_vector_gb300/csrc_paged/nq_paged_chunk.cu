@@ -312,7 +312,8 @@ struct __align__(16) Piece {
     int kv, key0, lo, hi;
     int head, request;
     int slot;           // workspace slot for the results, -1: the piece is the whole row tile
-    int pad[2];
+    int ctx;            // the request's cached keys, before its rows' own
+    int pad;
 };
 
 struct ChunkControl {
@@ -331,7 +332,7 @@ struct ChunkControl {
 };
 constexpr int kPieceReaders = 11;  // eight softmax warps, loads, products, clearing
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TREE>
 __global__ void __launch_bounds__(kThreadsChunk, 1)
     attention_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                            const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map,
@@ -589,6 +590,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     w.n = x.t.n;
                     w.pos = x.q.kv - x.q.n + x.t.token0;
                     w.kv = x.q.kv;
+                    w.ctx = x.q.kv - x.q.n;
                     w.key0 = (x.t.first + x.tile) * kKeyTile;
                     w.lo = x.t.lo;
                     w.hi = x.t.hi;
@@ -646,9 +648,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             const int first = w.shared ? 0 : h * a.half_tokens, n_tokens = min(w.n - first, a.half_tokens);
             const bool mine = row_token < n_tokens;
             const int token = first + min(row_token, n_tokens - 1), head = w.head * a.group + row_head;
-            const int lo = keys_from(a, w.pos + token), hi = keys_to(a, w.kv, w.pos + token);
+            const int lo = TREE ? tree_keys_from(a, w.row + token, w.ctx, w.pos + token) : keys_from(a, w.pos + token);
+            const int hi = keys_to(a, w.kv, w.pos + token);
             // keys [all_lo, all_hi) are seen by every row of the half
-            const int all_lo = keys_from(a, w.pos + first + n_tokens - 1), all_hi = keys_to(a, w.kv, w.pos + first);
+            const int all_lo = keys_from(a, w.pos + first + n_tokens - 1), all_hi = TREE ? w.ctx : keys_to(a, w.kv, w.pos + first);
             const int ppt = max(kKeyTile >> a.page_shift, 1);
             const uint32_t all = uint32_t((1ull << ppt) - 1);
             // p = 2^(s sc + neg), lifted in fp16.  neg is the fp32 number nearest to lift - m sc, and rest what it leaves of that; a
@@ -667,7 +670,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
 #pragma unroll 1
                     for (int x = 0; x < kKeyTile; x += 16) {
                         const bool page = live >> (x >> a.page_shift) & 1u;
-                        const uint32_t see = page ? low_bits(to - x) & ~low_bits(from - x) : 0u;
+                        uint32_t see = page ? low_bits(to - x) & ~low_bits(from - x) : 0u;
+                        if constexpr (TREE) see &= tree_bits(a, w.row + token, w.ctx, key0 + x);
                         if (__all_sync(0xffffffffu, (see & 0xffffu) == 0xffffu)) continue;
                         float y[16];
                         if (__any_sync(0xffffffffu, (see & 0xffffu) != 0u)) {
@@ -852,10 +856,10 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
     }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TREE>
 int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                  const AttnWorkspace& ws, const ChunkPlan& plan) {
-    if (!ensure_smem(reinterpret_cast<const void*>(attention_chunk_kernel<D, BF16>), Chunk<D>::SMEM)) return NQ_ERR_CUDA;
+    if (!ensure_smem(reinterpret_cast<const void*>(attention_chunk_kernel<D, BF16, TREE>), Chunk<D>::SMEM)) return NQ_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -866,17 +870,17 @@ int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm
     cfg.stream = a.stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_chunk_kernel<D, BF16>, a, km, vm, qm, ws, plan);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_chunk_kernel<D, BF16, TREE>, a, km, vm, qm, ws, plan);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
-template <bool BF16>
+template <bool BF16, bool TREE>
 int launch_chunk(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                  const AttnWorkspace& ws, const ChunkPlan& plan) {
     switch (a.head_dim) {
-        case 64: return launch_chunk<64, BF16>(a, km, vm, qm, ws, plan);
-        case 96: return launch_chunk<96, BF16>(a, km, vm, qm, ws, plan);
-        default: return launch_chunk<128, BF16>(a, km, vm, qm, ws, plan);
+        case 64: return launch_chunk<64, BF16, TREE>(a, km, vm, qm, ws, plan);
+        case 96: return launch_chunk<96, BF16, TREE>(a, km, vm, qm, ws, plan);
+        default: return launch_chunk<128, BF16, TREE>(a, km, vm, qm, ws, plan);
     }
 }
 
@@ -898,7 +902,9 @@ int launch_attention_chunk(const AttnArgs& a) {
     const ChunkPlan plan = chunk_plan(base + ws.total, pairs, a.requests, &bytes);
     attention_plan_kernel<<<1, kPlanThreads, 0, a.stream>>>(a, plan, pairs);
     if (cudaGetLastError() != cudaSuccess) return NQ_ERR_CUDA;
-    const int st = a.bf16 ? launch_chunk<true>(a, km, vm, qm, ws, plan) : launch_chunk<false>(a, km, vm, qm, ws, plan);
+    const int st = a.ancestors
+                       ? a.bf16 ? launch_chunk<true, true>(a, km, vm, qm, ws, plan) : launch_chunk<false, true>(a, km, vm, qm, ws, plan)
+                       : a.bf16 ? launch_chunk<true, false>(a, km, vm, qm, ws, plan) : launch_chunk<false, false>(a, km, vm, qm, ws, plan);
     return st == NQ_OK ? launch_join_many_rows(a, ws) : st;
 }
 

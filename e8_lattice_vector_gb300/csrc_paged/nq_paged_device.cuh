@@ -182,15 +182,21 @@ __host__ __device__ __forceinline__ int keys_to(const AttnArgs& a, int kv, int p
 
 // ------------------------------------------------------------- drafted trees
 
-// First key that drafted token i of a request, at row t, may see: its position comes from memory, and a node of a tree stands
-// somewhere between its root's place and its own in the row order.  The window is for cached keys, the drafted ones have bits.
-__device__ __forceinline__ int tree_keys_from(const AttnArgs& a, const Request& q, int t, int i) {
-    const int ctx = q.kv - q.n;
-    return min(keys_from(a, min(max(a.positions[t], ctx), ctx + i)), max(ctx, 0));
+// A row sees cached keys from tree_keys_from on and those drafted keys, up to its own, that its bits name.
+
+// First key of a drafted token at row t, whose request's cached keys end at ctx and which has the place `place` in the row order: its
+// position comes from memory, and a node of a tree stands between its root's place and its own.  The window is for cached keys.
+__device__ __forceinline__ int tree_keys_from(const AttnArgs& a, int t, int ctx, int place) {
+    return a.window > 0 ? min(keys_from(a, min(max(a.positions[t], ctx), place)), max(ctx, 0)) : 0;
 }
-// Whether row t sees the request's drafted token j >= 0.
-__device__ __forceinline__ bool tree_sees(const AttnArgs& a, int t, int j) {
-    return j >> 6 < a.tree_words && (a.ancestors[int64_t(t) * a.tree_words + (j >> 6)] >> (j & 63) & 1);
+// Which of the 32 keys from `key` on row t's bits show: cached keys (before ctx) all.
+__device__ __forceinline__ uint32_t tree_bits(const AttnArgs& a, int t, int ctx, int key) {
+    const int off = key - ctx, at = off >> 5;
+    if (at < -1) return 0xffffffffu;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(a.ancestors) + int64_t(t) * 2 * a.tree_words;
+    const uint32_t low = at < 0 ? 0xffffffffu : at < 2 * a.tree_words ? __ldg(words + at) : 0u;
+    const uint32_t high = at + 1 < 2 * a.tree_words ? __ldg(words + at + 1) : 0u;
+    return __funnelshift_r(low, high, off & 31);
 }
 
 }  // namespace nq

@@ -132,7 +132,7 @@ struct Walk {
     }
 };
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TREE>
 __global__ void __launch_bounds__(kThreadsSmall, 1)
     attention_small_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap k_map,
                            const __grid_constant__ CUtensorMap v_map, const AttnWorkspace ws) {
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             const int take = w.take();
             const int p0 = w.q.kv - w.q.n + a.by_group.of(w.row_tile * kSmallRows);
             const int p1 = w.q.kv - w.q.n + a.by_group.of(min((w.row_tile + 1) * kSmallRows, w.q.n * a.group) - 1);
-            const int lo = keys_from(a, p0), hi = keys_to(a, w.q.kv, p1);
+            const int lo = keys_from(a, TREE ? w.q.kv - w.q.n : p0), hi = keys_to(a, w.q.kv, p1);
             const int32_t* table = a.table + w.r * a.table_stride;
             auto page_of = [&](int i) {  // this lane's page of tile i of the piece, -1: none
                 const int k0 = (w.s.first + w.tile + i) * kKeyTile + (pg << a.page_shift);
@@ -268,13 +268,14 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
         const int row0 = w.row_tile * kSmallRows, n_rows = min(w.q.n * a.group - row0, kSmallRows);
         const int pbase = w.q.kv - w.q.n;
         // rows of the tile: positions and the fragments of q
-        int pos2[2];
+        int pos2[2], t2[2];
         uint32_t qf[KS][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = rq + 8 * e;
             const int gi = row0 + min(row, n_rows - 1), t = a.by_group.of(gi), h = w.head * a.group + gi - t * a.group;
             pos2[e] = pbase + t;
+            t2[e] = w.q.begin + t;
             const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
                                                                     (w.q.begin + t) * a.q_token_stride +
                                                                     h * a.q_head_stride);
@@ -285,9 +286,9 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
             }
         }
         const int p_min = pbase + a.by_group.of(row0), p_max = pbase + a.by_group.of(row0 + n_rows - 1);
-        const int lo = keys_from(a, p_min), hi = keys_to(a, w.q.kv, p_max);
+        const int lo = keys_from(a, TREE ? pbase : p_min), hi = keys_to(a, w.q.kv, p_max);
         // keys [all_lo, all_hi) are seen by every row
-        const int all_lo = keys_from(a, p_max), all_hi = keys_to(a, w.q.kv, p_min);
+        const int all_lo = keys_from(a, p_max), all_hi = TREE ? pbase : keys_to(a, w.q.kv, p_min);
         float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
@@ -317,7 +318,18 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
                     }
                 }
                 const bool partial = key < all_lo || key + 16 > all_hi;
-                if (partial) {
+                if (TREE && partial) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int from = tree_keys_from(a, t2[e], pbase, pos2[e]), to = keys_to(a, w.q.kv, pos2[e]);
+                        const uint32_t bits = tree_bits(a, t2[e], pbase, key);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int x = 8 * (j >> 1) + 2 * cq + (j & 1);
+                            if (key + x < from || key + x >= to || !(bits >> x & 1u)) s[j >> 1][2 * e + (j & 1)] = -INFINITY;
+                        }
+                    }
+                } else if (partial) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -478,19 +490,19 @@ __global__ void __launch_bounds__(kThreadsSmall, 1)
 
 }  // namespace
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TREE>
 static int launch_small(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const AttnWorkspace& ws) {
-    if (!ensure_smem(reinterpret_cast<const void*>(attention_small_kernel<D, BF16>), Small<D>::SMEM)) return NQ_ERR_CUDA;
-    attention_small_kernel<D, BF16><<<kAttnGrid, kThreadsSmall, Small<D>::SMEM, a.stream>>>(a, km, vm, ws);
+    if (!ensure_smem(reinterpret_cast<const void*>(attention_small_kernel<D, BF16, TREE>), Small<D>::SMEM)) return NQ_ERR_CUDA;
+    attention_small_kernel<D, BF16, TREE><<<kAttnGrid, kThreadsSmall, Small<D>::SMEM, a.stream>>>(a, km, vm, ws);
     return cudaGetLastError() == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
 }
 
-template <bool BF16>
+template <bool BF16, bool TREE>
 static int launch_small(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, const AttnWorkspace& ws) {
     switch (a.head_dim) {
-        case 64: return launch_small<64, BF16>(a, km, vm, ws);
-        case 96: return launch_small<96, BF16>(a, km, vm, ws);
-        default: return launch_small<128, BF16>(a, km, vm, ws);
+        case 64: return launch_small<64, BF16, TREE>(a, km, vm, ws);
+        case 96: return launch_small<96, BF16, TREE>(a, km, vm, ws);
+        default: return launch_small<128, BF16, TREE>(a, km, vm, ws);
     }
 }
 
@@ -498,7 +510,8 @@ int launch_attention_small(const AttnArgs& a) {
     CUtensorMap km, vm;
     if (!make_pool_maps(a, &km, &vm)) return NQ_ERR_CUDA;
     const AttnWorkspace ws = attn_workspace(a.workspace, kSmallRows, a.head_dim);
-    const int st = a.bf16 ? launch_small<true>(a, km, vm, ws) : launch_small<false>(a, km, vm, ws);
+    const int st = a.ancestors ? a.bf16 ? launch_small<true, true>(a, km, vm, ws) : launch_small<false, true>(a, km, vm, ws)
+                               : a.bf16 ? launch_small<true, false>(a, km, vm, ws) : launch_small<false, false>(a, km, vm, ws);
     return st == NQ_OK ? launch_join_few_rows(a, ws) : st;
 }
 

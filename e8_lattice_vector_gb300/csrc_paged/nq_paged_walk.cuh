@@ -82,7 +82,7 @@ __host__ __device__ __forceinline__ RowTile row_tile_of(const AttnArgs& a, const
     t.n = min(q.n - t.token0, 2 * a.half_tokens);
     t.shared = t.n <= a.half_tokens;
     const int p0 = q.kv - q.n + t.token0;
-    t.lo = keys_from(a, p0);
+    t.lo = keys_from(a, a.ancestors ? q.kv - q.n : p0);  // any node of a tree may stand next to its root
     t.hi = keys_to(a, q.kv, p0 + t.n - 1);
     t.first = min(t.lo, t.hi) / kKeyTile;
     t.count = max((t.hi + kKeyTile - 1) / kKeyTile - t.first, 1);
