@@ -46,6 +46,7 @@ struct Chunk {
     static constexpr int STAGES = (224 * 1024 - Q) / TILE;  // 5, or 12 of half the size
     static constexpr int SMEM = 1024 + Q + STAGES * TILE;
 };
+constexpr int kMostPages = kKeyTile / 16;  // of a key tile
 constexpr int kLiveRing = 8;  // tiles whose page masks are kept; the loads are at most six tiles ahead of a half
 
 // Block-wide inclusive sum; *total the sum over all threads.
@@ -405,6 +406,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
             // -------------------------------------------------------- loads
+            constexpr bool ONE_ISSUES = TREE && HALVES > 1;
             const int ppt = max(kKeyTile >> a.page_shift, 1), rows = min(1 << a.page_shift, kKeyTile);
             const int pg = lane % ppt, half = lane / ppt;  // a lane for each page and 64 columns
             Ring<STAGES> at;
@@ -420,9 +422,17 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 int page = page_of(0);
                 for (int i = 0; go && i < w.take; ++i) {
                     const int next = page_of(i + 1);  // on its way while this tile waits for room
-                    const int slot0 = (w.key0 + i * kKeyTile + (pg << a.page_shift)) & ((1 << a.page_shift) - 1);
+                    const int slot0 = (w.key0 + i * kKeyTile) & ((1 << a.page_shift) - 1);  // in each of the tile's pages
                     const bool load = page >= 0 && page < a.pages;
                     const uint32_t mask = __ballot_sync(0xffffffffu, load && half == 0);
+                    // Trees mostly have up to 128 rows, and then a tile's time is its loads'.  Lanes that issue a box each take turns, at 110
+                    // cycles a box; from one thread, the pages in its registers, 64 rows over 8000 cached in pages of 16 take (32
+                    // requests) 188 us in place of 215 at head_dim 128 in bf16 and 152 in place of 192 at 96, in pages of 32 and more the
+                    // same within 2%.  With one box a page (head_dim 64) larger pages would be 9% slower.
+                    int pages[ONE_ISSUES ? kMostPages : 1];
+                    if constexpr (ONE_ISSUES)
+#pragma unroll
+                        for (int x = 0; x < kMostPages; ++x) pages[x] = __shfl_sync(0xffffffffu, page, x);
 #pragma unroll 1
                     for (int is_v = 0; is_v < 2; ++is_v, ++n, at.step()) {
                         if (n >= STAGES)
@@ -434,9 +444,23 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                             mbar_arrive_tx(full, uint32_t(__popc(mask)) * uint32_t(rows) * 128u * HALVES);
                         }
                         __syncwarp();
-                        if (load)
-                            tma_load_box(smem_ptr(ring + at.stage * C::TILE + half * kHalfBytes + pg * rows * 128),
-                                         is_v ? &v_map : &k_map, full, half * 64, slot0, w.head, page);
+                        const uint32_t dst = smem_ptr(ring + at.stage * C::TILE);
+                        if constexpr (!ONE_ISSUES) {
+                            if (load)
+                                tma_load_box(dst + half * kHalfBytes + pg * rows * 128, is_v ? &v_map : &k_map, full, half * 64, slot0,
+                                             w.head, page);
+                        } else {
+                            if (elect_one()) {
+#pragma unroll
+                                for (int x = 0; x < kMostPages; ++x)
+                                    if (mask >> x & 1u)
+#pragma unroll
+                                        for (int y = 0; y < HALVES; ++y)
+                                            tma_load_box(dst + y * kHalfBytes + x * rows * 128, is_v ? &v_map : &k_map, full, y * 64,
+                                                         slot0, w.head, pages[x]);
+                            }
+                            __syncwarp();
+                        }
                     }
                     page = next;
                     if (go) tile.step();
