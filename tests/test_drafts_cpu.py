@@ -165,3 +165,32 @@ def test_binding_refusals(nq):
     raises("kv_lens must be", rel, n=vec(3, I64), k=vec(3))
     raises("block_table is on", rel, t=_Fake((3, 7), I32, device="cuda:1"))
     raises("out has", rel, out=vec(3))
+
+
+def test_a_paged_cache_keeps_accepted_rows_and_counts_pages(monkeypatch):
+    """keep() and end() hand the right lengths on, and the free list's top follows them."""
+    from e8_lattice_vector_gb300 import serve
+    from e8_lattice_vector_gb300.drafts import DraftTree, Verdict
+    from e8_lattice_vector_gb300.paged import PageMap
+
+    calls = []
+    monkeypatch.setattr(serve, "page_map", lambda ctx, new, free, *a: PageMap(*(torch.zeros(0),) * 5) if calls.append(
+        ("map", ctx.tolist(), new.tolist(), free.numel())) else PageMap(torch.zeros(4), ctx + new, *(torch.zeros(0),) * 3))
+    monkeypatch.setattr(serve, "draft_tree", lambda parents, q, kv, most: calls.append(("tree", parents.tolist(), most)) or DraftTree(
+        torch.zeros(0), torch.zeros(0)))
+    monkeypatch.setattr(serve, "paged_compact", lambda K, V, table, q, kv, path: calls.append(("compact", path.tolist())))
+    monkeypatch.setattr(serve, "page_release", lambda table, lens, keep, size, free, top: calls.append(
+        ("release", lens.tolist(), keep.tolist(), size, free.numel(), top)))
+    c = serve.PagedCache(1, 3, 1, 64, 16, 60, torch.float16, torch.device("cpu"))  # four pages each
+    c.extend([30, 16, 0])
+    step = c.draft([[-1, 0, 0, 1], [], [-1] + list(range(39))])
+    assert c.lengths == [34, 16, 40] and c.top == 3 + 1 + 3 and c.free.numel() == 5
+    assert calls[-2:] == [("map", [30, 16, 0], [4, 0, 40], 9), ("tree", [-1, 0, 0, 1, -1] + list(range(39)), 40)]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)
+    path = [0, 2, -1, -1] + list(range(17)) + [-1] * 23
+    assert c.keep(step, Verdict(i32([2, 0, 17]), i32(path), None)) == [2, 0, 17]
+    assert calls[-2:] == [("compact", path), ("release", [34, 16, 40], [32, 16, 17], 16, 12, 7)]
+    assert c.lengths == [32, 16, 17] and c.top == 2 + 1 + 2
+    c.end([1, 2])
+    assert calls[-1] == ("release", [32, 16, 17], [32, 0, 0], 16, 12, 5)
+    assert c.lengths == [32, 0, 0] and c.top == 2 and c.free.numel() == 10

@@ -670,3 +670,191 @@ def test_release_and_map_share_the_free_list(nq):
         lens = keep
         held = [p for r in range(R) for p in table[r, :-(-lens[r] // P)].tolist()]
         assert sorted(held + free[top:].tolist()) == list(range(pages))
+
+
+# ------------------------------------------------------------------ together
+
+
+@pytest.mark.parametrize("config,kw", [("tiny", {"steps": 4, "tree": 8}), ("tiny", {"steps": 3, "tree": 70, "page_size": 32}),
+                                       ("phi3mini", {"layers": 2, "tokens": 300, "q_heads": 32, "steps": 3, "tree": 5, "vocab": 1000})])
+def test_serving_trees_from_a_compressed_cache(nq, config, kw):
+    from e8_lattice_vector_gb300.serve import serve
+    from e8_lattice_vector_gb300.synth import CONFIGS
+
+    r = serve(CONFIGS[config], **kw)
+    assert 0.01 < r["attention_rel_error"] < 1.0 and 1.0 <= r["accepted_per_step"] <= kw["tree"]
+    nq.paged_status()
+
+
+class ToyModel:
+    """Two layers of attention and an output over 40 tokens; its states are kept in fp16 pages."""
+
+    def __init__(self, layers=2, heads=4, kv_heads=2, D=64, V=40, seed=0):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        def rand(*shape):
+            return torch.randn(shape, generator=g, device=DEV)
+
+        self.L, self.H, self.G, self.D, self.V = layers, heads, kv_heads, D, V
+        W = 96
+        self.E, self.P = rand(V, W), rand(500, W) * 0.5
+        self.qkv = [rand(W, (heads + 2 * kv_heads) * D) * W ** -0.5 for _ in range(layers)]
+        self.o = [rand(heads * D, W) * (heads * D) ** -0.5 for _ in range(layers)]
+
+    def __call__(self, nq, cache, m, tokens, positions, max_q, tree=None):
+        x = self.E[tokens.long()] + self.P[positions.long()]
+        for l in range(self.L):
+            y = (x @ self.qkv[l]).view(-1, self.H + 2 * self.G, self.D).half()
+            nq.paged_append(y[:, self.H:self.H + self.G], y[:, self.H + self.G:], cache.K[l], cache.V[l], m.slots)
+            a = nq.paged_attention(y[:, :self.H], cache.K[l], cache.V[l], cache.table, m.q_start, m.kv_lens, max_q=max_q, tree=tree)
+            x = x + a.float().flatten(1) @ self.o[l]
+        return x @ self.E.T
+
+
+def test_speculating_with_trees_gives_the_sequential_tokens(nq):
+    """Greedy decoding (the model's probabilities are one at its best token), token by token and with drafted trees that hold the right
+    continuation here and there: the same tokens, and in the end every page is accounted for."""
+    from e8_lattice_vector_gb300.serve import PagedCache, random_tree
+
+    R, steps, P = 5, 40, 16
+    model, rng = ToyModel(), random.Random(1)
+    dev = torch.device(DEV, 0)
+
+    def new_cache():
+        torch.manual_seed(3)
+        return PagedCache(2, R, 2, 64, P, 130, torch.float16, dev)
+
+    first = [rng.randrange(40) for _ in range(R)]
+    prompts = [[rng.randrange(40) for _ in range(n)] for n in (1, 15, 16, 17, 33)]
+    # one token after another
+    cache = new_cache()
+    m = cache.extend([len(p) for p in prompts])
+    model(nq, cache, m, _i32(sum(prompts, [])), m.positions, 33)
+    now, truth, margin = list(first), [[] for _ in range(R)], []
+    for _ in range(steps):
+        m = cache.extend([1] * R)
+        logits = model(nq, cache, m, _i32(now), m.positions, 1)
+        top = logits.topk(2).values
+        margin.append(float((top[:, 0] - top[:, 1]).min()))
+        now = logits.argmax(1).tolist()
+        for r in range(R):
+            truth[r].append(now[r])
+    assert min(margin) > 1e-3  # no choice hangs on a rounding
+    # trees: some children are the right token, others are not
+    cache = new_cache()
+    m = cache.extend([len(p) for p in prompts])
+    model(nq, cache, m, _i32(sum(prompts, [])), m.positions, 33)
+    now, said = list(first), [[] for _ in range(R)]
+    while min(len(s) for s in said) < steps:
+        trees, ids = [], []
+        for r in range(R):
+            if len(said[r]) >= steps:
+                trees.append([])
+                continue
+            t = random_tree(rng.randrange(1, 14), rng)
+            depth, right = [], []  # right: the path down to the node is the true continuation
+            for i, p in enumerate(t):
+                depth.append(0 if i == 0 else depth[p] + 1)
+                at = len(said[r]) + depth[i] - 1
+                true = truth[r][at] if i > 0 and at < steps else -1
+                tok = now[r] if i == 0 else true if true >= 0 and rng.random() < 0.6 else rng.randrange(40)
+                right.append(i == 0 or (right[p] and tok == true))
+                ids.append(tok)
+            trees.append(t)
+        step = cache.draft(trees)
+        logits = model(nq, cache, step.map, _i32(ids), step.tree.positions, max(step.nodes), step.tree)
+        probs = torch.nn.functional.one_hot(logits.argmax(1), 40).float()
+        u = torch.rand(len(ids), device=DEV)
+        before = list(cache.lengths)
+        v = nq.verify_drafts(probs, _i32(ids), step.parents, step.map.q_start, u)
+        kept = cache.keep(step, v)
+        tokens, at = v.tokens.tolist(), 0
+        for r, t in enumerate(trees):
+            got = tokens[at:at + kept[r]]
+            said[r] += got
+            assert tokens[at + kept[r]:at + len(t)] == [-1] * (len(t) - kept[r])
+            assert cache.lengths[r] == before[r] - len(t) + kept[r]
+            if t:
+                now[r] = got[-1]
+            at += len(t)
+        held = [p for r in range(R) for p in cache.table[r, :-(-cache.lengths[r] // P)].tolist()]
+        assert sorted(held + cache.free.tolist()) == list(range(R * cache.columns))
+    for r in range(R):
+        assert said[r][:steps] == truth[r]
+    cache.end([0, 3])
+    assert cache.lengths[0] == cache.lengths[3] == 0 and cache.lengths[1] > 0
+    held = [p for r in range(R) for p in cache.table[r, :-(-cache.lengths[r] // P)].tolist()]
+    assert sorted(held + cache.free.tolist()) == list(range(R * cache.columns))
+
+
+def test_a_whole_step_in_one_graph(nq):
+    """Map, tree, append, attention, verification, compaction and release captured once, replayed over other lengths and trees."""
+    R, n, P, H, D, V, L = 4, 12, 16, 2, 64, 500, 2
+    T, cols, pages = R * n, 12, 60
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device=DEV)
+
+    pools = [rand(L, pages, H, P, D).half() for _ in range(2)]
+    saved = [p.clone() for p in pools]
+    q, k, v = rand(L, T, 4, D).half(), rand(L, T, H, D).half(), rand(L, T, H, D).half()
+    probs, draft = torch.softmax(rand(T, V) * 2, 1), torch.softmax(rand(T, V) * 2, 1)
+    draft = (draft + probs) / 2
+    u = torch.rand(T, generator=g, device=DEV)
+    ids = torch.multinomial(draft, 1, generator=g).squeeze(1).to(torch.int32)
+    order = torch.randperm(pages, generator=g, device=DEV).to(torch.int32)
+    ctx, new, parents = _i32([0] * R), _i32([n] * R), _i32(make_tree("wide", n) * R)
+    table = torch.full((R, cols), -1, dtype=torch.int32, device=DEV)
+    free, top = order.clone(), 24  # entries before it are in the table
+
+    def step():
+        m = nq.page_map(ctx, new, free[top:], table, P, T)
+        t = nq.draft_tree(parents, m.q_start, m.kv_lens, n)
+        out = [None] * L
+        for l in range(L):
+            nq.paged_append(k[l], v[l], pools[0][l], pools[1][l], m.slots)
+            out[l] = nq.paged_attention(q[l], pools[0][l], pools[1][l], table, m.q_start, m.kv_lens, max_q=n, tree=t)
+        w = nq.verify_drafts(probs, ids, parents, m.q_start, u, draft_probs=draft)
+        nq.paged_compact(pools[0], pools[1], table, m.q_start, m.kv_lens, w.path)
+        counts = nq.page_release(table, m.kv_lens, ctx + w.accepted, P, free, top)
+        return [*out, t.positions, w.accepted, w.path, w.tokens, counts]
+
+    def setup(lens, sizes, shape):
+        ctx.copy_(_i32(lens))
+        new.copy_(_i32(sizes))
+        parents.copy_(_i32([p for r, s in enumerate(sizes) for p in make_tree(shape, s, r)] + [-1] * (T - sum(sizes))))
+        free.copy_(order)
+        table.fill_(-1)
+        at = 0
+        for r, c in enumerate(lens):
+            held = -(-c // P)
+            table[r, :held] = order[at:at + held]
+            at += held
+        for p, s in zip(pools, saved):
+            p.copy_(s)
+
+    cases = [([10, 0, 33, 80], [12, 12, 12, 12], "wide"), ([90, 16, 15, 1], [1, 12, 7, 0], "random"), ([5, 6, 7, 8], [12, 3, 12, 12], "chain")]
+    setup(*cases[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = step()
+    torch.cuda.synchronize()
+    for case in cases:
+        setup(*case)
+        graph.replay()
+        torch.cuda.synchronize()
+        rows, state = sum(case[1]), [pools[0].clone(), pools[1].clone(), free.clone(), table.clone()]
+        one = [x.clone() for x in got]
+        setup(*case)
+        want = step()
+        for a, b in zip(one, want):
+            n_rows = rows if a.shape[0] == T else a.shape[0]
+            assert torch.equal(a[:n_rows], b[:n_rows])
+        for a, b in zip(state, (pools[0], pools[1], free, table)):
+            assert torch.equal(a, b)
+    nq.paged_status()
