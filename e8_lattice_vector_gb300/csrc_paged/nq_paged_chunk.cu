@@ -322,7 +322,8 @@ struct ChunkControl {
     // two phases from the barrier's own, whatever order the loads end in.
     uint64_t empty[12];
     uint64_t k_full[kLiveRing], v_full[kLiveRing], clean[kLiveRing];  // clean: V has no values that no row sees
-    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], drained;
+    uint64_t q_full[2], q_free[2], drained;
+    uint64_t s_full[4], p_full[4], o_full[4];  // of the halves; with three buffers of scores two for each half, by turns
     uint64_t piece_full[kPieceRing], piece_free[kPieceRing];
     uint64_t merge_full, merge_free;
     Piece piece[kPieceRing];
@@ -331,6 +332,23 @@ struct ChunkControl {
     int gave_up;
     float m[128], l[128];  // a shared row tile's second half, for the first
 };
+// Buffers of scores in tensor memory.  Two, one for each half, beside a half's results at head_dim 128; at 64 there is room for a third,
+// and with three that go round between the halves a half's next scores are there while its exponentials are taken.  64 nodes of 4 heads
+// (256 rows) over 8000 cached, 32 requests: 225 -> 202 us in bf16, 169 -> 159 in fp16; a tile's exponentials (2260 of 3260 cycles, 1700 of
+// 2430 in fp16) are what it waits for then.
+template <int D, bool TREE>
+constexpr int kScoreBuffers = TREE && D == 64 ? 3 : 2;
+// The barrier of a half's n-th tile among s_full, p_full and o_full, and the parity of its phase.  With three buffers a half's next
+// scores may be there before all its warps have seen the last ones, so it has two barriers that take turns.
+template <int BUFFERS>
+__device__ __forceinline__ int turn_of(int h, int n) {
+    return BUFFERS == 3 ? 2 * h + (n & 1) : h;
+}
+template <int BUFFERS>
+__device__ __forceinline__ uint32_t turn_parity(int n) {
+    return (BUFFERS == 3 ? n >> 1 : n) & 1;
+}
+
 constexpr int kPieceReaders = 11;  // eight softmax warps, loads, products, clearing
 
 template <int D, bool BF16, bool TREE>
@@ -339,7 +357,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                            const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap q_map,
                            const AttnWorkspace ws, const ChunkPlan plan) {
     using C = Chunk<D>;
-    constexpr int HALVES = C::HALVES, STAGES = C::STAGES;
+    constexpr int HALVES = C::HALVES, STAGES = C::STAGES, BUFFERS = kScoreBuffers<D, TREE>;
+    constexpr int O_AT = BUFFERS * 128, O_NEXT = (512 - O_AT) / 2;  // columns of the first half's results, from them to the second's
     extern __shared__ char smem_raw[];
     __shared__ ChunkControl c;
     char* q_smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -358,6 +377,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_ptr(&c.q_full[i]), 1);
             mbar_init(smem_ptr(&c.q_free[i]), 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(smem_ptr(&c.s_full[i]), 1);
             mbar_init(smem_ptr(&c.p_full[i]), 4);
             mbar_init(smem_ptr(&c.o_full[i]), 1);
@@ -496,62 +517,129 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     go = go && mbar_wait(smem_ptr(&bar), parity, &c.gave_up);
                     tc_fence_after();
                 };
-                while (go && next_piece(piece_at, w, true)) {
-                    const int ahead = w.shared ? 2 : 1;  // key tiles between a half's products
+                if constexpr (BUFFERS == 2) {
+                    while (go && next_piece(piece_at, w, true)) {
+                        const int ahead = w.shared ? 2 : 1;  // key tiles between a half's products
 #pragma unroll 1
-                    for (int i = -ahead; go && i < w.take; ++i) {  // the product with V of tile i, the scores of tile i + ahead
-                        const bool more = i + ahead < w.take;
-                        if (i >= 0) await(c.clean[tile.stage], tile.phase);
+                        for (int i = -ahead; go && i < w.take; ++i) {  // the product with V of tile i, the scores of tile i + ahead
+                            const bool more = i + ahead < w.take;
+                            if (i >= 0) await(c.clean[tile.stage], tile.phase);
 #pragma unroll 1
-                        for (int h = w.shared ? i & 1 : 0; go && h < (w.shared ? (i & 1) + 1 : 2); ++h) {
-                            const int count = h ? w.count[1] : w.count[0];
-                            // of the half's tiles
-                            const int of_v = w.shared ? i >> 1 : i, of_k = w.shared ? (i + 2) >> 1 : i + 1;
-                            const uint32_t p = tmem + h * 128;
-                            if (i >= 0 && of_v < count) {  // O_h += P_h V
-                                await(c.p_full[h], h ? p_phase[1] : p_phase[0]);
-                                (h ? p_phase[1] : p_phase[0]) ^= 1;
-                                if (!go) break;
-                                uint32_t vd = v_desc + v.stage * (C::TILE >> 4);
-                                asm volatile("" : "+r"(vd));  // the steps are added here, not kept in registers
-#pragma unroll
-                                for (int x = 0; x < kKeyTile / 16; ++x) {
-                                    tc_mma_ta(p + 256, p + 8 * x, vd + 128 * x, o_idesc, of_v > 0 || x > 0);
-                                    if constexpr (BF16) tc_mma_ta(p + 256, p + 64 + 8 * x, vd + 128 * x, o_idesc, true);
-                                }
-                                tc_commit(smem_ptr(&c.o_full[h]));
-                            }
-                            const bool last = w.shared || h == 1;  // of the halves that read this V and K
-                            if (i >= 0 && last) tc_commit(smem_ptr(&c.empty[v.stage]));
-                            if (more && (w.shared || h == 0)) await(c.k_full[k_tile.stage], k_tile.phase);
-                            if (!go) break;
-                            if (more && of_k < count) {  // S_h = Q_h K^T; the last of a piece frees Q
-                                if (of_k == 0) {
-                                    await(c.q_full[h], h ? q_phase[1] : q_phase[0]);
-                                    (h ? q_phase[1] : q_phase[0]) ^= 1;
+                            for (int h = w.shared ? i & 1 : 0; go && h < (w.shared ? (i & 1) + 1 : 2); ++h) {
+                                const int count = h ? w.count[1] : w.count[0];
+                                // of the half's tiles
+                                const int of_v = w.shared ? i >> 1 : i, of_k = w.shared ? (i + 2) >> 1 : i + 1;
+                                const uint32_t p = tmem + h * 128;
+                                if (i >= 0 && of_v < count) {  // O_h += P_h V
+                                    await(c.p_full[h], h ? p_phase[1] : p_phase[0]);
+                                    (h ? p_phase[1] : p_phase[0]) ^= 1;
                                     if (!go) break;
-                                }
-                                uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + k.stage * (C::TILE >> 4);
-                                asm volatile("" : "+r"(qd), "+r"(kd));
+                                    uint32_t vd = v_desc + v.stage * (C::TILE >> 4);
+                                    asm volatile("" : "+r"(vd));  // the steps are added here, not kept in registers
 #pragma unroll
-                                for (int x = 0; x < D / 16; ++x) {
-                                    const uint32_t step = (x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2;
-                                    tc_mma(p, qd + step, kd + step, s_idesc, x > 0);
+                                    for (int x = 0; x < kKeyTile / 16; ++x) {
+                                        tc_mma_ta(p + 256, p + 8 * x, vd + 128 * x, o_idesc, of_v > 0 || x > 0);
+                                        if constexpr (BF16) tc_mma_ta(p + 256, p + 64 + 8 * x, vd + 128 * x, o_idesc, true);
+                                    }
+                                    tc_commit(smem_ptr(&c.o_full[h]));
                                 }
-                                tc_commit(smem_ptr(&c.s_full[h]));
-                                if (of_k + 1 == count) tc_commit(smem_ptr(&c.q_free[h]));
+                                const bool last = w.shared || h == 1;  // of the halves that read this V and K
+                                if (i >= 0 && last) tc_commit(smem_ptr(&c.empty[v.stage]));
+                                if (more && (w.shared || h == 0)) await(c.k_full[k_tile.stage], k_tile.phase);
+                                if (!go) break;
+                                if (more && of_k < count) {  // S_h = Q_h K^T; the last of a piece frees Q
+                                    if (of_k == 0) {
+                                        await(c.q_full[h], h ? q_phase[1] : q_phase[0]);
+                                        (h ? q_phase[1] : q_phase[0]) ^= 1;
+                                        if (!go) break;
+                                    }
+                                    uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + k.stage * (C::TILE >> 4);
+                                    asm volatile("" : "+r"(qd), "+r"(kd));
+#pragma unroll
+                                    for (int x = 0; x < D / 16; ++x) {
+                                        const uint32_t step = (x >> 2) * (kHalfBytes >> 4) + (x & 3) * 2;
+                                        tc_mma(p, qd + step, kd + step, s_idesc, x > 0);
+                                    }
+                                    tc_commit(smem_ptr(&c.s_full[h]));
+                                    if (of_k + 1 == count) tc_commit(smem_ptr(&c.q_free[h]));
+                                }
+                                if (more && last) tc_commit(smem_ptr(&c.empty[k.stage]));
                             }
-                            if (more && last) tc_commit(smem_ptr(&c.empty[k.stage]));
+                            if (i >= 0) {
+                                v.step();
+                                v.step();
+                                tile.step();
+                            }
+                            if (more) {
+                                k_tile.step();
+                                k.step();
+                                k.step();
+                            }
                         }
-                        if (i >= 0) {
-                            v.step();
-                            v.step();
-                            tile.step();
-                        }
-                        if (more) {
-                            k_tile.step();
-                            k.step();
-                            k.step();
+                    }
+                } else {
+                    // Unit u is tile u >> 1 of half u & 1 (of its own tiles), its scores in buffer u % 3: the product with V of unit u - 3,
+                    // then the scores of unit u over its P.
+                    int s_made[2] = {0, 0}, p_seen[2] = {0, 0};
+                    while (go && next_piece(piece_at, w, true)) {
+                        const int units = w.shared ? w.take : 2 * w.take;
+                        uint32_t buffer = 0;
+#pragma unroll 1
+                        for (int u = 0; go && u < units + BUFFERS; ++u, buffer = buffer == BUFFERS - 1 ? 0 : buffer + 1) {
+                            const uint32_t p = tmem + buffer * 128;
+                            const int x = u - BUFFERS;
+                            if (x >= 0) {
+                                const int h = x & 1;
+                                if (w.shared || h == 0) await(c.clean[tile.stage], tile.phase);
+                                if (x >> 1 < (h ? w.count[1] : w.count[0])) {  // O_h += P V
+                                    const int n = h ? p_seen[1]++ : p_seen[0]++, bar = turn_of<BUFFERS>(h, n);
+                                    await(c.p_full[bar], turn_parity<BUFFERS>(n));
+                                    if (!go) break;
+                                    uint32_t vd = v_desc + v.stage * (C::TILE >> 4);
+                                    asm volatile("" : "+r"(vd));
+#pragma unroll
+                                    for (int y = 0; y < kKeyTile / 16; ++y) {
+                                        tc_mma_ta(tmem + O_AT + h * O_NEXT, p + 8 * y, vd + 128 * y, o_idesc, x > 1 || y > 0);
+                                        if constexpr (BF16)
+                                            tc_mma_ta(tmem + O_AT + h * O_NEXT, p + 64 + 8 * y, vd + 128 * y, o_idesc, true);
+                                    }
+                                    tc_commit(smem_ptr(&c.o_full[bar]));
+                                }
+                                if (w.shared || h == 1) {
+                                    tc_commit(smem_ptr(&c.empty[v.stage]));
+                                    v.step();
+                                    v.step();
+                                    tile.step();
+                                }
+                            }
+                            if (u < units) {
+                                const int h = u & 1, count = h ? w.count[1] : w.count[0];
+                                if (w.shared || h == 0) await(c.k_full[k_tile.stage], k_tile.phase);
+                                if (!go) break;
+                                if (u >> 1 < count) {  // S = Q_h K^T; the last of a piece frees Q
+                                    if (u < 2) {
+                                        await(c.q_full[h], h ? q_phase[1] : q_phase[0]);
+                                        (h ? q_phase[1] : q_phase[0]) ^= 1;
+                                        if (!go) break;
+                                    }
+                                    uint32_t qd = q_desc + h * (C::TILE >> 4), kd = k_desc + k.stage * (C::TILE >> 4);
+                                    asm volatile("" : "+r"(qd), "+r"(kd));
+#pragma unroll
+                                    for (int y = 0; y < D / 16; ++y) {
+                                        const uint32_t step = (y >> 2) * (kHalfBytes >> 4) + (y & 3) * 2;
+                                        tc_mma(p, qd + step, kd + step, s_idesc, y > 0);
+                                    }
+                                    const int n = h ? s_made[1]++ : s_made[0]++;
+                                    tc_commit(smem_ptr(&c.s_full[turn_of<BUFFERS>(h, n)]));
+                                    if ((u >> 1) + 1 == count) tc_commit(smem_ptr(&c.q_free[h]));
+                                }
+                                if (w.shared || h == 1) {
+                                    tc_commit(smem_ptr(&c.empty[k.stage]));
+                                    k_tile.step();
+                                    k.step();
+                                    k.step();
+                                }
+                            }
                         }
                     }
                 }
@@ -654,7 +742,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int h = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-        const uint32_t s_at = tmem + h * 128 + lanes, o_at = tmem + 256 + h * 128 + lanes;
+        const uint32_t o_at = tmem + O_AT + h * O_NEXT + lanes;
+        uint32_t s_at = tmem + h * 128 + lanes;
         const float sc = a.scale * kLog2e;
         constexpr float lift = kLift<BF16, 7>;
         auto wait = [&](uint64_t& bar, uint32_t parity) {
@@ -682,10 +771,16 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
             // huge m sc (far) would leave no digits for the difference, there s - m is taken first and neg is the lift.
             float m = -INFINITY, l = 0.0f, neg = 0.0f, rest = 0.0f;
             bool far = false;
+            int buffer = h;
             for (int j = 0; j < count; ++j, ++n_s) {
+                if constexpr (BUFFERS == 3) {
+                    s_at = tmem + buffer * 128 + lanes;
+                    buffer = buffer == 0 ? 2 : buffer - 1;  // two further of three
+                }
                 const int i = w.shared ? 2 * j + h : j;  // of the piece's tiles
                 const int key0 = w.key0 + i * kKeyTile;
-                wait(c.s_full[h], n_s & 1);
+                const int bar = turn_of<BUFFERS>(h, n_s);
+                wait(c.s_full[bar], turn_parity<BUFFERS>(n_s));
                 const uint32_t live = *(volatile uint32_t*)&c.live[(tiles + i) % kLiveRing];
                 if (key0 < all_lo || key0 + kKeyTile > all_hi || live != all) {
                     // Keys that the row does not see, in place.  This and the other rare parts are loops over 16 columns in tensor
@@ -730,7 +825,8 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     const float rest_new = beyond_reference<BF16>(m_new, sc);
                     if (__any_sync(0xffffffffu, moves && m != -INFINITY)) {
                         const float f = moves && m != -INFINITY ? exp2_fast(__fmaf_rn(m - m_new, sc, rest_new - rest)) : 1.0f;
-                        wait(c.o_full[h], (n_s - 1) & 1);  // the previous product has added to O
+                        // the previous product has added to O
+                        wait(c.o_full[turn_of<BUFFERS>(h, n_s - 1)], turn_parity<BUFFERS>(n_s - 1));
                         l *= f;
 #pragma unroll 1
                         for (int x = 0; x < D; x += 16) {
@@ -788,11 +884,11 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_ptr(&c.p_full[h]));
+                if (lane == 0) mbar_arrive(smem_ptr(&c.p_full[bar]));
             }
 
             // ------------------------------------------------------- results
-            wait(c.o_full[h], (n_s - 1) & 1);
+            wait(c.o_full[turn_of<BUFFERS>(h, n_s - 1)], turn_parity<BUFFERS>(n_s - 1));
             float to_m = exp2_fast(-rest) * (1.0f / kLifted<BF16, 7>);  // from the reference to m
             l *= to_m;
             const bool both = w.shared && w.take > 1, whole = w.slot < 0;
@@ -833,7 +929,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                 for (int x = 0; x < 32; ++x) o[x] *= to_m;
                 if (both) {
                     float o1[32];
-                    tm_load(o1, o_at + 128 + x0);
+                    tm_load(o1, o_at + O_NEXT + x0);
                     tm_wait<32>(o1);
 #pragma unroll
                     for (int x = 0; x < 32; ++x) o[x] = __fmaf_rn(o1[x], to_other, o[x]);
