@@ -99,6 +99,7 @@ extern "C" int nq_paged_compact(const nq_pool* pool, int32_t layers, int64_t lay
     if (int64_t(table_cols) * pool->page_size > INT32_MAX - 65536) return NQ_ERR_ARG;
     if (requests > 1 && table_stride < table_cols) return NQ_ERR_ARG;
     if (tokens == 0 || requests == 0 || layers == 0 || table_cols == 0) return NQ_OK;
+    if (k_pages == v_pages) return NQ_ERR_ARG;  // rows of one would move twice
     if (!k_pages || !v_pages || !block_table || !q_start || !kv_lens || !path) return NQ_ERR_ARG;
     for (const void* p : {static_cast<const void*>(k_pages), static_cast<const void*>(v_pages)})
         if (!nq::paged_aligned(p, 16)) return NQ_ERR_ARG;

@@ -9,7 +9,7 @@
 // cluster's barrier.  For a sum it writes the node and A into every block's shared memory; each block forms its part and writes that
 // into every other's, so that after one more barrier all know the whole, and the block whose part holds the token finds it.
 //
-// Sums decide between whole numbers, so they carry 40 bits and more.  The GPU's 64-bit units are too slow for that (used for no more
+// Sums decide between whole numbers, so they carry 38 bits and more.  The GPU's 64-bit units are too slow for that (used for no more
 // than the threads' totals and the search they took four fifths of the time), so a number that matters is the sum of two fp32: an
 // addition's rounding error is found by Knuth's two-sum, a product's by a fused multiply-add.
 #include <cuda_bf16.h>
@@ -143,7 +143,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
 
-// Two running sums side by side, with their rounding errors.
+// Two running sums side by side, with their rounding errors.  What is lost is the rounding of the errors' own sum: for each vector ten times
+// 2^-48 of the running sum at most, and a thread adds 64 vectors of 2^19 tokens: 2^-38.
 struct Sums {
     float2 s = {0.0f, 0.0f}, e = {0.0f, 0.0f};
     __device__ __forceinline__ void add(float2 x, float2 low) {
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
         if (i >= n || i == 0) return;
         parent = a.parents[begin + i];
         drafted = a.drafts[begin + i];
-        u = a.uniform[begin + i];
+        u = weight_of(a.uniform[begin + i]);
         if (parent < 0 || parent >= i || drafted < 0 || drafted >= V) {
             parent = -1;
             return;
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
         for (int k = c.kept + threadIdx.x; k < n; k += kVerifyThreads) a.path[begin + k] = a.tokens_out[begin + k] = -1;
     }
     if (!positive(total)) return;
-    const Pair target = total * a.uniform[begin];
+    const Pair target = total * weight_of(a.uniform[begin]);
     Pair before{0.0f, 0.0f};
     if (part_of(sh.part[(turn - 1) & 1], int(blocks), target, before) != int(rank)) return;
     // The warp whose part it is in; that part in turn in equal parts for all the block's warps: one warp alone would be all latency.
@@ -688,6 +689,19 @@ extern "C" int nq_verify_drafts(const void* probs, int64_t probs_stride, const v
                           static_cast<const void*>(accepted), static_cast<const void*>(path),
                           static_cast<const void*>(tokens_out)})
         if (!nq::paged_aligned(p, 4)) return NQ_ERR_ARG;
+    // the walk writes while other blocks read
+    const uintptr_t bytes = uintptr_t(tokens) * 4;
+    auto overlap = [](const void* x, uintptr_t nx, const void* y, uintptr_t ny) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+        return a < b + ny && b < a + nx;
+    };
+    for (const void* out : {static_cast<const void*>(path), static_cast<const void*>(tokens_out)}) {
+        for (const void* in : {static_cast<const void*>(drafts), static_cast<const void*>(parents), static_cast<const void*>(uniform)})
+            if (overlap(out, bytes, in, bytes)) return NQ_ERR_ARG;
+        if (overlap(out, bytes, q_start, (uintptr_t(requests) + 1) * 4) || overlap(out, bytes, accepted, uintptr_t(requests) * 4))
+            return NQ_ERR_ARG;
+    }
+    if (overlap(path, bytes, tokens_out, bytes)) return NQ_ERR_ARG;
     const nq::VerifyArgs a{probs,   draft_probs, probs_stride, draft_stride, drafts, parents, q_start,
                            uniform, accepted,    path,         tokens_out,   vocab,  tokens};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

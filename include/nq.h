@@ -406,7 +406,7 @@ int nq_paged_attention(const nq_attention* a, const void* q, const nq_pool* pool
  *              fewer than `window` levels above it.  Bits past the words are left out
  *   positions  device int32[tokens]: c + the number of the node's ancestors
  * 1 <= words <= NQ_TREE_WORDS.  q_start is clamped to [0, tokens].  Rows of no
- * request are left as they are. */
+ * request are left as they are.  Outputs must not overlap inputs. */
 int nq_draft_tree(const int32_t* parents, int32_t tokens, const int32_t* q_start, const int32_t* kv_lens,
                   int32_t requests, int32_t window, int32_t words, int64_t* ancestors, int32_t* positions,
                   void* stream);
@@ -446,10 +446,11 @@ int nq_paged_tree_attention(const nq_attention* a, const int64_t* ancestors, con
  *   path        device int32[tokens]: at the request's rows the accepted nodes in order, then -1
  *   tokens_out  device int32[tokens]: at the request's rows the tokens of the accepted
  *               nodes but the first, then the one that follows, then -1: as many as accepted
- * Probabilities are >= 0; NaN and negative ones count as 0.  Sums over the
- * vocabulary, S and the comparisons carry at least 44 bits.  When all p_cur are 0 the token that
- * follows is -1.  q_start is clamped to [0, tokens]; rows of no request are
- * left as they are.  Outputs must not overlap inputs.
+ * Probabilities must be finite; NaN and negative ones count as 0, and a negative
+ * uniform too.  Sums over the vocabulary, S and the comparisons carry 38 bits at
+ * least for up to 2^19 tokens (fp32 pairs).  When all p_cur are 0 the token that follows is -1.
+ * q_start is clamped to [0, tokens]; rows of no request are left as they
+ * are.  path and tokens_out must overlap neither each other nor the inputs.
  * The result does not depend on the run. */
 int nq_verify_drafts(const void* probs, int64_t probs_stride, const void* draft_probs, int64_t draft_stride,
                      int32_t dtype, int32_t vocab, const int32_t* drafts, const int32_t* parents,
@@ -462,7 +463,8 @@ int nq_verify_drafts(const void* probs, int64_t probs_stride, const void* draft_
  * above path[k - 1] (path[0] >= 0) and below n; the first entry that is not ends the
  * request's moves.  Tokens without a page of the pool are passed over.  Pools:
  * `layers` of them, layer_stride elements apart (a multiple of 8).  q_start and kv_lens are those of
- * the step, clamped as in nq_paged_attention.  Requests must not share pages. */
+ * the step, clamped as in nq_paged_attention.  Requests must not share pages, and
+ * k_pages and v_pages must not overlap. */
 int nq_paged_compact(const nq_pool* pool, int32_t layers, int64_t layer_stride, void* k_pages, void* v_pages,
                      const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* q_start,
                      const int32_t* kv_lens, int32_t requests, const int32_t* path, int32_t tokens, void* stream);

@@ -56,10 +56,15 @@ def test_tree_attention_refusals(nq):
 
 def test_verify_refusals(nq):
     f = nq.lib().nq_verify_drafts
-    good = [P16, 100, P16, 100, 2, 100, P16, P16, P16, 4, P16, 2, P16, P16, P16, None]
+    at = lambda i: 4096 * i
+    good = [at(1), 100, at(2), 100, 2, 100, at(3), at(4), at(5), 4, at(6), 2, at(7), at(8), at(9), None]
     run(f, good, [(i, None, ARG) for i in (0, 6, 7, 8, 10, 12, 13, 14)] + [(i, 99, ARG) for i in (1, 3)] +
         [(4, v, UNSUPPORTED) for v in (-1, 3)] + [(5, v, ARG) for v in (0, -1, 2 ** 31 - 1)] + [(i, -1, ARG) for i in (9, 11)] +
         [(i, P2, ARG) for i in (0, 2, 6, 7, 8, 10, 12, 13, 14)])
+    for i, j, by in ((13, 6, 0), (14, 6, 12), (14, 7, -12), (13, 8, 0), (14, 13, 4), (13, 10, 8), (14, 12, 4)):  # outputs over others
+        args = list(good)
+        args[i] = good[j] + by
+        assert f(*args) == ARG, (i, j)
     odd = list(good)
     odd[4], odd[0] = 0, 3  # fp16 on an odd address
     assert f(*odd) == ARG
@@ -68,10 +73,10 @@ def test_verify_refusals(nq):
 
 def test_compact_refusals(nq):
     f, pool = nq.lib().nq_paged_compact, _pool(nq)
-    good = [ctypes.byref(pool), 3, 10 * 8 * 16 * 128, P16, P16, P16, 5, 5, P16, P16, 2, P16, 4, None]
+    good = [ctypes.byref(pool), 3, 10 * 8 * 16 * 128, P16, 2 * P16, P16, 5, 5, P16, P16, 2, P16, 4, None]
     run(f, good, [(i, None, ARG) for i in (0, 3, 4, 5, 8, 9, 11)] + [(i, -1, ARG) for i in (1, 7, 10, 12)] + [(1, 65536, ARG)] +
         [(2, v, ARG) for v in (1004, 0, -128, 64, 1 << 39)] + [(i, P8, ARG) for i in (3, 4)] + [(i, P2, ARG) for i in (5, 8, 9, 11)] +
-        [(6, 4, ARG), (7, 1 << 27, ARG)])
+        [(6, 4, ARG), (7, 1 << 27, ARG), (4, P16, ARG)])
     for kw, status in BAD_POOLS:
         args = list(good)
         args[0] = ctypes.byref(_pool(nq, **kw))

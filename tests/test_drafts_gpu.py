@@ -508,6 +508,12 @@ def test_verify_borders(nq):
     nan = float("nan")
     one([[nan, -1.0, 0.5, 0.5]] * 3, q[:3], [0, 0, 2], [-1, 0, 0], [0.3, 0.0, 0.9])
     one([[nan, -1.0, 0.5, 0.5]] * 3, [[nan, -3.0, 0.5, 0.5]] * 3, [0, 1, 2], [-1, 0, 0], [0.3, 0.0, 0.9])
+    # a number that is not in [0, 1): below 0 as 0, NaN as 0, from 1 on the last token with anything left
+    want = {-1.0: 0, nan: 0, 1.0: 2, 5.0: 2}
+    for u0, token in want.items():
+        v = nq.verify_drafts(torch.tensor(p[:2], device=DEV), _i32([0, 3]), _i32([-1, 0]), _i32([0, 2]),
+                             torch.tensor([u0, -1.0], device=DEV))
+        assert v.tokens.tolist() == [token, -1] and v.accepted.tolist() == [1]
     # tokens outside the vocabulary are no drafts; parents that are not below their node are nobody's children
     one(p, q, [0, -1, 4, 1], [-1, 0, 0, 0], [0.3, 0.0, 0.0, 0.2])
     one(p, None, [0, 2 ** 31 - 1, -2 ** 31, 0], [-1, 0, 0, 0], [0.3, 0.0, 0.0, 0.2])
@@ -607,20 +613,22 @@ def test_compact_offsets_past_32_bits(nq):
     K = torch.zeros(layers, pages, heads, P, D, dtype=torch.float16, device=DEV)
     row = torch.randn(layers, heads, D, device=DEV).half()
     K[:, pages - 1, :, 5] = row
-    nq.paged_compact(K, K, _i32([[pages - 2, pages - 1]]), _i32([0, 20]), _i32([P + 10]),
+    V = K.clone()
+    nq.paged_compact(K, V, _i32([[pages - 2, pages - 1]]), _i32([0, 20]), _i32([P + 10]),
                      _i32([15] + [-1] * 19))  # c = 246: token 261 becomes token 246, slot 246 of the page before
     assert torch.equal(K[:, pages - 2, :, 246], row)
     assert int(K.count_nonzero()) == 2 * int(row.count_nonzero())
+    assert torch.equal(K, V)
 
 
 def test_compact_device_data_is_clamped(nq):
     K = torch.randn(2, 4, 2, 16, 64, device=DEV).half()
-    before = K.clone()
+    before, V = K.clone(), K.clone()
     path = _i32([1, 2, 3, 4])
     for starts, lens, table in (([-4, 2 ** 31 - 1], [2 ** 31 - 1], [[-1, 4]]), ([4, 0], [9], [[0, 1]]), ([0, 4], [-3], [[0, 1]]),
                                 ([0, 4], [0], [[0, 1]]), ([0, 4], [3], [[2 ** 31 - 1, -2 ** 31]])):
-        nq.paged_compact(K, K, _i32(table), _i32(starts), _i32(lens), path)
-        assert torch.equal(K, before)
+        nq.paged_compact(K, V, _i32(table), _i32(starts), _i32(lens), path)
+        assert torch.equal(K, before) and torch.equal(V, before)
 
 
 def ref_release(table, lens, keep, P, free, top):
@@ -785,6 +793,20 @@ def test_speculating_with_trees_gives_the_sequential_tokens(nq):
     assert cache.lengths[0] == cache.lengths[3] == 0 and cache.lengths[1] > 0
     held = [p for r in range(R) for p in cache.table[r, :-(-cache.lengths[r] // P)].tolist()]
     assert sorted(held + cache.free.tolist()) == list(range(R * cache.columns))
+
+
+def test_a_step_without_drafts(nq):
+    """Every request sits the step out."""
+    from e8_lattice_vector_gb300.serve import PagedCache
+
+    c = PagedCache(1, 2, 2, 64, 16, 40, torch.float16, torch.device(DEV, 0))
+    c.fill(*(torch.randn(1, 2, 2, 20, 64, device=DEV).half() for _ in range(2)))
+    step = c.draft([[], []])
+    out = c.draft_step(*(torch.empty(1, 0, h, 64, dtype=torch.float16, device=DEV) for h in (4, 2, 2)), step)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    v = nq.verify_drafts(torch.empty(0, 50, device=DEV), none, step.parents, step.map.q_start, torch.empty(0, device=DEV))
+    assert out.shape[1] == 0 and v.accepted.tolist() == [0, 0]
+    assert c.keep(step, v) == [0, 0] and c.lengths == [20, 20] and c.top == 4
 
 
 def test_a_whole_step_in_one_graph(nq):
