@@ -371,6 +371,39 @@ def test_tree_in_a_graph_and_on_a_stream(nq):
                 assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("n", [3, 40])
+def test_tree_pools_past_32_bits(nq, n):
+    """Pages at the far end of pools with more than 2^31 elements."""
+    heads, P, D = 8, 256, 128
+    pages = 2 ** 31 // (heads * P * D) + 8
+    s = TreeStep([(700, make_tree("wide", n)), (90, make_tree("random", n))], 16, heads, D, P, torch.float16, seed=n)
+    want = s.check(nq)
+    held = s.Kp.shape[0]
+    big = [torch.empty(pages, heads, P, D, dtype=torch.float16, device=DEV) for _ in range(2)]
+    big[0][-held:], big[1][-held:] = s.Kp, s.Vp
+    s.Kp, s.Vp = big
+    s.table = torch.where((s.table >= 0) & (s.table < held), s.table + (pages - held), torch.full_like(s.table, -1))
+    assert torch.equal(s.check(nq), want)
+
+
+def test_tree_calls_at_once_on_two_streams(nq):
+    """Calls of both kernels on two streams, each with its own scratch and outputs."""
+    steps = [TreeStep([(c, make_tree("wide", n, c)) for c in (3000, 500, 90)], 8, 2, D, 16, torch.bfloat16, seed=n)
+             for n, D in ((4, 128), (40, 128), (40, 64), (90, 64))]
+    want = [s.call(nq) for s in steps]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i, s in enumerate(steps):
+            with torch.cuda.stream(streams[i % 2]):
+                got.append((i, s.call(nq)))
+    torch.cuda.synchronize()
+    for i, o in got:
+        assert torch.equal(o, want[i])
+    nq.paged_status()
+
+
 # -------------------------------------------------------------- verification
 
 
@@ -538,6 +571,47 @@ def test_verify_gives_the_models_distribution(nq, sampled):
     first = v.tokens.view(R, 3)[:, 0]
     count = torch.bincount(first.long(), minlength=V).double()
     assert bool(((count - R * p.double()).abs() <= 5 * (R * p.double() * (1 - p.double())).sqrt()).all()), count.tolist()
+
+
+@pytest.mark.parametrize("sampled", [True, False])
+def test_verify_rows_past_32_bits(nq, sampled):
+    """Requests at the far end of more than 2^31 probabilities."""
+    V, n = 131072, 5
+    T = 2 ** 31 // V + 10
+    probs = torch.zeros(T, V, dtype=torch.bfloat16, device=DEV)
+    draft = torch.zeros_like(probs) if sampled else None
+    probs[-n:] = torch.softmax(torch.randn(n, V, device=DEV) * 4, 1)
+    if sampled:
+        draft[-n:] = torch.softmax(torch.randn(n, V, device=DEV) * 4, 1)
+    tree = make_tree("wide", n)
+    ids = torch.zeros(T, dtype=torch.int32, device=DEV)
+    ids[-n:] = probs[-n:].float().argmax(1).to(torch.int32).roll(1)
+    parents, u = _i32([0] * (T - n) + tree), torch.rand(T, device=DEV)
+    v = nq.verify_drafts(probs, ids, parents, _i32([T - n, T]), u, draft_probs=draft)
+    far = lambda x: x[-n:].double().cpu().numpy()
+    path, said = ref_verify(far(probs), far(draft) if sampled else None, far(ids), tree, far(u))
+    assert v.path[-n:].tolist()[:len(path)] == path and v.tokens[-n:].tolist()[:len(path)] == said
+
+
+def test_verify_calls_at_once_on_two_streams(nq):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    R, n, V = 30, 6, 5000
+    probs = torch.softmax(torch.randn(R * n, V, generator=g, device=DEV) * 3, 1)
+    draft = torch.softmax(torch.randn(R * n, V, generator=g, device=DEV) * 3, 1) / 2 + probs / 2
+    ids = torch.multinomial(draft, 1, generator=g).squeeze(1).to(torch.int32)
+    u = torch.rand(R * n, generator=g, device=DEV)
+    args = (probs, ids, _i32(make_tree("wide", n) * R), _i32(list(range(0, R * n + 1, n))), u)
+    want = [nq.verify_drafts(*args, draft_probs=d) for d in (draft, None)]
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    torch.cuda.synchronize()
+    for i in range(20):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(nq.verify_drafts(*args, draft_probs=(draft, None)[i // 2 % 2]))
+    torch.cuda.synchronize()
+    for i, v in enumerate(got):
+        w = want[i // 2 % 2]
+        assert torch.equal(v.accepted, w.accepted) and torch.equal(v.path, w.path) and torch.equal(v.tokens, w.tokens)
 
 
 def test_verify_wild_row_starts(nq):
