@@ -415,8 +415,9 @@ int nq_draft_tree(const int32_t* parents, int32_t tokens, const int32_t* q_start
  * table shows, key j < c when window = 0 or j > positions - window (positions
  * are clamped to [c, c + i]), and key c + j, j <= i, when the row's bit j is
  * set.  ancestors and positions as nq_draft_tree leaves them; bits past row i's
- * own and past the words are not set.  causal has to be 1.  Keys and values of
- * all drafted rows must be finite; all else, the workspace too, is as there. */
+ * own and past the words count as not set.  causal has to be 1.  Keys and values
+ * of all drafted rows must be finite, and of the cached ones all, or from key
+ * c - window + 1 on (which a root sees); all else, the workspace too, is as there. */
 int nq_paged_tree_attention(const nq_attention* a, const int64_t* ancestors, const int32_t* positions, int32_t words,
                             const void* q, const nq_pool* pool, const void* k_pages, const void* v_pages,
                             const int32_t* block_table, const int32_t* q_start, const int32_t* kv_lens, void* out,
