@@ -653,11 +653,15 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
     if (lane == 0) a.tokens_out[last] = token;
 }
 
-// The least blocks whose threads have four vectors of a row each, at most a portable cluster.
-int cluster_blocks(int vocab, int size) {
+// Blocks of a cluster: so many that a thread has four vectors of a row, at most a portable cluster's eight; fewer, with up to sixteen
+// vectors a thread, while there are more blocks than run at once (four on each of 152 multiprocessors).  8, 4, 2 blocks: 256
+// requests, 32000 tokens in fp32, 38, 28, 25 us (chains of 3 drafts that were drawn), 50, 41, 43 (trees of 8), 37, 26, 21 (chosen);
+// 128 requests 21, 16, 16, then 29, 25, 30, then 19, 15, 15; 128256 tokens in fp32, 128 requests, 38, 38, 37, then 54, 65, 86, then 34, 31, 38.
+int cluster_blocks(int vocab, int size, int requests) {
     const int64_t vectors = int64_t(vocab) * size / 16;
     int blocks = 1;
     while (blocks < kMostBlocks && blocks * kVerifyThreads * 4 < vectors) blocks *= 2;
+    while (blocks > 1 && int64_t(requests) * blocks > 152 * kBlocksPerSm && vectors <= blocks / 2 * kVerifyThreads * 16) blocks /= 2;
     return blocks;
 }
 
@@ -665,7 +669,7 @@ template <typename T>
 int launch_verify(const VerifyArgs& a, int requests, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = unsigned(cluster_blocks(a.vocab, sizeof(T)));
+    attr.val.clusterDim.x = unsigned(cluster_blocks(a.vocab, sizeof(T), requests));
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(requests) * attr.val.clusterDim.x);
