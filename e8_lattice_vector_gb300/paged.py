@@ -275,15 +275,26 @@ def paged_attention(Q, K_pages, V_pages, block_table, q_start, kv_lens, max_q=No
     q, k, v, o = Q.data_ptr(), K_pages.data_ptr(), V_pages.data_ptr(), out.data_ptr()
     if (q | k | v | o) & 15:
         _check_starts(Q=Q, K_pages=K_pages, V_pages=V_pages, out=out)
-    if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
-    elif not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == Q.device):
-        raise ValueError("ws must be a contiguous uint8 CUDA tensor on the call's device")
-    elif ws.numel() < need:
-        raise ValueError("ws has %d bytes; the call needs %d" % (ws.numel(), need))
     what = (a,) if tree is None else (a, tree.ancestors.data_ptr(), tree.positions.data_ptr(), tree.ancestors.shape[1])
-    _launch(index, fn, *what, q, pool, k, v, block_table.data_ptr(), q_start.data_ptr(), kv_lens.data_ptr(), o,
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel())
+    args = (*what, q, pool, k, v, block_table.data_ptr(), q_start.data_ptr(), kv_lens.data_ptr(), o,
+            None if lse is None else lse.data_ptr())
+    if ws is not None:
+        if not (ws.is_cuda and ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == Q.device):
+            raise ValueError("ws must be a contiguous uint8 CUDA tensor on the call's device")
+        if ws.numel() < need:
+            raise ValueError("ws has %d bytes; the call needs %d" % (ws.numel(), need))
+        _launch(index, fn, *args, ws.data_ptr(), ws.numel())
+    elif torch._C._cuda_getDevice() == index:
+        # straight from torch's allocator, in stream order (and into a graph's own memory) like a tensor's: making and dropping the tensor
+        # would take 6 us of a call's 20
+        scratch = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, torch._C._cuda_getCurrentRawStream(index))
+        try:
+            _launch(index, fn, *args, scratch, need)
+        finally:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
+    else:
+        ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        _launch(index, fn, *args, ws.data_ptr(), need)
     return out if lse is None else (out, lse)
 
 
