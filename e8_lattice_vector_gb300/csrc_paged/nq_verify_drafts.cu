@@ -5,9 +5,11 @@
 // is left, w = max(p - A q, 0), where A adds up the S of the node's rejections (max(max(p - a, 0) - b, 0) = max(p - a - b, 0), so
 // no w is ever stored), and in the end the token where the running sum of w passes its part of the whole.
 //
-// A cluster of blocks takes a request, each a part of the vocabulary.  The first block's first warp walks; the others wait at the
-// cluster's barrier.  For a sum it writes the node and A into every block's shared memory; each block forms its part and writes that
-// into every other's, so that after one more barrier all know the whole, and the block whose part holds the token finds it.
+// A cluster of blocks takes a request, each a part of the vocabulary.  The first block loads what the walk needs, 32 nodes at a time, and
+// writes it into every block's shared memory; from there all warps of all blocks walk alike, so that nobody waits to be told what to sum.
+// Each block forms its part of a sum and writes that into every other's shared memory; after a barrier of the cluster all know the
+// whole and walk on, and in the end the block whose part holds the token finds it.  What decides how often the blocks meet comes from
+// that one load, so that inputs that change meanwhile, by mistake, cannot part them.
 //
 // Sums decide between whole numbers, so they carry 38 bits and more.  The GPU's 64-bit units are too slow for that (used for no more
 // than the threads' totals and the search they took four fifths of the time), so a number that matters is the sum of two fp32: an
@@ -165,14 +167,16 @@ struct Sums {
     __device__ __forceinline__ Pair total() const { return normal(s.x, e.x) + normal(s.y, e.y); }
 };
 
-// What a block is to sum: what is left at node `cur` after rejections worth `taken`.
-struct __align__(8) Command {
-    Pair taken;
-    int cur, kept;  // kept < 0: the walk goes on after this sum
+// 32 nodes of a request, from `first` on.
+struct __align__(8) Nodes {
+    int2 drafts[32];    // parent (-1: not to be walked to), token
+    float2 chances[32];  // its random number, p at its parent and token
+    float2 q[32];       // q there; q[0].y and q[1].y hold the request's first row and its rows, as whole numbers
 };
+constexpr int kNodeWords = sizeof(Nodes) / 8;
 
 struct __align__(8) VerifyShared {
-    Command command;
+    Nodes nodes[2];             // by turns
     Pair part[2][kMostBlocks];  // of each block, by turns
     Pair warp[2][kVerifyWarps];  // of each warp's part; of its part of the warp's part that holds the token
     int rejected[kVerifyWarps][kRejectedTokens], rejected_count[kVerifyWarps];
@@ -489,41 +493,80 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
     const int r = blockIdx.x / blocks;
     uint4* ring = rings[warp];
-    const int begin = min(max(a.q_start[r], 0), a.tokens), n = max(min(max(a.q_start[r + 1], 0), a.tokens) - begin, 0);
-    if (n == 0) {  // the same for the whole cluster
-        if (rank == 0 && threadIdx.x == 0) a.accepted[r] = 0;
-        return;
-    }
     cluster_arrive();  // the blocks' shared memory exists
     const int segments = kVerifyWarps * int(blocks), segment = int(rank) * kVerifyWarps + warp;
 
-    // ---------------------------------------- the walk (first warp of the first block)
+    // ------------------------------------------------------------------ nodes
+    int begin = 0, n = 0;
+    int loaded = -1, parent = -1, drafted = -1;  // of node loaded + lane
+    float u = 0.0f, p = 0.0f, q = 1.0f;
+    int loads = 0;
+    // Nodes i0 .. i0 + 31 for every warp of the cluster.  All call it together.
+    auto load = [&](int i0) {
+        loaded = i0;
+        Nodes& nodes = sh.nodes[loads & 1];
+        if (rank == 0) {
+            if (warp == 0) {
+                if (loads == 0) {
+                    begin = min(max(a.q_start[r], 0), a.tokens);
+                    n = max(min(max(a.q_start[r + 1], 0), a.tokens) - begin, 0);
+                }
+                const int i = i0 + lane;
+                parent = drafted = -1;
+                if (i < n && i > 0) {
+                    parent = a.parents[begin + i];
+                    drafted = a.drafts[begin + i];
+                    u = weight_of(a.uniform[begin + i]);
+                    if (parent < 0 || parent >= i || drafted < 0 || drafted >= V) {
+                        parent = -1;
+                    } else {
+                        const int64_t row = begin + parent;
+                        p = weight_of(load_one(static_cast<const T*>(a.probs) + row * a.probs_stride + drafted));
+                        if (SAMPLED) q = weight_of(load_one(static_cast<const T*>(a.draft_probs) + row * a.draft_stride + drafted));
+                    }
+                }
+                nodes.drafts[lane] = make_int2(parent, drafted);
+                nodes.chances[lane] = make_float2(u, p);
+                nodes.q[lane] = make_float2(q, __int_as_float(lane == 0 ? begin : n));
+            }
+            __syncthreads();
+            if (loads == 0) cluster_wait();
+            if (warp > 0 && warp < int(blocks)) {  // a warp for each other block
+                uint64_t* place = reinterpret_cast<uint64_t*>(&nodes);
+#pragma unroll
+                for (int i = 0; i < kNodeWords; i += 32) store_remote(place + i + lane, warp, place[i + lane]);
+            }
+            __syncwarp();
+        } else if (loads == 0) {
+            cluster_wait();
+        }
+        cluster_arrive();
+        cluster_wait();
+        ++loads;
+        parent = nodes.drafts[lane].x;
+        drafted = nodes.drafts[lane].y;
+        u = nodes.chances[lane].x;
+        p = nodes.chances[lane].y;
+        q = nodes.q[lane].x;
+        begin = __float_as_int(nodes.q[0].y);
+        n = __float_as_int(nodes.q[1].y);
+    };
+    load(0);
+    if (n == 0) {
+        if (rank == 0 && threadIdx.x == 0) a.accepted[r] = 0;
+        return;
+    }
+
+    // --------------------------------------------------------------- the walk
+    const bool writes = rank == 0 && warp == 0 && lane == 0;
     int cur = 0, at = 1, kept = 1;
     Pair taken{0.0f, 0.0f}, total{1.0f, 0.0f};
-    bool pending = false;                        // a sum that the next draft needs, or the token that follows
-    int loaded = -1, parent = -1, drafted = -1;  // of node loaded + lane; 32 nodes are held at a time
-    float u = 0.0f, p = 0.0f, q = 1.0f;
-    auto load = [&](int i0) {
-        if (loaded == i0) return;
-        loaded = i0;
-        const int i = i0 + lane;
-        parent = -1;
-        if (i >= n || i == 0) return;
-        parent = a.parents[begin + i];
-        drafted = a.drafts[begin + i];
-        u = weight_of(a.uniform[begin + i]);
-        if (parent < 0 || parent >= i || drafted < 0 || drafted >= V) {
-            parent = -1;
-            return;
-        }
-        p = weight_of(load_one(static_cast<const T*>(a.probs) + int64_t(begin + parent) * a.probs_stride + drafted));
-        if (SAMPLED) q = weight_of(load_one(static_cast<const T*>(a.draft_probs) + int64_t(begin + parent) * a.draft_stride + drafted));
-    };
+    bool pending = false;  // a sum that the next draft needs, or the token that follows
     // Up to a rejection that another draft follows (false), or to the end (true).
     auto walk = [&]() {
         while (at < n) {
             const int i0 = at & ~31;
-            load(i0);
+            if (loaded != i0) load(i0);
             const uint32_t mine = __ballot_sync(0xffffffffu, parent == cur && i0 + lane >= at);
             if (mine == 0) {
                 at = i0 + 32;
@@ -548,7 +591,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
             }
             at = node + 1;
             if (total * qq * uu < w) {
-                if (lane == 0) {
+                if (writes) {
                     a.tokens_out[begin + kept - 1] = token;
                     a.path[begin + kept] = node;
                 }
@@ -581,26 +624,14 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
         cluster_wait();
         return sum_few<kMostBlocks>(sh.part[turn++ & 1], int(blocks), lane);
     };
-    bool end = false;
-    if (rank == 0 && warp == 0) end = walk();
-    __syncwarp();
-    cluster_wait();
-    Command c;
     Rejected rejected{sh.rejected[warp], 0, a.parents + begin, a.drafts + begin, 0, n};
     while (true) {
-        if (rank == 0 && warp == 0 && lane < int(blocks)) {
-            store_remote(&sh.command.taken, lane, bits_of(taken));
-            store_remote(&sh.command.cur, lane, uint64_t(uint32_t(cur)) | uint64_t(uint32_t(end ? kept : -1)) << 32);
-        }
-        __syncwarp();
-        cluster_arrive();
-        cluster_wait();
-        c = sh.command;
+        const bool end = walk();
         if (!SAMPLED) {  // the walk is over: the node's children have all been rejected
-            const Slice<T, SAMPLED> mine(a, begin + c.cur, segment, segments);
-            rejected.node = c.cur;
-            for (int j0 = c.cur + 1; j0 < n; j0 += 32) {
-                const int j = j0 + lane, token = j < n && a.parents[begin + j] == c.cur ? a.drafts[begin + j] : -1;
+            const Slice<T, SAMPLED> mine(a, begin + cur, segment, segments);
+            rejected.node = cur;
+            for (int j0 = cur + 1; j0 < n; j0 += 32) {
+                const int j = j0 + lane, token = j < n && a.parents[begin + j] == cur ? a.drafts[begin + j] : -1;
                 const bool here = token >= mine.begin() && token < mine.end();
                 const uint32_t all = __ballot_sync(0xffffffffu, here);
                 const int slot = rejected.count + __popc(all & ((1u << lane) - 1));
@@ -610,28 +641,26 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
             if (lane == 0) sh.rejected_count[warp] = rejected.count;
             __syncwarp();
         }
-        total = sum(c.cur, c.taken, rejected);
-        if (c.kept >= 0) break;
-        if (rank == 0 && warp == 0) end = walk();
-        __syncwarp();
+        total = sum(cur, taken, rejected);
+        if (end) break;
     }
-    Pair less = c.taken;
+    Pair less = taken;
     if (!positive(total)) {  // nothing is left: the node's own probabilities
         rejected.count = 0;
         rejected.node = -1;
         less = Pair{0.0f, 0.0f};
-        total = sum(c.cur, less, rejected);
+        total = sum(cur, less, rejected);
     }
 
     // ------------------------------------------------- the token that follows
-    const int last = begin + c.kept - 1;
+    const int last = begin + kept - 1;
     if (rank == 0) {
         if (threadIdx.x == 0) {
-            a.accepted[r] = c.kept;
+            a.accepted[r] = kept;
             a.path[begin] = 0;
             if (!positive(total)) a.tokens_out[last] = -1;
         }
-        for (int k = c.kept + threadIdx.x; k < n; k += kVerifyThreads) a.path[begin + k] = a.tokens_out[begin + k] = -1;
+        for (int k = kept + threadIdx.x; k < n; k += kVerifyThreads) a.path[begin + k] = a.tokens_out[begin + k] = -1;
     }
     if (!positive(total)) return;
     const Pair target = total * weight_of(a.uniform[begin]);
@@ -639,7 +668,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kBlocksPerSm) verify_drafts_ke
     if (part_of(sh.part[(turn - 1) & 1], int(blocks), target, before) != int(rank)) return;
     // The warp whose part it is in; that part in turn in equal parts for all the block's warps: one warp alone would be all latency.
     const int holder = part_of(sh.warp[0], kVerifyWarps, target, before);
-    Slice<T, SAMPLED> x(a, begin + c.cur, int(rank) * kVerifyWarps + holder, segments);
+    Slice<T, SAMPLED> x(a, begin + cur, int(rank) * kVerifyWarps + holder, segments);
     x.narrow(warp, kVerifyWarps);
     if (!SAMPLED) {
         rejected.tokens = sh.rejected[holder];
