@@ -447,7 +447,7 @@ int nq_paged_tree_attention(const nq_attention* a, const int64_t* ancestors, con
  *   path        device int32[tokens]: at the request's rows the accepted nodes in order, then -1
  *   tokens_out  device int32[tokens]: at the request's rows the tokens of the accepted
  *               nodes but the first, then the one that follows, then -1: as many as accepted
- * Probabilities must be finite; NaN and negative ones count as 0, and a negative
+ * 1 <= vocab < 2^31 - 65536, requests < 2^28.  Probabilities must be finite; NaN and negative ones count as 0, and a negative
  * uniform too.  Sums over the vocabulary, S and the comparisons carry 38 bits at
  * least for up to 2^19 tokens (fp32 pairs).  When all p_cur are 0 the token that follows is -1.
  * q_start is clamped to [0, tokens]; rows of no request are left as they
@@ -478,7 +478,8 @@ int nq_paged_compact(const nq_pool* pool, int32_t layers, int64_t layer_stride, 
  * lower by counts[0] afterwards.
  *   counts  device int32[2]: columns released; those among them for which
  *           there was no room (k >= top), which go nowhere
- * Entries are copied, not checked; the table is left as it is. */
+ * Entries are copied, not checked; the table is left as it is, so columns that
+ * are released twice are on the list twice. */
 int nq_page_release(const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
                     const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top,
                     int32_t* counts, void* stream);

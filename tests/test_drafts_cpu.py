@@ -59,7 +59,7 @@ def test_verify_refusals(nq):
     at = lambda i: 4096 * i
     good = [at(1), 100, at(2), 100, 2, 100, at(3), at(4), at(5), 4, at(6), 2, at(7), at(8), at(9), None]
     run(f, good, [(i, None, ARG) for i in (0, 6, 7, 8, 10, 12, 13, 14)] + [(i, 99, ARG) for i in (1, 3)] +
-        [(4, v, UNSUPPORTED) for v in (-1, 3)] + [(5, v, ARG) for v in (0, -1, 2 ** 31 - 1)] + [(i, -1, ARG) for i in (9, 11)] +
+        [(4, v, UNSUPPORTED) for v in (-1, 3)] + [(5, v, ARG) for v in (0, -1, 2 ** 31 - 1)] + [(i, -1, ARG) for i in (9, 11)] + [(11, 1 << 28, ARG)] +
         [(i, P2, ARG) for i in (0, 2, 6, 7, 8, 10, 12, 13, 14)])
     for i, j, by in ((13, 6, 0), (14, 6, 12), (14, 7, -12), (13, 8, 0), (14, 13, 4), (13, 10, 8), (14, 12, 4)):  # outputs over others
         args = list(good)
