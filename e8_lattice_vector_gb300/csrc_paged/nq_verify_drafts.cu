@@ -15,10 +15,10 @@
 // than the threads' totals and the search they took four fifths of the time), so a number that matters is the sum of two fp32: an
 // addition's rounding error is found by Knuth's two-sum, a product's by a fused multiply-add.
 //
-// Measured (median of graph replays): one request, a chain of 5 drafts, 32000 tokens in bf16 9.6 us: the launch, 1.7 us of walk (three
-// dependent loads), 0.6 us for each barrier, 1.3 us of sum, 3 us of search, all latency.  64 sampled trees of 16, 128256 tokens in fp32
-// 37 us with 62 MB to read: requests sum 3.6 times on average, and the one with the most rejections decides, 5 us a sum.  64 chains of 5
-// drafts 21 us, 256 of 3 drafts 62 us, 4.2 TB/s of p and q.
+// Measured (median of graph replays): one request, a chain of 5 drafts, 32000 tokens in bf16 9.3 us: the launch, 1.7 us of loads for the
+// walk (three after one another), 0.6 us for each barrier, 1.3 us of sum, 3 us of search, all latency; every further sum 2.6 us, of
+// 128256 tokens in fp32 4.8 us.  64 requests, 128256 tokens in fp32: 18.6 us with one sum (3.5 TB/s of p and q), 12 us for a further one
+// of all (5.5 TB/s, the rows come from the L2 in part); sampled trees of 16 36 us, 3.6 sums on average.  256 chains of 3 drafts 63 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
