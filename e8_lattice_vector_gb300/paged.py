@@ -387,8 +387,9 @@ def page_release(block_table, kv_lens, keep_lens, page_size, free_pages, top, ou
     """Give back the pages past the tokens that requests keep (device int32 [requests] each: tokens with pages, tokens to keep).
 
     free_pages (int32, updated in place) is the whole free list, a stack whose free part begins at `top`: free_pages[top:] is what
-    page_map is given.  The k-th released page, requests and columns in order, goes to free_pages[top - 1 - k].
-    Returns counts [2]: pages released (top is lower by as many), those that found no room.  The table stays as it is."""
+    page_map is given.  The k-th released page, requests and columns in order, goes to free_pages[top - 1 - k]; columns that never
+    got a page (entries below zero) give none back.
+    Returns counts [2]: pages released, those that found no room (top is lower by the difference).  The table stays as it is."""
     n_free = free_pages.numel()
     if not 0 <= top <= n_free or n_free > _I32_MAX:
         raise ValueError("top is %d; free_pages has %d entries" % (top, n_free))

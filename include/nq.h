@@ -472,13 +472,15 @@ int nq_paged_compact(const nq_pool* pool, int32_t layers, int64_t layer_stride, 
 
 /* Give back the pages past the tokens that requests keep.
  * Request r's columns from ceil(keep_lens[r] / page_size) to ceil(kv_lens[r] /
- * page_size) (both device int32[requests], at least 0; columns past table_cols do not count) are
- * released, requests in order, columns in order: the k-th goes to free_pages[top - 1 - k].
+ * page_size) (both device int32[requests], at least 0; columns past table_cols do not count)
+ * give back their pages, requests in order, columns in order: the k-th page goes to
+ * free_pages[top - 1 - k].  A column whose entry is below zero has no page (the free list had run
+ * out when the column began) and gives none back.
  * The free list is a stack: free_pages[top ...] is what nq_page_map is given, and top is
- * lower by counts[0] afterwards.
- *   counts  device int32[2]: columns released; those among them for which
+ * lower by counts[0] - counts[1] afterwards.
+ *   counts  device int32[2]: pages given back; those among them for which
  *           there was no room (k >= top), which go nowhere
- * Entries are copied, not checked; the table is left as it is, so columns that
+ * Other entries are copied, not checked; the table is left as it is, so columns that
  * are released twice are on the list twice. */
 int nq_page_release(const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
                     const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top,

@@ -1,0 +1,91 @@
+"""Calls on drafted trees that test_drafts_gpu leaves out: releases of columns without pages."""
+import random
+
+import pytest
+import torch
+
+from test_paged_gpu import DEV, _i32, nq  # noqa: F401  (nq is the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------- release
+
+
+def ref_release_pages(table, lens, keep, P, free, top):
+    """The header's words: columns without a page give nothing back."""
+    free, k, cols = list(free), 0, len(table[0]) if table else 0
+    for row, n, m in zip(table, lens, keep):
+        for c in range(-(-max(m, 0) // P), min(-(-max(n, 0) // P), cols)):
+            if row[c] < 0:
+                continue
+            if top - 1 - k >= 0:
+                free[top - 1 - k] = row[c]
+            k += 1
+    return free, [k, max(k - top, 0)]
+
+
+@pytest.mark.parametrize("share", [0.02, 0.5, 1.0])
+@pytest.mark.parametrize("R", [1, 13, 511, 1024, 1025, 3000])
+def test_release_of_columns_without_pages(nq, R, share):
+    """Entries below zero are nobody's pages: they are neither counted nor put on the list, and take no page's place there."""
+    rng = random.Random(R)
+    for cols, most in ((1, 16), (9, 200), (300, 16 * 300)):
+        if R * cols > 400000:
+            continue
+        lens = [rng.choice([0, 1, 16, 17, -3, rng.randrange(most), most]) for _ in range(R)]
+        keep = [rng.choice([0, n, n - 1, n - 16, -1]) for n in lens]
+        table = [[rng.choice([-1, -1, -2 ** 31]) if rng.random() < share else rng.randrange(10 ** 6) for _ in range(cols)] for _ in range(R)]
+        total = ref_release_pages(table, lens, keep, 16, [], 0)[1][0]
+        for top in (total, total + 5, max(total - 3, 0), 0):
+            free = [rng.randrange(10 ** 6) for _ in range(top + 4)]
+            want, counts = ref_release_pages(table, lens, keep, 16, free, top)
+            dev, at = _i32(free), torch.tensor(table, dtype=torch.int32, device=DEV).view(R, cols)
+            got = nq.page_release(at, _i32(lens), _i32(keep), 16, dev, top)
+            assert got.tolist() == counts and dev.tolist() == want
+
+
+def test_release_of_more_columns_than_a_round(nq):
+    """Hundreds of thousands of columns, of many requests and of one, some without pages."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(9)
+    for R, cols in ((700, 700), (2, 300000)):
+        table = torch.randint(0, 10 ** 6, (R, cols), generator=g, device=DEV, dtype=torch.int32)
+        table[torch.rand((R, cols), generator=g, device=DEV) < 0.01] = -1
+        lens, keep = _i32([16 * (cols - r % 5) for r in range(R)]), _i32([0 if r % 7 else 16 * 9 for r in range(R)])
+        col = torch.arange(cols, device=DEV)
+        gone = table[(col >= (keep // 16)[:, None]) & (col < (lens // 16)[:, None])]
+        gone = gone[gone >= 0]
+        for spare in (3, -1000):
+            top = gone.numel() + spare
+            free = torch.full((top + 2,), -7, dtype=torch.int32, device=DEV)
+            got = nq.page_release(table, lens, keep, 16, free, top)
+            put = min(gone.numel(), top)
+            assert got.tolist() == [gone.numel(), gone.numel() - put]
+            assert torch.equal(free[top - put:top].flip(0), gone[:put])
+            assert bool((free[:top - put] == -7).all()) and bool((free[top:] == -7).all())
+
+
+def test_a_free_list_that_ran_out_and_a_release(nq):
+    """Steps that ask for more pages than there are, and releases after them: no page is lost or handed out twice, and the list
+    holds nothing but pages."""
+    P, R, pages = 16, 6, 16
+    rng = random.Random(5)
+    free, top = torch.randperm(pages, device=DEV).to(torch.int32), 0
+    table = torch.full((R, 20), -1, dtype=torch.int32, device=DEV)
+    lens, ran_out = [0] * R, 0
+    for step in range(60):
+        new = [rng.randrange(60) if n < 200 else 0 for n in lens]
+        m = nq.page_map(_i32(lens), _i32(new), free[top:], table, P, sum(new))
+        taken, lacked = m.counts.tolist()[1:3]
+        ran_out += lacked > 0
+        top += taken - lacked
+        lens = [a + b for a, b in zip(lens, new)]
+        keep = [0 if rng.random() < 0.3 else rng.randrange(n + 1) for n in lens]
+        released, no_room = nq.page_release(table, _i32(lens), _i32(keep), P, free, top).tolist()
+        assert no_room == 0
+        top -= released
+        lens = keep
+        held = [p for r in range(R) for p in table[r, :-(-lens[r] // P)].tolist() if p >= 0]
+        assert sorted(held + free[top:].tolist()) == list(range(pages))
+    assert ran_out > 5
