@@ -123,6 +123,9 @@ SIGNATURES = {
     "nq_page_release": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
                                        ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                        ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
+    "nq_page_release_clear": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
+                                             ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                             ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
     "nq_paged_status": (ctypes.c_int, [ctypes.c_void_p]),
     "nq_strerror": (ctypes.c_char_p, [ctypes.c_int]),
 }

@@ -39,10 +39,12 @@ __device__ __forceinline__ T sum_upto(T x, int lane) {
     return x;
 }
 
+// CLEAR: -1 into the columns whose pages went on the list.
+template <bool CLEAR>
 __global__ void __launch_bounds__(kReleaseThreads)
-    page_release_kernel(const int32_t* __restrict__ table, int64_t table_stride, int table_cols,
+    page_release_kernel(int32_t* table, int64_t table_stride, int table_cols,
                         const int32_t* __restrict__ kv_lens, const int32_t* __restrict__ keep_lens, int requests, int page_shift,
-                        int32_t* __restrict__ free_pages, int top, int32_t* __restrict__ counts) {
+                        int32_t* free_pages, int top, int32_t* counts) {
     __shared__ long long s_upto[kReleaseThreads];  // columns released by the chunk's requests up to this one's end
     __shared__ int s_end[kReleaseThreads];         // the request's last column + 1
     __shared__ long long s_warp[kReleaseWarps];    // columns of a warp's requests
@@ -82,40 +84,46 @@ __global__ void __launch_bounds__(kReleaseThreads)
         for (bool more = true; more; begin += part * warps, turn ^= 1) {
             const long long from = min(begin + part * ((long long)rank * kReleaseWarps + warp), total), to = min(from + part, total);
             const int groups = int((to - from + 31) >> 5);
-            int at = 0;                    // a group's first column is this request's (the first whose columns end past it) or a later one's
-            long long ends = 0;            // the columns up to its end
-            const int32_t* row = nullptr;  // row[i] is its column i's entry
-            auto go_to = [&](int request) {
-                at = request;
-                ends = s_upto[at];
-                row = table + (r0 + at) * table_stride + (s_end[at] - ends);
-            };
-            if (from < to) {
-                const int of_32 = 32 * (__ffs(__ballot_sync(0xffffffffu, lane < kReleaseWarps && s_upto[32 * lane + 31] > from)) - 1);
-                go_to(of_32 + __ffs(__ballot_sync(0xffffffffu, s_upto[of_32 + lane] > from)) - 1);
-            }
-#pragma unroll 1
-            for (int u = 0; u < groups; ++u) {
-                const long long first = from + 32 * u, mine = first + lane;
-                const int32_t* entry = row + mine;
-                if (min(first + 32, to) > ends) {  // columns of several requests
-                    int lo = at;
-                    for (int hi = kReleaseThreads - 1; lo < hi;) {
-                        const int mid = (lo + hi) >> 1;
-                        if (s_upto[mid] > min(mine, to - 1))
-                            hi = mid;
-                        else
-                            lo = mid + 1;
-                    }
-                    __syncwarp();
-                    entry = table + (r0 + lo) * table_stride + (s_end[lo] - s_upto[lo]) + mine;
-                    go_to(__shfl_sync(0xffffffffu, lo, 31));
+            // f(group, this lane's entry, whether it has one) for the groups in order.
+            auto each = [&](auto f) {
+                int at = 0;              // a group's first column is this request's (the first whose columns end past it) or a later one's
+                long long ends = 0;      // the columns up to its end
+                int32_t* row = nullptr;  // row[i] is its column i's entry
+                auto go_to = [&](int request) {
+                    at = request;
+                    ends = s_upto[at];
+                    row = table + (r0 + at) * table_stride + (s_end[at] - ends);
+                };
+                if (from < to) {
+                    const int of_32 = 32 * (__ffs(__ballot_sync(0xffffffffu, lane < kReleaseWarps && s_upto[32 * lane + 31] > from)) - 1);
+                    go_to(of_32 + __ffs(__ballot_sync(0xffffffffu, s_upto[of_32 + lane] > from)) - 1);
                 }
-                if (mine < to)
+#pragma unroll 1
+                for (int u = 0; u < groups; ++u) {
+                    const long long first = from + 32 * u, mine = first + lane;
+                    int32_t* entry = row + mine;
+                    if (min(first + 32, to) > ends) {  // columns of several requests
+                        int lo = at;
+                        for (int hi = kReleaseThreads - 1; lo < hi;) {
+                            const int mid = (lo + hi) >> 1;
+                            if (s_upto[mid] > min(mine, to - 1))
+                                hi = mid;
+                            else
+                                lo = mid + 1;
+                        }
+                        __syncwarp();
+                        entry = table + (r0 + lo) * table_stride + (s_end[lo] - s_upto[lo]) + mine;
+                        go_to(__shfl_sync(0xffffffffu, lo, 31));
+                    }
+                    f(u, entry, mine < to);
+                }
+            };
+            each([&](int u, const int32_t* entry, bool there) {
+                if (there)
                     copy_async(&s_page[warp][u][lane], entry);
                 else
                     s_page[warp][u][lane] = -1;
-            }
+            });
             copies_wait();  // a lane reads what it copied
             int pages = 0;
             for (int u = 0; u < groups; ++u) pages += __popc(__ballot_sync(0xffffffffu, s_page[warp][u][lane] >= 0));
@@ -141,12 +149,22 @@ __global__ void __launch_bounds__(kReleaseThreads)
                 more = more || (told & 1);
             }
             int left = int(max(top - k, 0ll));  // places on the list in front of this warp's
-            for (int u = 0; u < groups; ++u) {
+            auto put = [&](int u) {
                 const int page = s_page[warp][u][lane];
                 const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
                 const int to_list = left - 1 - __popc(have & ((1u << lane) - 1));
-                if (page >= 0 && to_list >= 0) free_pages[to_list] = page;
                 left -= __popc(have);
+                if (page < 0 || to_list < 0) return false;
+                free_pages[to_list] = page;
+                return true;
+            };
+            if constexpr (CLEAR) {
+                each([&](int u, int32_t* entry, bool) {
+                    if (put(u)) *entry = -1;
+                    __syncwarp();
+                });
+            } else {
+                for (int u = 0; u < groups; ++u) put(u);
             }
         }
     }
@@ -158,6 +176,7 @@ __global__ void __launch_bounds__(kReleaseThreads)
 }
 
 // Blocks for a call: what takes all columns that there may be in one round, 16 at most and 8 where a cluster cannot be larger.
+template <bool CLEAR>
 unsigned cluster_blocks(int requests, int table_cols) {
     static std::mutex mu;
     static std::map<int, unsigned> most;  // per device
@@ -179,22 +198,20 @@ unsigned cluster_blocks(int requests, int table_cols) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        known = cudaFuncSetAttribute(page_release_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                        cudaOccupancyMaxActiveClusters(&clusters, page_release_kernel, &cfg) == cudaSuccess && clusters > 0
+        const auto kernel = page_release_kernel<CLEAR>;
+        known = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters > 0
                     ? kReleaseBlocks
                     : 8;
     }
     return known;
 }
 
-}  // namespace
-}  // namespace nq
-
-extern "C" int nq_page_release(const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
-                               const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top,
-                               int32_t* counts, void* stream) {
+template <bool CLEAR>
+int release(int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens, const int32_t* keep_lens,
+            int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top, int32_t* counts, void* stream) {
     if (requests < 0 || table_cols < 0 || top < 0) return NQ_ERR_ARG;
-    if (!nq::paged_page_size_ok(page_size)) return NQ_ERR_UNSUPPORTED;
+    if (!paged_page_size_ok(page_size)) return NQ_ERR_UNSUPPORTED;
     if (!counts) return NQ_ERR_ARG;
     if (requests > 0 && (!kv_lens || !keep_lens)) return NQ_ERR_ARG;
     if (requests > 0 && table_cols > 0 && !block_table) return NQ_ERR_ARG;
@@ -203,18 +220,35 @@ extern "C" int nq_page_release(const int32_t* block_table, int64_t table_stride,
     for (const void* p : {static_cast<const void*>(block_table), static_cast<const void*>(kv_lens),
                           static_cast<const void*>(keep_lens), static_cast<const void*>(free_pages),
                           static_cast<const void*>(counts)})
-        if (!nq::paged_aligned(p, 4)) return NQ_ERR_ARG;
+        if (!paged_aligned(p, 4)) return NQ_ERR_ARG;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = nq::cluster_blocks(requests, table_cols);
+    attr.val.clusterDim.x = cluster_blocks<CLEAR>(requests, table_cols);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(attr.val.clusterDim.x);
-    cfg.blockDim = dim3(nq::kReleaseThreads);
+    cfg.blockDim = dim3(kReleaseThreads);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, nq::page_release_kernel, block_table, table_stride, table_cols, kv_lens, keep_lens,
-                                             requests, nq::paged_page_shift(page_size), free_pages, top, counts);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, page_release_kernel<CLEAR>, block_table, table_stride, table_cols, kv_lens, keep_lens,
+                                             requests, paged_page_shift(page_size), free_pages, top, counts);
     return e == cudaSuccess ? NQ_OK : NQ_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace nq
+
+extern "C" int nq_page_release(const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
+                               const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top,
+                               int32_t* counts, void* stream) {
+    return nq::release<false>(const_cast<int32_t*>(block_table), table_stride, table_cols, kv_lens, keep_lens, requests, page_size,
+                              free_pages, top, counts, stream);
+}
+
+extern "C" int nq_page_release_clear(int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
+                                     const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top,
+                                     int32_t* counts, void* stream) {
+    return nq::release<true>(block_table, table_stride, table_cols, kv_lens, keep_lens, requests, page_size, free_pages, top, counts,
+                             stream);
 }

@@ -153,7 +153,7 @@ def page_map(ctx_lens, new_lens, free_pages, block_table, page_size, tokens, out
     """Block table and slot map of a step from its lengths (device int32 [requests] each: tokens cached, tokens
     new).  New columns of block_table (int32 [requests, columns], updated in place) take the next entries of
     free_pages (int32), requests in order.  tokens: the step's room, at least the sum of new_lens (the rows past
-    the sum are padding).  Returns a PageMap: q_start [requests + 1], kv_lens [requests], slots [tokens] (int64:
+    the sum are padding; columns that only tokens past the room would begin stay as they are).  Returns a PageMap: q_start [requests + 1], kv_lens [requests], slots [tokens] (int64:
     page * page_size + offset, -1 for padding and for tokens without a page), positions [tokens] (-1 for padding) and
     counts [4]: new tokens, pages taken, pages the free list lacked, requests longer than their table row."""
     # the free list's length changes from step to step, and is checked here
@@ -383,21 +383,24 @@ def _check_compact(K_pages, V_pages, block_table, q_start, kv_lens, path):
             block_table.shape[1], n, path.shape[0])
 
 
-def page_release(block_table, kv_lens, keep_lens, page_size, free_pages, top, out=None):
+def page_release(block_table, kv_lens, keep_lens, page_size, free_pages, top, out=None, clear=False):
     """Give back the pages past the tokens that requests keep (device int32 [requests] each: tokens with pages, tokens to keep).
 
     free_pages (int32, updated in place) is the whole free list, a stack whose free part begins at `top`: free_pages[top:] is what
     page_map is given.  The k-th released page, requests and columns in order, goes to free_pages[top - 1 - k]; columns that never
     got a page (entries below zero) give none back.
-    Returns counts [2]: pages released, those that found no room (top is lower by the difference).  The table stays as it is."""
+    Returns counts [2]: pages released, those that found no room (top is lower by the difference).  The table stays as it is; with
+    clear, columns whose pages went on the list become -1, as they must where a later step may bring more tokens than its room
+    (page_map writes no column for those, and the old entry would name a page that another request has by then)."""
     n_free = free_pages.numel()
     if not 0 <= top <= n_free or n_free > _I32_MAX:
         raise ValueError("top is %d; free_pages has %d entries" % (top, n_free))
-    key = ("release", page_size, *_meta(block_table), *_meta(kv_lens), *_meta(keep_lens), free_pages.dtype, free_pages.dim(),
+    clear = bool(clear)
+    key = ("release", page_size, clear, *_meta(block_table), *_meta(kv_lens), *_meta(keep_lens), free_pages.dtype, free_pages.dim(),
            free_pages.is_contiguous(), free_pages.get_device(), None if out is None else _meta(out))
     kept = _KEPT.get(key)
     if kept is None:
-        kept = _keep(key, _check_release(block_table, kv_lens, keep_lens, page_size, free_pages, out))
+        kept = _keep(key, _check_release(block_table, kv_lens, keep_lens, page_size, free_pages, out, clear))
     index, fn, n, cols, stride = kept
     if out is None:
         out = torch.empty(2, dtype=torch.int32, device=kv_lens.device)
@@ -406,7 +409,7 @@ def page_release(block_table, kv_lens, keep_lens, page_size, free_pages, top, ou
     return out
 
 
-def _check_release(block_table, kv_lens, keep_lens, page_size, free_pages, out):
+def _check_release(block_table, kv_lens, keep_lens, page_size, free_pages, out, clear):
     dev, n, i32 = kv_lens.device, kv_lens.numel(), torch.int32
     if page_size > 0:  # others are the library's to refuse
         _check_size(page_size, "page_size")
@@ -416,7 +419,8 @@ def _check_release(block_table, kv_lens, keep_lens, page_size, free_pages, out):
     _check_table(block_table, n, dev)
     if out is not None:
         _check_vec(out, "out", i32, dev, 2)
-    return dev.index, _lib.lib().nq_page_release, n, block_table.shape[1], block_table.stride(0)
+    fn = _lib.lib().nq_page_release_clear if clear else _lib.lib().nq_page_release
+    return dev.index, fn, n, block_table.shape[1], block_table.stride(0)
 
 
 def paged_status(device=None):

@@ -323,7 +323,8 @@ typedef struct {
  *   counts       device int32[4]: total of n; pages asked for; pages that
  *                the free list lacked; requests longer than their table row
  * `tokens` is the step's room: tokens past it get no row and no page
- * (counts[0] > tokens tells).  Sums past 2^31 - 1 are stored as 2^31 - 1.
+ * (counts[0] > tokens tells).  Columns that they alone would begin stay, though kv_lens counts them: they
+ * must name no page then (as from the start, or after nq_page_release_clear).  Sums past 2^31 - 1 are stored as 2^31 - 1.
  * The free list is not changed: the caller drops its first counts[1] entries.
  * Entries of the table and of the free list are copied, not checked. */
 int nq_page_map(const int32_t* ctx_lens, const int32_t* new_lens, int32_t requests, const int32_t* free_pages,
@@ -481,10 +482,18 @@ int nq_paged_compact(const nq_pool* pool, int32_t layers, int64_t layer_stride, 
  *   counts  device int32[2]: pages given back; those among them for which
  *           there was no room (k >= top), which go nowhere
  * Other entries are copied, not checked; the table is left as it is, so columns that
- * are released twice are on the list twice. */
+ * are released twice are on the list twice, and go on naming pages that other requests may have
+ * by then.  nq_page_map writes over such a column as soon as one of the request's tokens begins it, so no
+ * length that it returns covers one, unless the step had more tokens than its room. */
 int nq_page_release(const int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
                     const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages, int32_t top,
                     int32_t* counts, void* stream);
+
+/* nq_page_release that also writes -1 into each column whose page went on the list: it
+ * names nobody's page from there on, and gives nothing back when it is released again. */
+int nq_page_release_clear(int32_t* block_table, int64_t table_stride, int32_t table_cols, const int32_t* kv_lens,
+                          const int32_t* keep_lens, int32_t requests, int32_t page_size, int32_t* free_pages,
+                          int32_t top, int32_t* counts, void* stream);
 
 /* Waits for `stream`, then returns NQ_ERR_CUDA if it failed or if an attention
  * kernel on the current device gave up waiting for its loads since that was

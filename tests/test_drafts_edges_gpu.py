@@ -89,3 +89,61 @@ def test_a_free_list_that_ran_out_and_a_release(nq):
         held = [p for r in range(R) for p in table[r, :-(-lens[r] // P)].tolist() if p >= 0]
         assert sorted(held + free[top:].tolist()) == list(range(pages))
     assert ran_out > 5
+
+
+@pytest.mark.parametrize("R", [1, 13, 512, 1500])
+def test_release_that_clears_the_table(nq, R):
+    """Columns whose pages went on the list become -1, all others stay (those past the columns too); a second call gives nothing back."""
+    rng = random.Random(R)
+    for cols, most in ((1, 16), (9, 200), (200, 16 * 200)):
+        lens = [rng.choice([0, 1, 16, 17, -3, rng.randrange(most), most]) for _ in range(R)]
+        keep = [rng.choice([0, n, n - 1, n - 16, -1]) for n in lens]
+        table = [[-1 if rng.random() < 0.1 else rng.randrange(10 ** 6) for _ in range(cols)] for _ in range(R)]
+        total = ref_release_pages(table, lens, keep, 16, [], 0)[1][0]
+        for top in (total, total + 5, max(total - 3, 0)):
+            free = [rng.randrange(10 ** 6) for _ in range(top + 4)]
+            want, counts = ref_release_pages(table, lens, keep, 16, free, top)
+            left, k = [list(row) for row in table], 0
+            for row, n, m in zip(left, lens, keep):
+                for c in range(-(-max(m, 0) // 16), min(-(-max(n, 0) // 16), cols)):
+                    if row[c] >= 0:
+                        k += 1
+                        if k <= top:
+                            row[c] = -1
+            wide = torch.full((R, cols + 3), 5, dtype=torch.int32, device=DEV)
+            wide[:, :cols] = torch.tensor(table, dtype=torch.int32, device=DEV).view(R, cols)
+            dev = _i32(free)
+            args = (wide[:, :cols], _i32(lens), _i32(keep), 16, dev)
+            assert nq.page_release(*args, top, clear=True).tolist() == counts
+            assert dev.tolist() == want and wide[:, :cols].tolist() == left and bool((wide[:, cols:] == 5).all())
+            lost, put = counts[1], counts[0] - counts[1]
+            assert nq.page_release(*args, top - put, clear=True).tolist() == [lost, max(lost - (top - put), 0)]
+            assert dev[top - put:].tolist() == want[top - put:]
+
+
+def test_a_step_past_its_room_after_a_release_that_clears(nq):
+    """A request gives pages back, another gets them, and then the first one's step has more tokens than its room: kv_lens counts tokens
+    whose columns were never written, and neither the attention nor the next step's append reaches the other's pages through them."""
+    P, H, D, pages = 16, 2, 64, 12
+    table = torch.full((2, 8), -1, dtype=torch.int32, device=DEV)
+    free, top = torch.arange(pages, dtype=torch.int32, device=DEV), 0
+    Kp, Vp = (torch.randn(pages, H, P, D, device=DEV).half() for _ in range(2))
+    nq.page_map(_i32([0, 0]), _i32([80, 0]), free[top:], table, P, 80)
+    top += 5
+    top -= int(nq.page_release(table, _i32([80, 0]), _i32([20, 0]), P, free, top, clear=True)[0])
+    nq.page_map(_i32([20, 0]), _i32([0, 70]), free[top:], table, P, 70)  # the other request takes them
+    top += 5
+    others = table[1, :5].tolist()
+    assert set(others) & {0, 1, 2, 3, 4}
+    m = nq.page_map(_i32([20, 70]), _i32([50, 0]), free[top:], table, P, 3)  # room for three of fifty
+    assert m.counts.tolist()[0] == 50 and m.kv_lens.tolist() == [70, 70]
+    assert not set(table[0].tolist()) & set(others)
+    Q = torch.randn(3, 4, D, device=DEV).half()
+    saw = []
+    for value in (1.0, 500.0):
+        Kp[others], Vp[others] = value, value
+        saw.append(nq.paged_attention(Q, Kp, Vp, table, m.q_start, m.kv_lens, max_q=3, causal=False))
+    assert torch.equal(*saw)
+    m = nq.page_map(m.kv_lens, _i32([1, 0]), free[top:], table, P, 1)
+    nq.paged_append(*(torch.randn(1, H, D, device=DEV).half() for _ in range(2)), Kp, Vp, m.slots)
+    assert m.slots.tolist() == [-1] and bool((Kp[others] == 500).all()) and bool((Vp[others] == 500).all())
