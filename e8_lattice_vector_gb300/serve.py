@@ -19,6 +19,7 @@ from dataclasses import dataclass
 
 import torch
 
+from . import _lib
 from .codec import RopeTable, compress_kv, decompress_kv
 from .drafts import DraftTree, draft_tree, verify_drafts
 from .paged import (PageMap, page_map, page_release, paged_append, paged_attention, paged_attention_workspace,
@@ -77,8 +78,10 @@ class PagedCache:
     def draft(self, trees):
         """Map a step whose request r brings the tree trees[r] (its nodes' parents, the root first; [] for none)."""
         nodes = [len(t) for t in trees]
-        m = self.extend(nodes)
+        if max(nodes, default=0) > 64 * _lib.NQ_TREE_WORDS:  # before the step takes pages
+            raise ValueError("a tree has %d nodes; there may be %d at most" % (max(nodes), 64 * _lib.NQ_TREE_WORDS))
         parents = self._ints([p for t in trees for p in t])
+        m = self.extend(nodes)
         return DraftStep(m, draft_tree(parents, m.q_start, m.kv_lens, max(nodes)), parents, nodes)
 
     def keep(self, step, verdict):

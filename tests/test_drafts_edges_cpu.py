@@ -19,3 +19,43 @@ def test_release_that_clears_refusals(nq):
         a = dict({"free": _Fake((9,), I32), "k": lens, "top": 4}, **kw)
         with pytest.raises(ValueError, match=text):
             pkg.page_release(table, lens, a["k"], 16, a["free"], a["top"], clear=True)
+
+
+class _Steps:
+    """A PagedCache on the CPU whose calls of the library are written down."""
+
+    def __init__(self, monkeypatch, requests=2, tokens=16 * 500, counts=None):
+        from e8_lattice_vector_gb300 import serve
+        from e8_lattice_vector_gb300.drafts import DraftTree, draft_tree
+        from e8_lattice_vector_gb300.paged import PageMap
+
+        self.calls, none = [], torch.zeros(0)
+        monkeypatch.setattr(serve, "page_map", lambda ctx, new, free, *a: self.calls.append(("map", ctx.tolist(), new.tolist(), free.numel()))
+                            or PageMap(none, ctx + new, none, none, none))
+        monkeypatch.setattr(serve, "draft_tree", lambda parents, q, kv, most: self.calls.append(("tree", most)) or DraftTree(none, none)
+                            if most <= 4096 else draft_tree(parents, q, kv, most))
+        monkeypatch.setattr(serve, "paged_compact", lambda *a: self.calls.append(("compact",)))
+        monkeypatch.setattr(serve, "paged_append", lambda *a: self.calls.append(("append",)))
+        monkeypatch.setattr(serve, "paged_attention", lambda *a, **kw: self.calls.append(("attention",)))
+        monkeypatch.setattr(serve, "page_release", lambda table, lens, keep, size, free, top: self.calls.append(
+            ("release", lens.tolist(), keep.tolist(), top)) or (counts.pop(0) if counts else None))
+        self.cache = serve.PagedCache(1, requests, 1, 64, 16, tokens, torch.float16, torch.device("cpu"))
+
+    def state(self):
+        return list(self.cache.lengths), self.cache.top, self.cache.free.tolist(), len(self.calls)
+
+
+def test_a_tree_that_is_refused_changes_nothing(monkeypatch):
+    s = _Steps(monkeypatch)
+    s.cache.extend([30, 5])
+    before = s.state()
+    for trees in ([[-1] + list(range(4096)), []], [[], [-1] * 5000]):
+        with pytest.raises(ValueError, match="nodes"):
+            s.cache.draft(trees)
+        assert s.state() == before
+    for trees in ([[-1, "x"], []], [[-1, 2 ** 40], []]):  # parents that are no 32-bit numbers
+        with pytest.raises((TypeError, ValueError, RuntimeError, OverflowError)):
+            s.cache.draft(trees)
+        assert s.state() == before
+    step = s.cache.draft([[-1] + list(range(4095)), [-1]])
+    assert step.nodes == [4096, 1] and s.cache.lengths == [30 + 4096, 6]
