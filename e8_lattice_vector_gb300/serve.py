@@ -49,6 +49,7 @@ class PagedCache:
         self.table = torch.full((requests, self.columns), -1, dtype=torch.int32, device=device)
         self.stack, self.top = torch.randperm(pages, device=device).to(torch.int32), 0  # free pages: stack[top:]
         self.lengths = [0] * requests  # the scheduler's copy: only accepted drafts are read back from the device
+        self.pending = None  # the step of trees that was mapped last, until its rows are kept or the requests' lengths change otherwise
 
     @property
     def free(self):
@@ -73,6 +74,7 @@ class PagedCache:
         m = page_map(ctx, fresh, self.free, self.table, self.page_size, sum(new))
         self.top += sum(self._pages(c + n) - self._pages(c) for c, n in zip(self.lengths, new))
         self.lengths = [c + n for c, n in zip(self.lengths, new)]
+        self.pending = None
         return m
 
     def draft(self, trees):
@@ -82,11 +84,19 @@ class PagedCache:
             raise ValueError("a tree has %d nodes; there may be %d at most" % (max(nodes), 64 * _lib.NQ_TREE_WORDS))
         parents = self._ints([p for t in trees for p in t])
         m = self.extend(nodes)
-        return DraftStep(m, draft_tree(parents, m.q_start, m.kv_lens, max(nodes)), parents, nodes)
+        self.pending = DraftStep(m, draft_tree(parents, m.q_start, m.kv_lens, max(nodes, default=0)), parents, nodes)
+        return self.pending
+
+    def _check_pending(self, step):
+        """A step's pages and lengths are those of the cache until the next change."""
+        if step is not self.pending:
+            raise ValueError("the step is not the one that was drafted last, or its rows have been kept already")
 
     def keep(self, step, verdict):
         """Keep the step's accepted rows alone: they move to the front of their request's, and pages past them are free again.
-        Returns how many each request keeps (read back, so this waits for the step)."""
+        Returns how many each request keeps (read back, so this waits for the step).  Only the step that was drafted last can be
+        kept, once, and before requests are extended or end."""
+        self._check_pending(step)
         m = step.map
         paged_compact(self.K, self.V, self.table, m.q_start, m.kv_lens, verdict.path)
         kept = verdict.accepted.tolist()
@@ -102,6 +112,7 @@ class PagedCache:
         page_release(self.table, lens, self._ints(keep), self.page_size, self.stack, self.top)
         self.top -= sum(self._pages(n) - self._pages(k) for n, k in zip(self.lengths, keep))
         self.lengths = keep
+        self.pending = None
 
     def fill(self, K, V):
         """Put a prompt's cache [layers, requests, kv_heads, tokens, head_dim] into the pages, as the codec leaves it."""
@@ -117,7 +128,8 @@ class PagedCache:
         return self._attend(self.extend(new), q, k, v, max(new), ws)
 
     def draft_step(self, q, k, v, step, ws=None):
-        """Append a mapped step's trees and let them attend; shapes as in step()."""
+        """Append a mapped step's trees and let them attend; shapes as in step().  The step must be the one that was drafted last."""
+        self._check_pending(step)
         return self._attend(step.map, q, k, v, max(step.nodes), ws, step.tree)
 
     def _attend(self, m, q, k, v, max_q, ws, tree=None):

@@ -59,3 +59,40 @@ def test_a_tree_that_is_refused_changes_nothing(monkeypatch):
         assert s.state() == before
     step = s.cache.draft([[-1] + list(range(4095)), [-1]])
     assert step.nodes == [4096, 1] and s.cache.lengths == [30 + 4096, 6]
+
+
+def _verdict(accepted, rows):
+    from e8_lattice_vector_gb300.drafts import Verdict
+
+    return Verdict(torch.tensor(accepted, dtype=torch.int32), torch.zeros(rows, dtype=torch.int32), None)
+
+
+def test_a_step_is_kept_once_and_before_the_next_change(monkeypatch):
+    """keep() counts pages from the cache's lengths, and the device from the step's: they must be the same step's."""
+    def refused(c, s, step, rows):
+        before = s.state()
+        with pytest.raises(ValueError, match="drafted last"):
+            c.keep(step, _verdict([1, 1], rows))
+        with pytest.raises(ValueError, match="drafted last"):
+            c.draft_step(*(torch.zeros(1, rows, 1, 64),) * 3, step)
+        assert s.state() == before
+
+    for change in ("keep", "extend", "draft", "end"):
+        s = _Steps(monkeypatch)
+        c = s.cache
+        c.extend([30, 5])
+        step = c.draft([[-1, 0, 0], [-1, 0]])
+        c.draft_step(*(torch.zeros(1, 5, 1, 64),) * 3, step)  # as often as it takes
+        c.draft_step(*(torch.zeros(1, 5, 1, 64),) * 3, step)
+        if change == "keep":
+            assert c.keep(step, _verdict([2, 1], 5)) == [2, 1] and c.lengths == [32, 6]
+        elif change == "extend":
+            c.extend([1, 1])
+        elif change == "draft":
+            newer = c.draft([[-1, 0], [-1]])
+        else:
+            c.end([1])
+        refused(c, s, step, 5)
+        if change == "draft":  # the newer one is the cache's
+            assert c.keep(newer, _verdict([1, 1], 3)) == [1, 1] and c.lengths == [34, 8]
+            refused(c, s, newer, 3)
