@@ -97,6 +97,9 @@ class PagedCache:
         Returns how many each request keeps (read back, so this waits for the step).  Only the step that was drafted last can be
         kept, once, and before requests are extended or end."""
         self._check_pending(step)
+        if verdict.accepted.numel() != len(step.nodes) or verdict.path.numel() != sum(step.nodes):
+            raise ValueError("the verdict is of %d requests and %d nodes; the step has %d and %d" % (
+                verdict.accepted.numel(), verdict.path.numel(), len(step.nodes), sum(step.nodes)))
         m = step.map
         paged_compact(self.K, self.V, self.table, m.q_start, m.kv_lens, verdict.path)
         kept = verdict.accepted.tolist()

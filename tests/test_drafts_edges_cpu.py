@@ -96,3 +96,14 @@ def test_a_step_is_kept_once_and_before_the_next_change(monkeypatch):
         if change == "draft":  # the newer one is the cache's
             assert c.keep(newer, _verdict([1, 1], 3)) == [1, 1] and c.lengths == [34, 8]
             refused(c, s, newer, 3)
+
+
+def test_a_verdict_of_another_step_is_refused(monkeypatch):
+    s = _Steps(monkeypatch)
+    step = s.cache.draft([[-1, 0, 0], [-1, 0]])
+    before = s.state()
+    for accepted, rows in (([1], 5), ([1, 1, 1], 5), ([1, 1], 4), ([1, 1], 6)):
+        with pytest.raises(ValueError, match="verdict is of"):
+            s.cache.keep(step, _verdict(accepted, rows))
+        assert s.state() == before
+    assert s.cache.keep(step, _verdict([3, 2], 5)) == [3, 2] and s.cache.lengths == [3, 2]
