@@ -109,6 +109,8 @@ class PagedCache:
     def end(self, requests):
         """Give back all pages of requests that have ended."""
         gone = set(requests)
+        if not gone <= set(range(len(self.lengths))):
+            raise ValueError("there are %d requests, numbered from 0; got %s" % (len(self.lengths), sorted(gone)))
         self._release(self._ints(self.lengths), [0 if r in gone else n for r, n in enumerate(self.lengths)])
 
     def _release(self, lens, keep):

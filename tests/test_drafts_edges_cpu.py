@@ -107,3 +107,15 @@ def test_a_verdict_of_another_step_is_refused(monkeypatch):
             s.cache.keep(step, _verdict(accepted, rows))
         assert s.state() == before
     assert s.cache.keep(step, _verdict([3, 2], 5)) == [3, 2] and s.cache.lengths == [3, 2]
+
+
+def test_requests_that_are_not_there_cannot_end(monkeypatch):
+    s = _Steps(monkeypatch, requests=3)
+    s.cache.extend([30, 16, 1])
+    before = s.state()
+    for gone in ([3], [-1], [0, 7], range(-2, 1)):
+        with pytest.raises(ValueError, match="there are 3 requests"):
+            s.cache.end(gone)
+        assert s.state() == before
+    s.cache.end(r for r in (2, 0, 2))
+    assert s.cache.lengths == [0, 16, 0]
