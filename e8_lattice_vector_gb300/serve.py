@@ -48,12 +48,20 @@ class PagedCache:
         self.V = torch.empty(shape, dtype=dtype, device=device)
         self.table = torch.full((requests, self.columns), -1, dtype=torch.int32, device=device)
         self.stack, self.top = torch.randperm(pages, device=device).to(torch.int32), 0  # free pages: stack[top:]
+        self.ran_out = False  # some columns may have no page: only the device knows how many come back
         self.lengths = [0] * requests  # the scheduler's copy: only accepted drafts are read back from the device
         self.pending = None  # the step of trees that was mapped last, until its rows are kept or the requests' lengths change otherwise
 
     @property
     def free(self):
         return self.stack[self.top:]
+
+    @free.setter
+    def free(self, pages):
+        # on a stack with room for those that the requests hold
+        held = sum(self._pages(n) for n in self.lengths)
+        self.top = max(self.stack.numel() - pages.numel(), held)
+        self.stack = torch.cat([pages.new_full((self.top,), -1), pages])
 
     def _pages(self, tokens):
         return -(-tokens // self.page_size)
@@ -72,7 +80,9 @@ class PagedCache:
                 raise ValueError("%d tokens do not fit %d pages of %d" % (c + n, self.columns, self.page_size))
         ctx, fresh = self._ints([self.lengths, new])
         m = page_map(ctx, fresh, self.free, self.table, self.page_size, sum(new))
-        self.top += sum(self._pages(c + n) - self._pages(c) for c, n in zip(self.lengths, new))
+        taken, left = sum(self._pages(c + n) - self._pages(c) for c, n in zip(self.lengths, new)), self.stack.numel() - self.top
+        self.top += min(taken, left)
+        self.ran_out |= taken > left
         self.lengths = [c + n for c, n in zip(self.lengths, new)]
         self.pending = None
         return m
@@ -114,8 +124,13 @@ class PagedCache:
         self._release(self._ints(self.lengths), [0 if r in gone else n for r, n in enumerate(self.lengths)])
 
     def _release(self, lens, keep):
-        page_release(self.table, lens, self._ints(keep), self.page_size, self.stack, self.top)
-        self.top -= sum(self._pages(n) - self._pages(k) for n, k in zip(self.lengths, keep))
+        # a step has room for all its tokens, so no length covers a column that was not written: the table need not be cleared
+        counts = page_release(self.table, lens, self._ints(keep), self.page_size, self.stack, self.top)
+        if self.ran_out:
+            released, no_room = counts.tolist()
+            self.top -= released - no_room
+        else:
+            self.top -= sum(self._pages(n) - self._pages(k) for n, k in zip(self.lengths, keep))
         self.lengths = keep
         self.pending = None
 

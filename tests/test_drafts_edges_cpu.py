@@ -119,3 +119,34 @@ def test_requests_that_are_not_there_cannot_end(monkeypatch):
         assert s.state() == before
     s.cache.end(r for r in (2, 0, 2))
     assert s.cache.lengths == [0, 16, 0]
+
+
+def test_the_free_list_can_be_set(monkeypatch):
+    """As an attribute: to other pages, a part of them, none; what requests hold still finds its place on it."""
+    s = _Steps(monkeypatch, requests=2, tokens=160, counts=[torch.tensor(x) for x in ([1, 0], [2, 0], [5, 0])])
+    c, pages = s.cache, s.cache.free.tolist()
+    assert sorted(pages) == list(range(20))
+    c.free = c.free.flip(0)
+    assert c.free.tolist() == pages[::-1] and c.top == 0
+    c.extend([33, 16])  # three pages and one
+    assert c.free.tolist() == pages[::-1][4:]
+    c.free = c.free[4:9]
+    assert c.free.tolist() == pages[::-1][8:13] and c.top >= 4
+    top = c.top
+    c.extend([20, 0])  # one more
+    assert c.top == top + 1 and c.free.tolist() == pages[::-1][9:13]
+    c.end([1])  # a column with its page
+    assert c.top == top
+    c.free = c.free[:2]
+    left = c.free.tolist()
+    c.extend([60, 20])  # four and two more, where two are left
+    assert c.free.tolist() == [] and s.calls[-1][3] == 2 and len(left) == 2
+    top = c.top
+    c.end([1])  # asked for two and got none or some: the device says how many came back
+    assert c.top == top - 2
+    c.end([0])
+    assert c.top == top - 7
+    c.free = torch.zeros(0, dtype=torch.int32)
+    assert c.free.numel() == 0
+    c.free = torch.arange(50, dtype=torch.int32)  # more than there were
+    assert c.free.tolist() == list(range(50)) and c.lengths == [0, 0]

@@ -147,3 +147,23 @@ def test_a_step_past_its_room_after_a_release_that_clears(nq):
     m = nq.page_map(m.kv_lens, _i32([1, 0]), free[top:], table, P, 1)
     nq.paged_append(*(torch.randn(1, H, D, device=DEV).half() for _ in range(2)), Kp, Vp, m.slots)
     assert m.slots.tolist() == [-1] and bool((Kp[others] == 500).all()) and bool((Vp[others] == 500).all())
+
+
+def test_a_paged_cache_that_runs_out_of_pages(nq):
+    """With fewer free pages than its requests may ask for: lengths go on, columns go without, and all pages are there in the end."""
+    from e8_lattice_vector_gb300.serve import PagedCache
+
+    cache = PagedCache(1, 3, 2, 64, 16, 160, torch.float16, torch.device(DEV, 0))
+    some = cache.free[:9].clone()
+    cache.free = some
+    m = cache.extend([40, 20, 10])  # 3 + 2 + 1
+    assert bool((m.slots >= 0).all()) and cache.free.tolist() == some[6:].tolist()
+    m = cache.extend([100, 1, 30])  # 6 + 0 + 2 of 3
+    assert m.counts.tolist() == [131, 8, 5, 0] and cache.free.numel() == 0
+    assert int((m.slots >= 0).sum()) == 8 + 48 + 1 + 6  # the rest of begun pages, and three new ones
+    cache.end([1, 2])
+    assert sorted(cache.free.tolist()) == sorted(some[3:6].tolist())
+    cache.extend([0, 33, 0])
+    assert cache.free.numel() == 0
+    cache.end([0, 1])
+    assert sorted(cache.free.tolist()) == sorted(some.tolist()) and cache.lengths == [0, 0, 0]
