@@ -712,19 +712,23 @@ extern "C" int nq_verify_drafts(const void* probs, int64_t probs_stride, const v
                           static_cast<const void*>(accepted), static_cast<const void*>(path),
                           static_cast<const void*>(tokens_out)})
         if (!nq::paged_aligned(p, 4)) return NQ_ERR_ARG;
-    // the walk writes while other blocks read
-    const uintptr_t bytes = uintptr_t(tokens) * 4;
-    auto overlap = [](const void* x, uintptr_t nx, const void* y, uintptr_t ny) {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-        return a < b + ny && b < a + nx;
+    // a request's results are written while other requests' blocks read
+    struct Range {
+        uintptr_t at, bytes;
     };
-    for (const void* out : {static_cast<const void*>(path), static_cast<const void*>(tokens_out)}) {
-        for (const void* in : {static_cast<const void*>(drafts), static_cast<const void*>(parents), static_cast<const void*>(uniform)})
-            if (overlap(out, bytes, in, bytes)) return NQ_ERR_ARG;
-        if (overlap(out, bytes, q_start, (uintptr_t(requests) + 1) * 4) || overlap(out, bytes, accepted, uintptr_t(requests) * 4))
-            return NQ_ERR_ARG;
-    }
-    if (overlap(path, bytes, tokens_out, bytes)) return NQ_ERR_ARG;
+    auto range = [](const void* p, uint64_t n) { return Range{reinterpret_cast<uintptr_t>(p), uintptr_t(n)}; };
+    auto rows = [&](const void* p, int64_t stride) {  // as far as 64 bits go
+        const unsigned __int128 n = p && tokens > 0 ? ((unsigned __int128)(tokens - 1) * uint64_t(tokens > 1 ? stride : 0) + vocab) * size : 0;
+        return range(p, uint64_t(std::min<unsigned __int128>(n, UINT64_MAX - reinterpret_cast<uintptr_t>(p))));
+    };
+    const uint64_t bytes = uint64_t(tokens) * 4;
+    const Range all[] = {range(accepted, uint64_t(requests) * 4), range(path, bytes), range(tokens_out, bytes),
+                         range(drafts, bytes), range(parents, bytes), range(uniform, bytes),
+                         range(q_start, (uint64_t(requests) + 1) * 4), rows(probs, probs_stride), rows(draft_probs, draft_stride)};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 9; ++j)
+            if (all[i].bytes > 0 && all[j].bytes > 0 && all[i].at < all[j].at + all[j].bytes && all[j].at < all[i].at + all[i].bytes)
+                return NQ_ERR_ARG;
     const nq::VerifyArgs a{probs,   draft_probs, probs_stride, draft_stride, drafts, parents, q_start,
                            uniform, accepted,    path,         tokens_out,   vocab,  tokens};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -452,7 +452,7 @@ int nq_paged_tree_attention(const nq_attention* a, const int64_t* ancestors, con
  * uniform too.  Sums over the vocabulary, S and the comparisons carry 38 bits at
  * least for up to 2^19 tokens (fp32 pairs).  When all p_cur are 0 the token that follows is -1.
  * q_start is clamped to [0, tokens]; rows of no request are left as they
- * are.  path and tokens_out must overlap neither each other nor the inputs.
+ * are.  accepted, path and tokens_out must overlap neither each other nor the inputs.
  * The result does not depend on the run. */
 int nq_verify_drafts(const void* probs, int64_t probs_stride, const void* draft_probs, int64_t draft_stride,
                      int32_t dtype, int32_t vocab, const int32_t* drafts, const int32_t* parents,

@@ -150,3 +150,20 @@ def test_the_free_list_can_be_set(monkeypatch):
     assert c.free.numel() == 0
     c.free = torch.arange(50, dtype=torch.int32)  # more than there were
     assert c.free.tolist() == list(range(50)) and c.lengths == [0, 0]
+
+
+def test_verify_refuses_results_over_its_inputs(nq):
+    """A request's results are written while other requests read: none may lie over any input, or over another."""
+    f = nq.lib().nq_verify_drafts
+    at = lambda i: 4096 * i
+    good = [at(1), 100, at(2), 100, 2, 100, at(3), at(4), at(5), 4, at(6), 2, at(7), at(8), at(9), None]
+    rows = 4 * (3 * 100 + 100)
+    cases = [(12, 6, 0), (12, 7, 12), (12, 8, -4), (12, 10, 8), (12, 10, -4), (12, 13, 4), (12, 14, 12)]  # accepted
+    cases += [(i, j, by) for i in (12, 13, 14) for j in (0, 2) for by in (0, -4, rows - 4)]  # over probabilities
+    for i, j, by in cases:
+        args = list(good)
+        args[i] = good[j] + by
+        assert f(*args) == ARG, (i, j, by)
+    wide = list(good)
+    wide[1], wide[13] = 2 ** 62, good[0] + 2 ** 40  # a stride beyond all memory
+    assert f(*wide) == ARG
