@@ -11,7 +11,10 @@
 // whole and walk on, and in the end the block whose part holds the token finds it.  What decides how often the blocks meet comes from
 // that one load, so that inputs that change meanwhile, by mistake, cannot part them.
 //
-// Sums decide between whole numbers, so they carry 38 bits and more.  The GPU's 64-bit units are too slow for that (used for no more
+// Sums decide between whole numbers, so they are off by no more than 2^-37 of the sum of p for each rejection and one: 2^-38 of themselves
+// for the additions (see Sums), 2^-45 for a term's and A's own roundings, and an error of A only shrinks, since more taken leaves less.
+// That is no fraction of what is left: with a draft near the model p - A q is small and has p's roundings (S = 2e-7 has 30 bits), but
+// then it is as seldom needed.  The GPU's 64-bit units are too slow for that (used for no more
 // than the threads' totals and the search they took four fifths of the time), so a number that matters is the sum of two fp32: an
 // addition's rounding error is found by Knuth's two-sum, a product's by a fused multiply-add.
 //

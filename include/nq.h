@@ -449,8 +449,9 @@ int nq_paged_tree_attention(const nq_attention* a, const int64_t* ancestors, con
  *   tokens_out  device int32[tokens]: at the request's rows the tokens of the accepted
  *               nodes but the first, then the one that follows, then -1: as many as accepted
  * 1 <= vocab < 2^31 - 65536, requests < 2^28.  Probabilities must be finite; NaN and negative ones count as 0, and a negative
- * uniform too.  Sums over the vocabulary, S and the comparisons carry 38 bits at
- * least for up to 2^19 tokens (fp32 pairs).  When all p_cur are 0 the token that follows is -1.
+ * uniform too.  For up to 2^19 tokens a sum of w after k rejections is off by at most (k + 1) 2^-37 of
+ * the sum of p_cur, and a w(x) by what that makes of q(x) and 2^-45 of p_cur(x) (fp32 pairs): fractions of the whole, not of
+ * what is left, which is little where draft_probs are near probs.  When all p_cur are 0 the token that follows is -1.
  * q_start is clamped to [0, tokens]; rows of no request are left as they
  * are.  accepted, path and tokens_out must overlap neither each other nor the inputs.
  * The result does not depend on the run. */

@@ -167,3 +167,49 @@ def test_verify_refuses_results_over_its_inputs(nq):
     wide = list(good)
     wide[1], wide[13] = 2 ** 62, good[0] + 2 ** 40  # a stride beyond all memory
     assert f(*wide) == ARG
+
+
+@pytest.mark.parametrize("apart", [1.0, 1e-2, 1e-4, 1e-6])
+def test_what_is_left_is_off_by_a_fraction_of_the_whole(apart):
+    """The verification's arithmetic (pairs of fp32, from the kernel's formulas) against fractions: after k rejections the sum of what is left
+    is off by at most (k + 1) 2^-37 of the sum of p, of which the terms alone, added exactly here, take 10 (k + 1) 2^-48.  It is no such fraction of
+    itself: with a draft near the model little is left, and p - A q has p's roundings."""
+    from fractions import Fraction
+
+    import numpy as np
+
+    f, of = np.float32, lambda x: Fraction(float(x))
+
+    def normal(s, e):
+        t = f(s + e)
+        return t, f(e - f(t - s))
+
+    def add(a, b):
+        t = f(a[0] + b[0])
+        v = f(t - a[0])
+        return normal(t, f(f(f(a[0] - f(t - v)) + f(b[0] - v)) + f(a[1] + b[1])))
+
+    def fma(a, b, c):  # 48 bits of product and a sum in 64: a second rounding past the 53rd bit
+        return (np.float64(a) * b.astype(np.float64) + c.astype(np.float64)).astype(f)
+
+    def left(p, q, taken):
+        h = taken[0] * q
+        below = fma(taken[1], q, fma(taken[0], q, -h))
+        d = p - h
+        low = ((p - d) - h) - below
+        return np.where(d + low > 0, d, f(0)), np.where(d + low > 0, low, f(0))
+
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal(1000) * 2
+    p, q = (np.exp(z) / np.exp(z).sum() for z in (x, x + apart * rng.standard_normal(1000)))
+    p, q = p.astype(f), q.astype(f)
+    P, Q = [of(v) for v in p], [of(v) for v in q]
+    taken, total, A, S, worst = (f(0), f(0)), (f(1), f(0)), Fraction(0), Fraction(1), 0
+    for k in range(1, 9):
+        taken, A = add(taken, total), A + S
+        got = sum(of(v) for part in left(p, q, taken) for v in part)
+        S = sum(max(a - A * b, 0) for a, b in zip(P, Q))
+        assert abs(got - S) <= Fraction(10 * (k + 1), 2 ** 48) * sum(P)
+        worst = max(worst, abs(got - S) / S)
+        total = normal(f(float(got)), f(float(got - of(f(float(got))))))
+    assert (worst > Fraction(1, 2 ** 38)) == (apart < 1e-2)

@@ -1,9 +1,11 @@
-"""Calls on drafted trees that test_drafts_gpu leaves out: releases of columns without pages."""
+"""Calls on drafted trees that test_drafts_gpu leaves out: releases of columns without pages, verification of drafts that are all but
+the model's."""
 import random
 
 import pytest
 import torch
 
+from test_drafts_gpu import check_verify, make_tree
 from test_paged_gpu import DEV, _i32, nq  # noqa: F401  (nq is the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -167,3 +169,29 @@ def test_a_paged_cache_that_runs_out_of_pages(nq):
     assert cache.free.numel() == 0
     cache.end([0, 1])
     assert sorted(cache.free.tolist()) == sorted(some.tolist()) and cache.lengths == [0, 0, 0]
+
+
+# -------------------------------------------------------------- verification
+
+
+@pytest.mark.parametrize("apart", [1e-1, 1e-2, 1e-4, 1e-6])
+@pytest.mark.parametrize("V", [3000, 32000, 128256])
+def test_verify_drafts_near_the_model(nq, V, apart):
+    """Drafts all but the model's, the first of them rejected: what is left is as small as the difference, and the later ones are accepted or
+    not by it."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(V)
+    kept = tried = 0
+    for shape in ("star", "star", "wide", "random"):
+        n = 14
+        x = torch.randn(n, V, generator=g, device=DEV) * 2
+        probs = torch.softmax(x, 1)
+        draft = torch.softmax(x + apart * torch.randn(n, V, generator=g, device=DEV), 1)
+        tree = make_tree(shape, n, 1)
+        ids = torch.multinomial(draft[[max(p, 0) for p in tree]], 1, generator=g).squeeze(1).to(torch.int32)
+        ids[1] = int((probs[0] / draft[0]).argmin())  # the least of p / q
+        u = torch.rand(n, generator=g, device=DEV)
+        u[1] = 1 - 2.0 ** -24
+        kept += check_verify(nq, [tree], V, torch.float32, True, probs=probs, draft=draft, ids=ids, u=u)
+        tried += 1
+    assert kept > tried  # some draft is accepted after a rejection
