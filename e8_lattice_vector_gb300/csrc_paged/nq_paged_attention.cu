@@ -7,7 +7,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "nq_paged_device.cuh"
+#include "nq_paged_walk.cuh"
 
 namespace nq {
 namespace {
@@ -176,19 +176,6 @@ bool few_rows(const nq_attention* a, int group, int head_dim) {
            (head_dim <= 96 && 4 * int64_t(a->tokens) * group <= 3 * kSmallRows * int64_t(a->requests));
 }
 
-// Drafted trees of more rows than the small kernel's tile, where the whole call is short: it reads the keys once for each row tile,
-// but has two launches and no plan.  At most six key tiles of 128 x 128 for each block, by the lengths that the table has room for.
-// Requests over cached tokens, rows per KV head (32 heads on 8, head_dim 128, fp16), the small kernel against the large one: 1 over 1500, 32
-// and 64: 13.1 and 16.7 against 18.3 and 18.4 us; 1 over 6000, 32 and 64: 19.4 and 26.1 against 21.9 and 22.2; 4 over 1500, 32 and 48: 20.2
-// and 24.5 against 21.0; 16 over 300, 32: 22.1 against 20.7; 4 over 300, 128: 22.4 against 18.1.
-// At head_dim 64 twice as many tiles are as long.
-bool few_tiles(const nq_attention* a, const nq_pool* pool, int group) {
-    const int64_t longest = int64_t(std::min(a->max_q, a->tokens)) * group;
-    const int64_t row_tiles = (longest + kSmallRows - 1) / kSmallRows;
-    const int64_t key_tiles = (int64_t(a->table_cols) * pool->page_size + kKeyTile - 1) / kKeyTile * pool->kv_heads;
-    return row_tiles <= 4 && double(row_tiles) * key_tiles * a->requests * pool->head_dim <= 6.0 * 128 * kAttnGrid;
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     static std::once_flag once;
@@ -339,7 +326,7 @@ int attention(const nq_attention* a, const int64_t* ancestors, const int32_t* po
     x.tree_words = words;
     x.scale = a->scale;
     x.stream = static_cast<cudaStream_t>(stream);
-    if (few_rows(a, x.group, x.head_dim) || (ancestors && few_tiles(a, pool, x.group))) return launch_attention_small(x);
+    if (few_rows(a, x.group, x.head_dim) || (ancestors && few_tree_tiles(a, pool, x.group))) return launch_attention_small(x);
     if (may_mix(a, x.group)) {
         x.mixed = 1;
         const int small = launch_attention_small(x);

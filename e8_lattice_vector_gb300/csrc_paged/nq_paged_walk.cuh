@@ -2,6 +2,8 @@
 // block's share begins, and the walk through its pieces.  Plain arithmetic on the step's lengths, for the device and the host.
 #pragma once
 
+#include <algorithm>
+
 #include "nq_paged_device.cuh"
 
 namespace nq {
@@ -10,6 +12,24 @@ namespace nq {
 // key tiles plus these, or the block whose share is many short row tiles (the beginning of a prompt) would be the last
 // to end.  Not counted when a share has few tiles: there a block's idle time is worth more than an even cost.
 constexpr int kRowTileCost = 3, kCostFrom = 16;
+
+// Drafted trees of more rows than the small kernel's tile, where the whole call is short: the small kernel reads the keys once for each row
+// tile, but has two launches and no plan.  A block takes at most six key tiles of 128 x 128, a row tile as much as one and a half on top of
+// its own, by the lengths that the table has room for and the window leaves: the lengths themselves are on the device, so a table with room
+// for much more than a step's tokens sends it to the large kernel.
+// Requests over cached tokens, rows per KV head (32 heads on 8, head_dim 128, fp16), the small kernel against the large one.  Below the
+// limit: 1 over 1500, 32 and 64 rows, 12.6 and 16.2 against 17.2 and 17.9 us; 1 over 6000, 32: 18.7 against 21.7; 4 over 1500, 32: 19.9 against 20.4; 1
+// over 8000 with a window of 1024, 64: 14.9 against 16.3.  Above it: 1 over 6000, 64: 25.5 against 21.6; 4 over 1500, 48: 24.0 against 20.5; 16
+// over 300, 32: 21.5 against 20.1; 16 over 60, 64: 20.9 against 16.3.  Of 216 such calls (head_dim 64, 96 and 128, 1 to 32 requests over 60 to
+// 12000) the rule costs 0.7% on average and 19% at most; without the row tiles' part it is 2.3% and 41%.
+inline bool few_tree_tiles(const nq_attention* a, const nq_pool* pool, int group) {
+    const int64_t tokens = std::min(a->max_q, a->tokens);
+    const int64_t row_tiles = (tokens * group + kSmallRows - 1) / kSmallRows;
+    int64_t key_tiles = (int64_t(a->table_cols) * pool->page_size + kKeyTile - 1) / kKeyTile;
+    if (a->window > 0) key_tiles = std::min(key_tiles, (a->window + tokens + kKeyTile - 1) / kKeyTile + 1);
+    return row_tiles <= 4 &&
+           double(row_tiles) * (key_tiles + 1.5) * pool->kv_heads * a->requests * pool->head_dim <= 6.0 * 128 * kAttnGrid;
+}
 
 // Where a block's share begins: `unit` counts the row tile's cost, then its key tiles.
 struct ChunkStart {

@@ -213,3 +213,40 @@ def test_what_is_left_is_off_by_a_fraction_of_the_whole(apart):
         worst = max(worst, abs(got - S) / S)
         total = normal(f(float(got)), f(float(got - of(f(float(got))))))
     assert (worst > Fraction(1, 2 ** 38)) == (apart < 1e-2)
+
+
+@pytest.fixture(scope="module")
+def choice(tmp_path_factory):
+    import ctypes
+    import os
+    import subprocess
+
+    from e8_lattice_vector_gb300 import build as nqbuild
+
+    out = str(tmp_path_factory.mktemp("choice") / "paged_choice.so")
+    subprocess.run([nqbuild._nvcc()] + nqbuild.ARCH + ["-std=c++17", "-O1", "-Xcompiler", "-fPIC", "-shared", "-I", nqbuild.INCLUDE,
+                                                       os.path.join(os.path.dirname(os.path.abspath(__file__)), "paged_choice.cu"), "-o", out],
+                   check=True)
+    f = ctypes.CDLL(out).few_tree_tiles
+
+    def few(requests, ctx, rows, dim=128, window=0, room=None, group=4, kv_heads=8):
+        n = rows // group
+        room = ctx + n if room is None else room
+        return bool(f(requests * n, n, requests, group, kv_heads, dim, 16, -(-room // 16), window))
+
+    return few
+
+
+def test_short_trees_go_to_the_kernel_that_was_measured_as_faster(choice):
+    """The rule's comment: requests, cached tokens, rows for each KV head; some with a window, a table with room for more, other head_dims."""
+    small = [(1, 1500, 32), (1, 1500, 64), (1, 6000, 32), (4, 1500, 32), (1, 3000, 64), (4, 300, 32), (8, 300, 32)]
+    large = [(16, 300, 32), (16, 150, 64), (16, 60, 64), (1, 6000, 64), (4, 1500, 48), (4, 300, 128), (32, 150, 32), (32, 60, 48)]
+    assert [choice(*c) for c in small] == [True] * len(small)
+    assert [choice(*c) for c in large] == [False] * len(large)
+    # a window bounds the keys whatever the table has room for
+    for room in (8100, 100000, 2 ** 20):
+        assert choice(1, 8000, 64, window=1024, room=room) and choice(1, 8000, 32, window=4096, room=room)
+        assert not choice(4, 8000, 64, window=1024, room=room) and not choice(16, 8000, 32, window=256, room=room)
+    assert choice(16, 300, 32, dim=64) and choice(4, 8000, 32, dim=64, window=1024)
+    assert not choice(32, 150, 64, dim=64) and not choice(1, 8000, 32, room=2 ** 20)
+    assert not choice(2 ** 20, 2 ** 20, 64, room=2 ** 27) and choice(0, 10, 32)  # no sum of it wraps
