@@ -1,12 +1,12 @@
 """Calls on drafted trees that test_drafts_gpu leaves out: releases of columns without pages, verification of drafts that are all but
-the model's."""
+the model's and of wide stars that are rejected, trees that are plain runs, and repeated calls."""
 import random
 
 import pytest
 import torch
 
-from test_drafts_gpu import check_verify, make_tree
-from test_paged_gpu import DEV, _i32, nq  # noqa: F401  (nq is the fixture)
+from test_drafts_gpu import ROWS, TreeStep, check_verify, make_tree
+from test_paged_gpu import DEV, TYPES, _i32, nq  # noqa: F401  (nq is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -195,3 +195,93 @@ def test_verify_drafts_near_the_model(nq, V, apart):
         kept += check_verify(nq, [tree], V, torch.float32, True, probs=probs, draft=draft, ids=ids, u=u)
         tried += 1
     assert kept > tried  # some draft is accepted after a rejection
+
+
+@pytest.mark.parametrize("dtype", ROWS)
+@pytest.mark.parametrize("V", [50, 1003, 32000])
+@pytest.mark.parametrize("n", [66, 67, 301])
+def test_verify_wide_stars_that_are_rejected(nq, dtype, V, n):
+    """More chosen drafts than a warp keeps of its part, all rejected: over a few tokens, with repeated ones, at the row's beginning, among
+    its 16-byte pieces and at its end, rows that begin on any boundary."""
+    rng = random.Random(n * V)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(n + V)
+    for places in ((0, V), (0, min(V, 40)), (max(V - 40, 0), V), (V // 2 - 20, V // 2 + 20)):
+        some = [rng.randrange(*places) for _ in range(n if V > 1003 else 30)]
+        ids = [0] + [rng.choice(some) for _ in range(n - 1)]
+        probs = torch.rand(n, V, generator=g, device=DEV) + 0.1
+        probs[:, sorted(set(ids[1:]))] *= 1e-3  # little on the drafted tokens
+        probs = (probs / probs.sum(1, keepdim=True)).to(dtype)
+        for u0 in (0.0, 0.3, 0.9999) if V < 32000 else (0.6,):
+            u = torch.full((n,), 0.9999, device=DEV)
+            u[0] = u0
+            for stride in (None, V + 5):
+                kept = check_verify(nq, [make_tree("star", n)], V, dtype, False, probs=probs, draft=None, ids=_i32(ids), u=u, stride=stride)
+                assert kept == 1  # the root alone
+
+
+@pytest.mark.parametrize("V", [40, 2000])
+def test_verify_wide_stars_that_leave_nothing(nq, V):
+    """All mass on drafted tokens whose own numbers reject them: nothing is left, and the node's own probabilities decide."""
+    n = 300
+    rng = random.Random(V)
+    ids = [0] + [rng.randrange(30) for _ in range(n - 1)]
+    probs = torch.zeros(n, V, device=DEV)
+    probs[:, sorted(set(ids[1:]))] = 1.0 / 32
+    for u0 in (0.0, 0.5, 0.97):
+        u = torch.full((n,), 1.0, device=DEV)
+        u[0] = u0
+        assert check_verify(nq, [make_tree("star", n), [-1, 0]], V, torch.float32, False, probs=torch.cat([probs, probs[:2]]), draft=None,
+                            ids=_i32(ids + [0, 1]), u=torch.cat([u, u[:2]])) == 2
+
+
+def test_verify_repeats_bit_for_bit(nq):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    n, V = 12, 70001
+    probs = torch.softmax(torch.randn(20 * n, V, generator=g, device=DEV) * 2, 1)
+    draft = torch.softmax(torch.randn(20 * n, V, generator=g, device=DEV), 1) / 3 + probs * (2 / 3)
+    ids = torch.multinomial(draft, 1, generator=g).squeeze(1).to(torch.int32)
+    args = (probs, ids, _i32(make_tree("wide", n) * 20), _i32(list(range(0, 20 * n + 1, n))), torch.rand(20 * n, generator=g, device=DEV), draft)
+    want = nq.verify_drafts(*args)
+    for _ in range(5):
+        got = nq.verify_drafts(*args)
+        assert all(torch.equal(a, b) for a, b in ((got.accepted, want.accepted), (got.path, want.path), (got.tokens, want.tokens)))
+
+
+# ----------------------------------------------------------------- attention
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,D", [(3, 128), (14, 64), (40, 64), (40, 96), (40, 128), (100, 64), (100, 128)])
+def test_tree_attention_repeats_bit_for_bit(nq, n, D, dtype):
+    s = TreeStep([(5000, make_tree("wide", n)), (100, make_tree("random", n)), (2500, make_tree("chain", n))], 8, 2, D, 16, dtype, seed=n)
+    first = s.check(nq)
+    ws = nq.paged_attention_workspace(s.Q, s.Kp, s.table, max_q=s.max_q)
+    ws.fill_(255)  # NaN everywhere: nothing in the scratch has to start at zero
+    for _ in range(3):
+        assert torch.equal(first, s.call(nq, ws=ws))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("n", [1, 2, 4])
+def test_a_short_chain_is_a_causal_run_bit_for_bit(nq, n, D, dtype):
+    """Up to 16 rows for each KV head go to the small kernel with a tree and without: the same sums in the same order."""
+    s = TreeStep([(500, make_tree("chain", n)), (3000, make_tree("chain", n)), (0, make_tree("chain", n))], 8, 2, D, 16, dtype, seed=n)
+    plain = nq.paged_attention(s.Q, s.Kp, s.Vp, s.table, s.q_start, s.kv_lens, max_q=n)
+    assert torch.equal(s.call(nq), plain)
+
+
+@pytest.mark.parametrize("n", [4, 40])
+def test_the_rows_of_a_star_are_single_tokens(nq, n):
+    """Without a cached token a star's row sees its root and itself: the call over those two keys alone, within both bounds."""
+    s = TreeStep([(0, make_tree("star", n))], 8, 2, 128, 16, torch.float16, seed=n)
+    got, tol = s.check(nq), s.reference(128 ** -0.5)[2]
+    k, v = s.k[0], s.v[0]
+    for i in range(n):
+        Kp, Vp = (torch.zeros(1, 2, 16, 128, dtype=torch.float16, device=DEV) for _ in range(2))
+        for slot, j in enumerate((0, i) if i else (0,)):
+            Kp[0, :, slot], Vp[0, :, slot] = k[j], v[j]
+        one = nq.paged_attention(s.Q[i:i + 1], Kp, Vp, _i32([[0]]), _i32([0, 1]), _i32([2 if i else 1]))
+        assert bool(((one[0].double() - got[i].double()).abs() <= 2 * tol[i]).all())
