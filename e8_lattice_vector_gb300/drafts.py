@@ -10,7 +10,9 @@
     page_release(block_table, m.kv_lens, ctx_lens + v.accepted, page_size, free_pages, top)
 
 A request's rows are its tree's nodes, the root first and every node after its parent.  The root is the token that the last step
-ended with: certain, but not cached yet.  Nothing here waits for the GPU, and a step can be captured as a CUDA graph.
+ended with: certain, but not cached yet.  Nothing here waits for the GPU, and a step can be captured as a CUDA graph.  The graph
+holds for one `top`: page_map has the address of free_pages[top:] and page_release the number, while how far `top` moves is in their
+counts on the device.  Steps that follow each other are replayed from one graph only without these two, which are called around it.
 """
 from dataclasses import dataclass
 

@@ -8,7 +8,8 @@
 A pool is an fp16 or bf16 CUDA tensor [pages, kv_heads, page_size, head_dim] with any strides that are
 multiples of 8 elements and a contiguous last axis: pages that are stored token-major
 ([pages, page_size, kv_heads, head_dim]) are passed as .transpose(1, 2).  Lengths, tables and slots stay on the
-device: no call waits for the GPU, and a step can be captured as a CUDA graph.  All work is enqueued on the
+device: no call waits for the GPU, and a step can be captured as a CUDA graph (for one place in the free list, whose address page_map
+is given).  All work is enqueued on the
 current torch CUDA stream.
 """
 import ctypes
