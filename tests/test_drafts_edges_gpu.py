@@ -285,3 +285,73 @@ def test_the_rows_of_a_star_are_single_tokens(nq, n):
             Kp[0, :, slot], Vp[0, :, slot] = k[j], v[j]
         one = nq.paged_attention(s.Q[i:i + 1], Kp, Vp, _i32([[0]]), _i32([0, 1]), _i32([2 if i else 1]))
         assert bool(((one[0].double() - got[i].double()).abs() <= 2 * tol[i]).all())
+
+
+def test_steps_in_a_row_from_one_graph(nq):
+    """Everything of a step but the map and the release in one graph, these two around it with the free list's place as it moves: the
+    same tokens, lengths and kept rows as steps that are called one by one."""
+    R, n, P, H, D, V, L = 3, 9, 16, 2, 64, 200, 2
+    T, cols, pages = R * n, 10, 30
+    dev = torch.device(DEV)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(6)
+    q, k, v = (torch.zeros(L, T, h, D, dtype=torch.float16, device=dev) for h in (4, H, H))
+    probs, draft, u = torch.zeros(T, V, device=dev), torch.zeros(T, V, device=dev), torch.zeros(T, device=dev)
+    ids, parents = torch.zeros(T, dtype=torch.int32, device=dev), _i32(make_tree("wide", n) * R)
+
+    class Side:
+        def __init__(self):
+            self.pools = [torch.zeros(L, pages, H, P, D, dtype=torch.float16, device=dev) for _ in range(2)]
+            self.table = torch.full((R, cols), -1, dtype=torch.int32, device=dev)
+            self.free, self.top, self.lens = torch.arange(pages, dtype=torch.int32, device=dev), 0, [0] * R
+            self.m, self.out = nq.PageMap.empty(R, T, dev), torch.zeros_like(q)
+            self.tree, self.verdict = nq.DraftTree.empty(T, n, dev), nq.Verdict.empty(R, T, dev)
+
+        def map(self):
+            nq.page_map(_i32(self.lens), _i32([n] * R), self.free[self.top:], self.table, P, T, out=self.m)
+            self.top += int(self.m.counts[1])
+
+        def middle(self):
+            m = self.m
+            nq.draft_tree(parents, m.q_start, m.kv_lens, n, out=self.tree)
+            for l in range(L):
+                nq.paged_append(k[l], v[l], self.pools[0][l], self.pools[1][l], m.slots)
+                nq.paged_attention(q[l], self.pools[0][l], self.pools[1][l], self.table, m.q_start, m.kv_lens, max_q=n, tree=self.tree,
+                                   out=self.out[l])
+            nq.verify_drafts(probs, ids, parents, m.q_start, u, draft_probs=draft, out=self.verdict)
+            nq.paged_compact(*self.pools, self.table, m.q_start, m.kv_lens, self.verdict.path)
+
+        def release(self):
+            keep = [a + b for a, b in zip(self.lens, self.verdict.accepted.tolist())]
+            counts = nq.page_release(self.table, self.m.kv_lens, _i32(keep), P, self.free, self.top)
+            self.top -= int(counts[0] - counts[1])
+            self.lens = keep
+
+    one, other, warm = Side(), Side(), Side()
+    warm.map()
+    warm.middle()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.middle()
+    tops = set()
+    for step in range(12):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, generator=g, device=dev).half())
+        probs.copy_(torch.softmax(torch.randn(T, V, generator=g, device=dev) * 2, 1))
+        draft.copy_(torch.softmax(probs.log() + 0.3 * torch.randn(T, V, generator=g, device=dev), 1))
+        source = torch.tensor([r * n + max(p, 0) for r in range(R) for p in make_tree("wide", n)], device=dev)
+        ids.copy_(torch.multinomial(draft[source], 1, generator=g).squeeze(1))
+        u.copy_(torch.rand(T, generator=g, device=dev))
+        one.map()
+        one.middle()
+        one.release()
+        other.map()
+        graph.replay()
+        other.release()
+        tops.add(other.top)
+        assert one.lens == other.lens and one.top == other.top
+        assert torch.equal(one.out, other.out) and torch.equal(one.table, other.table) and torch.equal(one.free[one.top:], other.free[other.top:])
+        assert torch.equal(one.verdict.tokens, other.verdict.tokens) and torch.equal(one.verdict.path, other.verdict.path)
+        assert all(torch.equal(a, b) for a, b in zip(one.pools, other.pools))
+    assert len(tops) > 1
