@@ -1,6 +1,9 @@
 """Calls on drafted trees that test_drafts_gpu leaves out: releases of columns without pages, verification of drafts that are all but
 the model's and of wide stars that are rejected, trees that are plain runs, and repeated calls."""
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -355,3 +358,26 @@ def test_steps_in_a_row_from_one_graph(nq):
         assert torch.equal(one.verdict.tokens, other.verdict.tokens) and torch.equal(one.verdict.path, other.verdict.path)
         assert all(torch.equal(a, b) for a, b in zip(one.pools, other.pools))
     assert len(tops) > 1
+
+
+def test_a_first_call_may_be_a_captured_one():
+    """Release and verification of a new process, whose first calls (of the largest cluster, too) are made while a graph is captured."""
+    code = """
+import torch, e8_lattice_vector_gb300 as nq
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+R, cols = 600, 500
+table = torch.arange(R * cols, dtype=torch.int32, device="cuda").view(R, cols)
+lens, keep, free, counts = i32([16 * cols] * R), i32([0] * R), torch.full((R * cols,), -1, dtype=torch.int32, device="cuda"), i32([0, 0])
+probs, ids, parents, starts, u = torch.full((3, 9000), 1 / 9000, device="cuda"), i32([0, 5, 6]), i32([-1, 0, 1]), i32([0, 3]), torch.zeros(3, device="cuda")
+v = nq.Verdict.empty(1, 3)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    nq.page_release(table, lens, keep, 16, free, R * cols, out=counts)
+    nq.verify_drafts(probs, ids, parents, starts, u, out=v)
+assert counts.tolist() == [0, 0]
+graph.replay()
+torch.cuda.synchronize()
+assert counts.tolist() == [R * cols, 0] and torch.equal(free.flip(0), table.view(-1)) and v.tokens.tolist() == [5, 6, 0]
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
