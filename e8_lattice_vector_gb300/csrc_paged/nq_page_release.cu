@@ -5,8 +5,8 @@
 // lengths; a page's k also depends on the table, since columns that never got a page (the list had run out) give none back.  So one
 // cluster of blocks takes a call: each block forms the sums itself, 512 requests at a time, each warp reads an equal part of the columns
 // into shared memory and counts its pages, the blocks tell each other their counts, and then each warp knows its first page's k.
-// Measured (median of graph replays): 64 requests that give back a page or none 4.6 us, 512 that give back 129362 pages 8.5 us: the
-// launch, two chains of dependent loads, the scan's barriers, and 16 multiprocessors that read and write 32 columns in 30 cycles each.
+// Measured (median of graph replays): 64 requests that give back a page or none 4.6 to 4.9 us, 512 that give back 129362 pages 8.5 to
+// 8.8 us: the launch, two chains of dependent loads, the scan's barriers, and 16 multiprocessors that take 32 columns in 30 cycles each.
 // (Clusters of 8 blocks 4.5 and 14.4, blocks of 256 threads 4.2 and 16.1, of 1024 6.4 and 9.8; columns loaded into registers by an unrolled
 // loop 6.1 and 9.3, the code being fetched anew for every call.  As many blocks as fit, none of which knows of columns without pages
 // elsewhere, took 2.6 and 4.7.)

@@ -338,7 +338,7 @@ struct ChunkControl {
 // Buffers of scores in tensor memory.  Two, one for each half, beside a half's results at head_dim 128; at 64 there is room for a third,
 // and with three that go round between the halves a half's next scores are there while its exponentials are taken.  64 nodes of 4 heads
 // (256 rows) over 8000 cached, 32 requests: 225 -> 202 us in bf16, 169 -> 159 in fp16; a tile's exponentials (2260 of 3260 cycles, 1700 of
-// 2430 in fp16) are what it waits for then.
+// 2430 in fp16) are what it waits for then.  Measured for trees alone: calls without them keep two.
 template <int D, bool TREE>
 constexpr int kScoreBuffers = TREE && D == 64 ? 3 : 2;
 // The barrier of a half's n-th tile among s_full, p_full and o_full, and the parity of its phase.  With three buffers a half's next
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreadsChunk, 1)
                     // Trees mostly have up to 128 rows, and then a tile's time is its loads'.  Lanes that issue a box each take turns, at 110
                     // cycles a box; from one thread, the pages in its registers, 64 rows over 8000 cached in pages of 16 take (32
                     // requests) 188 us in place of 215 at head_dim 128 in bf16 and 152 in place of 192 at 96, in pages of 32 and more the
-                    // same within 2%.  With one box a page (head_dim 64) larger pages would be 9% slower.
+                    // same within 2%.  Measured for trees alone, calls without them keep the lanes.  With one box a page (head_dim 64) larger pages would be 9% slower.
                     int pages[ONE_ISSUES ? kMostPages : 1];
                     if constexpr (ONE_ISSUES)
 #pragma unroll

@@ -18,10 +18,14 @@
 // than the threads' totals and the search they took four fifths of the time), so a number that matters is the sum of two fp32: an
 // addition's rounding error is found by Knuth's two-sum, a product's by a fused multiply-add.
 //
-// Measured (median of graph replays): one request, a chain of 5 drafts, 32000 tokens in bf16 9.3 us: the launch, 1.7 us of loads for the
+// Measured (median of graph replays): one request, a chain of 5 drafts, 32000 tokens in bf16 9.1 us: the launch, 1.7 us of loads for the
 // walk (three after one another), 0.6 us for each barrier, 1.3 us of sum, 3 us of search, all latency; every further sum 2.6 us, of
 // 128256 tokens in fp32 4.8 us.  64 requests, 128256 tokens in fp32: 18.6 us with one sum (3.5 TB/s of p and q), 12 us for a further one
-// of all (5.5 TB/s, the rows come from the L2 in part); sampled trees of 16 36 us, 3.6 sums on average.  256 chains of 3 drafts 63 us.
+// of all (5.5 TB/s, the rows come from the L2 in part); sampled trees of 16 35 us, 3 to 3.6 sums on average.  256 chains of 3 drafts 63 us.
+// Chosen drafts, 256 requests, 32000 tokens in fp32 18 us.
+// At the ends of the range (one request, 32000 tokens in fp32, calls timed by events): a chain of 256 accepted drafts 68 us, of 4096 0.79 ms;
+// a star of 256 chosen drafts that are all rejected 0.14 ms, of 1024 0.76 ms, of 4096 8.6 ms, since each draft is held against all earlier
+// ones for a repeated token, and past 64 rejected tokens in a warp's part every vector is held against all of them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
