@@ -276,6 +276,16 @@ def test_a_short_chain_is_a_causal_run_bit_for_bit(nq, n, D, dtype):
     assert torch.equal(s.call(nq), plain)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("n", [33, 130])
+def test_a_long_chain_is_a_causal_run_bit_for_bit(nq, n, D, dtype):
+    """In the large kernel, too: rows of one half and of two, and at head_dim 64 three score buffers against two."""
+    s = TreeStep([(500, make_tree("chain", n)), (3000, make_tree("chain", n)), (0, make_tree("chain", n))], 8, 2, D, 16, dtype, seed=n)
+    plain = nq.paged_attention(s.Q, s.Kp, s.Vp, s.table, s.q_start, s.kv_lens, max_q=n)
+    assert torch.equal(s.call(nq), plain)
+
+
 @pytest.mark.parametrize("n", [4, 40])
 def test_the_rows_of_a_star_are_single_tokens(nq, n):
     """Without a cached token a star's row sees its root and itself: the call over those two keys alone, within both bounds."""
